@@ -15,15 +15,17 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libsq.so")
-SOURCES = ["api.cu", "codebook.cpp"]
+SOURCES = ["api.cu", "kv4.cu", "codebook.cpp"]
 HEADERS = ["sq_common.cuh", "sm100.cuh", "calibrate.cuh", "codec.cuh", "blk_compress.cuh", "attention.cuh",
-           "tc_compress.cuh", "fast_attn.cuh", "tc_decode.cuh", "decode_step.cuh"]
+           "tc_compress.cuh", "fast_attn.cuh", "tc_decode.cuh", "decode_step.cuh", "kv4.cuh", "kv4_append.cuh",
+           "kv4_attn.cuh"]
 
 NVCC_FLAGS = [
     "-std=c++17", "-O3", "-lineinfo",
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-Xcompiler", "-fPIC", "-shared",
     "-diag-suppress", "550",
+    "--threads", "0",
 ]
 
 

@@ -51,11 +51,15 @@ bool valid_dtype(int t) { return t == SQ_F32 || t == SQ_F16 || t == SQ_BF16; }
 
 // The name of the last CUDA error a call of this thread ran into (for sq_last_error).
 thread_local char g_last_err[160] = "none";
+}  // namespace
+
 sq_status cuda_ok(cudaError_t e) {
   if (e == cudaSuccess) return SQ_OK;
   snprintf(g_last_err, sizeof(g_last_err), "%s: %s", cudaGetErrorName(e), cudaGetErrorString(e));
   return SQ_ERR_CUDA;
 }
+
+namespace {
 
 // Cell tables of the tensor-core compress for widths 4..8 (see tc_compress.cuh)
 // from the float32 positive thresholds T_1 < ... < T_n of each width; false if

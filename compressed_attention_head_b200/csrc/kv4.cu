@@ -1,0 +1,249 @@
+// Host entry points of the paged 4-bit cache: argument checks and launches.
+// The contract (arguments, layout, errors) is in include/sq.h.
+#include <algorithm>
+#include <cmath>
+
+#include "sq_common.cuh"
+
+#include "kv4_append.cuh"
+#include "kv4_attn.cuh"
+
+namespace sq {
+namespace kv4 {
+namespace {
+
+bool aligned(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+bool head_dim_ok(int d) { return d == 64 || d == 128 || d == 256; }
+bool page_ok(int t) { return t >= 16 && t <= 1024 && (t & (t - 1)) == 0; }
+bool strides_ok(int64_t tok, int64_t head) { return tok >= 0 && head >= 0 && tok % 8 == 0 && head % 8 == 0; }
+
+bool cache_ok(const sq_kv4_cache* c) {
+  return c->pages && aligned(c->pages, 16) && c->table && aligned(c->table, 4) && c->n_pages >= 1 &&
+         c->n_pages <= 0x7fffffff && c->batch >= 1 && c->pages_per_row >= 1 && c->table_stride >= c->pages_per_row &&
+         c->n_kv_heads >= 1 && c->n_kv_heads <= 65535 && page_ok(c->page_tokens) &&
+         (int64_t)c->pages_per_row * c->page_tokens <= 0x7fffffff;
+}
+
+bool rope_ok(const sq_rope* r, int d) {
+  return !r || (r->table && aligned(r->table, 16) && r->n_pos >= 1 && r->rot_dim >= 16 && r->rot_dim % 16 == 0 &&
+                r->rot_dim <= d);
+}
+
+Pool pool_of(const sq_kv4_cache* c) {
+  Pool p;
+  p.pages = c->pages;
+  p.table = c->table;
+  p.n_pages = c->n_pages;
+  p.table_stride = c->table_stride;
+  p.batch = c->batch;
+  p.per_row = c->pages_per_row;
+  p.n_kv = c->n_kv_heads;
+  p.d = c->d;
+  p.page_shift = 0;
+  while ((1 << p.page_shift) < c->page_tokens) ++p.page_shift;
+  return p;
+}
+
+RopeArgs rope_of(const sq_rope* r) {
+  if (!r) return RopeArgs{nullptr, 0, 0, 0};
+  return RopeArgs{r->table, r->n_pos, r->rot_dim, r->interleaved != 0};
+}
+
+// ---------------------------------------------------------------- append, read
+sq_status stream_args_ok(const sq_kv4_cache* c, const void* k, const void* v, sq_dtype dtype, const StreamArgs& a) {
+  if (!c) return SQ_ERR_ARG;
+  if (!head_dim_ok(c->d) || (dtype != SQ_F32 && dtype != SQ_F16 && dtype != SQ_BF16)) return SQ_ERR_UNSUPPORTED;
+  if (!cache_ok(c) || a.n_tok < 0 || a.n_tok > 0x7fffffff || !a.start || !aligned(a.start, 4) || !aligned(a.cu, 4) ||
+      !aligned(a.flags, 4) || !strides_ok(a.ks_tok, a.ks_head) || !strides_ok(a.vs_tok, a.vs_head))
+    return SQ_ERR_ARG;
+  if (a.n_tok > 0 && (!k || !v || !aligned(k, 16) || !aligned(v, 16))) return SQ_ERR_ARG;
+  const int64_t vecs = a.n_tok * 2 * c->n_kv_heads;
+  if (vecs / (kStreamThreads / (c->d / 8)) >= 0x7fffffff) return SQ_ERR_ARG;
+  return SQ_OK;
+}
+
+template <typename T, int D>
+void launch_append(const Pool& c, const RopeArgs& r, const void* k, const void* v, const StreamArgs& a, cudaStream_t st) {
+  constexpr int VPB = kStreamThreads / (D / 8);
+  const int64_t vecs = a.n_tok * 2 * c.n_kv;
+  const int64_t blocks = (vecs + VPB - 1) / VPB;
+  if (blocks > 4 * 148 * 8)
+    k_append4<T, D, 2><<<(unsigned)((vecs + 2 * VPB - 1) / (2 * VPB)), kStreamThreads, 0, st>>>(c, r, (const T*)k, (const T*)v, a);
+  else
+    k_append4<T, D, 1><<<(unsigned)blocks, kStreamThreads, 0, st>>>(c, r, (const T*)k, (const T*)v, a);
+}
+
+template <typename T, int D>
+void launch_read(const Pool& c, void* k, void* v, const StreamArgs& a, cudaStream_t st) {
+  constexpr int VPB = kStreamThreads / (D / 8);
+  const int64_t vecs = a.n_tok * 2 * c.n_kv;
+  k_read4<T, D><<<(unsigned)((vecs + VPB - 1) / VPB), kStreamThreads, 0, st>>>(c, (T*)k, (T*)v, a);
+}
+
+#define SQ_KV4_D(T, CALL)                \
+  switch (c.d) {                         \
+    case 64: CALL(T, 64); break;         \
+    case 128: CALL(T, 128); break;       \
+    default: CALL(T, 256); break;        \
+  }
+#define SQ_KV4_TD(CALL)                              \
+  if (dtype == SQ_F32) { SQ_KV4_D(float, CALL) }     \
+  else if (dtype == SQ_F16) { SQ_KV4_D(__half, CALL) } \
+  else { SQ_KV4_D(__nv_bfloat16, CALL) }
+
+sq_status run_append(const Pool& c, const RopeArgs& r, const void* k, const void* v, sq_dtype dtype,
+                     const StreamArgs& a, cudaStream_t st) {
+#define SQ_CALL(T, DD) launch_append<T, DD>(c, r, k, v, a, st)
+  SQ_KV4_TD(SQ_CALL)
+#undef SQ_CALL
+  return cuda_ok(cudaGetLastError());
+}
+
+sq_status run_read(const Pool& c, void* k, void* v, sq_dtype dtype, const StreamArgs& a, cudaStream_t st) {
+#define SQ_CALL(T, DD) launch_read<T, DD>(c, k, v, a, st)
+  SQ_KV4_TD(SQ_CALL)
+#undef SQ_CALL
+  return cuda_ok(cudaGetLastError());
+}
+
+// ---------------------------------------------------------------- attention
+sq_status attn_args_ok(const sq_kv4_cache* c, int n_q, const void* q, sq_dtype dtype, int64_t s_tok, int64_t s_head,
+                       const sq_rope* rope, int window, const void* out, sq_dtype out_dtype, const float* lse,
+                       const void* ws, const uint32_t* flags) {
+  if (!c) return SQ_ERR_ARG;
+  if (!head_dim_ok(c->d) || (dtype != SQ_F16 && dtype != SQ_BF16) ||
+      (out_dtype != SQ_F32 && out_dtype != SQ_F16 && out_dtype != SQ_BF16))
+    return SQ_ERR_UNSUPPORTED;
+  if (!cache_ok(c) || n_q < 1 || n_q > 65535 || n_q % c->n_kv_heads != 0 || !q || !aligned(q, 16) ||
+      !strides_ok(s_tok, s_head) || !rope_ok(rope, c->d) || window < 0 || !out || !aligned(out, 16) ||
+      !aligned(lse, 4) || !ws || !aligned(ws, 16) || !aligned(flags, 4))
+    return SQ_ERR_ARG;
+  return SQ_OK;
+}
+
+template <typename T, typename TO, int D>
+void launch_plain(const Pool& c, const RopeArgs& r, const void* q, void* out, const AttnArgs& a, cudaStream_t st) {
+  k_attn4_plain<T, TO, D><<<dim3((unsigned)a.n_tok, a.n_q), kPlainTile, 0, st>>>(c, r, (const T*)q, (TO*)out, a);
+}
+
+sq_status run_attn(const Pool& c, const RopeArgs& r, const void* q, sq_dtype dtype, void* out, sq_dtype out_dtype,
+                   const AttnArgs& a, cudaStream_t st) {
+#define SQ_CALL(T, DD)                                                                          \
+  if (out_dtype == SQ_F32) launch_plain<T, float, DD>(c, r, q, out, a, st);                     \
+  else if (out_dtype == SQ_F16) launch_plain<T, __half, DD>(c, r, q, out, a, st);               \
+  else launch_plain<T, __nv_bfloat16, DD>(c, r, q, out, a, st)
+  if (dtype == SQ_F16) { SQ_KV4_D(__half, SQ_CALL) }
+  else { SQ_KV4_D(__nv_bfloat16, SQ_CALL) }
+#undef SQ_CALL
+  return cuda_ok(cudaGetLastError());
+}
+
+float scale_of(float scale, int d) { return scale > 0.0f ? scale : 1.0f / sqrtf((float)d); }
+
+}  // namespace
+}  // namespace kv4
+}  // namespace sq
+
+using namespace sq;
+using namespace sq::kv4;
+
+extern "C" {
+
+size_t sq_kv4_page_bytes(int n_kv_heads, int d, int page_tokens) {
+  if (n_kv_heads < 1 || n_kv_heads > 65535 || !head_dim_ok(d) || !page_ok(page_tokens)) return 0;
+  return (size_t)n_kv_heads * (page_tokens / 16) * blk_bytes(d);
+}
+
+sq_status sq_kv4_append(const sq_kv4_cache* cache, const void* k, const void* v, sq_dtype dtype, int64_t k_stride_tok,
+                        int64_t k_stride_head, int64_t v_stride_tok, int64_t v_stride_head, int64_t n_tok,
+                        const int32_t* d_cu, const int32_t* d_start, const sq_rope* rope, uint32_t* d_flags,
+                        sq_stream stream) {
+  const StreamArgs a{d_cu, d_start, n_tok, k_stride_tok, k_stride_head, v_stride_tok, v_stride_head, d_flags};
+  sq_status s = stream_args_ok(cache, k, v, dtype, a);
+  if (s != SQ_OK) return s;
+  if (!rope_ok(rope, cache->d)) return SQ_ERR_ARG;
+  if (n_tok == 0) return SQ_OK;
+  return run_append(pool_of(cache), rope_of(rope), k, v, dtype, a, (cudaStream_t)stream);
+}
+
+sq_status sq_kv4_read(const sq_kv4_cache* cache, void* k_out, void* v_out, sq_dtype dtype, int64_t k_stride_tok,
+                      int64_t k_stride_head, int64_t v_stride_tok, int64_t v_stride_head, int64_t n_tok,
+                      const int32_t* d_cu, const int32_t* d_start, uint32_t* d_flags, sq_stream stream) {
+  const StreamArgs a{d_cu, d_start, n_tok, k_stride_tok, k_stride_head, v_stride_tok, v_stride_head, d_flags};
+  sq_status s = stream_args_ok(cache, k_out, v_out, dtype, a);
+  if (s != SQ_OK) return s;
+  if (n_tok == 0) return SQ_OK;
+  return run_read(pool_of(cache), k_out, v_out, dtype, a, (cudaStream_t)stream);
+}
+
+size_t sq_kv4_attn_workspace(int batch, int n_q_heads, int n_kv_heads, int d, int64_t max_ctx) {
+  if (batch < 1 || n_q_heads < 1 || n_kv_heads < 1 || n_q_heads % n_kv_heads != 0 || !head_dim_ok(d) || max_ctx < 1)
+    return 0;
+  return 256;
+}
+
+sq_status sq_kv4_attn_decode(const sq_kv4_cache* cache, const int32_t* d_seq_lens, int n_q_heads, int64_t max_ctx,
+                             const void* q, sq_dtype dtype, int64_t q_stride_row, int64_t q_stride_head,
+                             const sq_rope* rope, float scale, int window, void* out, sq_dtype out_dtype,
+                             float* lse_out, void* ws, size_t ws_bytes, uint32_t* d_flags, sq_stream stream) {
+  sq_status s = attn_args_ok(cache, n_q_heads, q, dtype, q_stride_row, q_stride_head, rope, window, out, out_dtype,
+                             lse_out, ws, d_flags);
+  if (s != SQ_OK) return s;
+  if (!d_seq_lens || !aligned(d_seq_lens, 4) || max_ctx < 1) return SQ_ERR_ARG;
+  if (ws_bytes < sq_kv4_attn_workspace(cache->batch, n_q_heads, cache->n_kv_heads, cache->d, max_ctx))
+    return SQ_ERR_WORKSPACE;
+  AttnArgs a{nullptr, d_seq_lens, -1, cache->batch, max_ctx, q_stride_row, q_stride_head, n_q_heads,
+             n_q_heads / cache->n_kv_heads, window, scale_of(scale, cache->d), lse_out, d_flags};
+  return run_attn(pool_of(cache), rope_of(rope), q, dtype, out, out_dtype, a, (cudaStream_t)stream);
+}
+
+sq_status sq_kv4_decode_step(const sq_kv4_cache* cache, const void* k, const void* v, const void* q, sq_dtype dtype,
+                             int64_t k_stride_tok, int64_t k_stride_head, int64_t v_stride_tok, int64_t v_stride_head,
+                             int64_t q_stride_row, int64_t q_stride_head, const int32_t* d_pos, int n_q_heads,
+                             int64_t max_ctx, const sq_rope* rope, float scale, int window, void* out,
+                             sq_dtype out_dtype, float* lse_out, void* ws, size_t ws_bytes, uint32_t* d_flags,
+                             sq_stream stream) {
+  sq_status s = attn_args_ok(cache, n_q_heads, q, dtype, q_stride_row, q_stride_head, rope, window, out, out_dtype,
+                             lse_out, ws, d_flags);
+  if (s != SQ_OK) return s;
+  const StreamArgs ap{nullptr, d_pos, cache->batch, k_stride_tok, k_stride_head, v_stride_tok, v_stride_head, d_flags};
+  s = stream_args_ok(cache, k, v, dtype, ap);
+  if (s != SQ_OK) return s;
+  if (max_ctx < 1) return SQ_ERR_ARG;
+  if (ws_bytes < sq_kv4_attn_workspace(cache->batch, n_q_heads, cache->n_kv_heads, cache->d, max_ctx))
+    return SQ_ERR_WORKSPACE;
+  const Pool c = pool_of(cache);
+  const RopeArgs r = rope_of(rope);
+  s = run_append(c, r, k, v, dtype, ap, (cudaStream_t)stream);
+  if (s != SQ_OK) return s;
+  AttnArgs a{nullptr, d_pos, 0, cache->batch, max_ctx, q_stride_row, q_stride_head, n_q_heads,
+             n_q_heads / cache->n_kv_heads, window, scale_of(scale, cache->d), lse_out, d_flags};
+  return run_attn(c, r, q, dtype, out, out_dtype, a, (cudaStream_t)stream);
+}
+
+size_t sq_kv4_attn_prefill_workspace(int batch, int n_q_heads, int n_kv_heads, int d, int64_t n_tok) {
+  if (batch < 1 || n_q_heads < 1 || n_kv_heads < 1 || n_q_heads % n_kv_heads != 0 || !head_dim_ok(d) || n_tok < 1 ||
+      n_tok > 0x7fffffff)
+    return 0;
+  return 256;
+}
+
+sq_status sq_kv4_attn_prefill(const sq_kv4_cache* cache, const int32_t* d_cu, const int32_t* d_start, int n_q_heads,
+                              int64_t n_tok, const void* q, sq_dtype dtype, int64_t q_stride_tok,
+                              int64_t q_stride_head, const sq_rope* rope, float scale, int window, void* out,
+                              sq_dtype out_dtype, float* lse_out, void* ws, size_t ws_bytes, uint32_t* d_flags,
+                              sq_stream stream) {
+  if (n_tok == 0 && cache && d_cu && d_start) return SQ_OK;
+  sq_status s = attn_args_ok(cache, n_q_heads, q, dtype, q_stride_tok, q_stride_head, rope, window, out, out_dtype,
+                             lse_out, ws, d_flags);
+  if (s != SQ_OK) return s;
+  if (!d_cu || !aligned(d_cu, 4) || !d_start || !aligned(d_start, 4) || n_tok < 1 || n_tok > 0x7fffffff)
+    return SQ_ERR_ARG;
+  if (ws_bytes < sq_kv4_attn_prefill_workspace(cache->batch, n_q_heads, cache->n_kv_heads, cache->d, n_tok))
+    return SQ_ERR_WORKSPACE;
+  AttnArgs a{d_cu, d_start, 0, n_tok, 0x7fffffff, q_stride_tok, q_stride_head, n_q_heads,
+             n_q_heads / cache->n_kv_heads, window, scale_of(scale, cache->d), lse_out, d_flags};
+  return run_attn(pool_of(cache), rope_of(rope), q, dtype, out, out_dtype, a, (cudaStream_t)stream);
+}
+
+}  // extern "C"

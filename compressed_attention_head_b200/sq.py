@@ -21,6 +21,7 @@ SQ_OK, SQ_ERR_ARG, SQ_ERR_UNSUPPORTED, SQ_ERR_CUDA = 0, 1, 2, 3
 SQ_ERR_NOT_CONVERGED, SQ_ERR_CAPACITY, SQ_ERR_WORKSPACE, SQ_ERR_RECORD = 4, 5, 6, 7
 SQ_F32, SQ_F16, SQ_BF16 = 0, 1, 2
 SQ_FLAG_CAPACITY, SQ_FLAG_RECORD, SQ_FLAG_SEQLEN, SQ_FLAG_TIMEOUT = 1, 2, 4, 0x80000000
+SQ_FLAG_PAGE, SQ_FLAG_ROPE = 8, 16
 DTYPE_CODE = {torch.float32: SQ_F32, torch.float16: SQ_F16, torch.bfloat16: SQ_BF16}
 
 
@@ -45,8 +46,20 @@ class sq_cache(ctypes.Structure):
                 ("words", ctypes.c_int)]
 
 
+class sq_kv4_cache(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("table", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
+                ("table_stride", ctypes.c_int64), ("batch", ctypes.c_int), ("pages_per_row", ctypes.c_int),
+                ("n_kv_heads", ctypes.c_int), ("d", ctypes.c_int), ("page_tokens", ctypes.c_int)]
+
+
+class sq_rope(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("n_pos", ctypes.c_int64), ("rot_dim", ctypes.c_int),
+                ("interleaved", ctypes.c_int)]
+
+
 _lib = None
 _P = ctypes.c_void_p
+_I64 = ctypes.c_int64
 _SIGNATURES = {
     "sq_abi_version": (ctypes.c_int, []),
     "sq_status_str": (ctypes.c_char_p, [ctypes.c_int]),
@@ -89,6 +102,19 @@ _SIGNATURES = {
                                               ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                               ctypes.c_int64, _P, ctypes.c_int, ctypes.c_float, _P, ctypes.c_int,
                                               _P, _P, _P]),
+    "sq_kv4_page_bytes": (ctypes.c_size_t, [ctypes.c_int, ctypes.c_int, ctypes.c_int]),
+    "sq_kv4_append": (ctypes.c_int, [_P, _P, _P, ctypes.c_int, _I64, _I64, _I64, _I64, _I64, _P, _P, _P, _P, _P]),
+    "sq_kv4_read": (ctypes.c_int, [_P, _P, _P, ctypes.c_int, _I64, _I64, _I64, _I64, _I64, _P, _P, _P, _P]),
+    "sq_kv4_attn_workspace": (ctypes.c_size_t, [ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, _I64]),
+    "sq_kv4_attn_decode": (ctypes.c_int, [_P, _P, ctypes.c_int, _I64, _P, ctypes.c_int, _I64, _I64, _P, ctypes.c_float,
+                                          ctypes.c_int, _P, ctypes.c_int, _P, _P, ctypes.c_size_t, _P, _P]),
+    "sq_kv4_decode_step": (ctypes.c_int, [_P, _P, _P, _P, ctypes.c_int, _I64, _I64, _I64, _I64, _I64, _I64, _P,
+                                          ctypes.c_int, _I64, _P, ctypes.c_float, ctypes.c_int, _P, ctypes.c_int, _P,
+                                          _P, ctypes.c_size_t, _P, _P]),
+    "sq_kv4_attn_prefill_workspace": (ctypes.c_size_t, [ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, _I64]),
+    "sq_kv4_attn_prefill": (ctypes.c_int, [_P, _P, _P, ctypes.c_int, _I64, _P, ctypes.c_int, _I64, _I64, _P,
+                                           ctypes.c_float, ctypes.c_int, _P, ctypes.c_int, _P, _P, ctypes.c_size_t, _P,
+                                           _P]),
     "sq_wait_selftest": (ctypes.c_int, [ctypes.c_uint32, _P, _P]),
 }
 
@@ -333,3 +359,178 @@ def sq_wait_selftest(limit_us, flags, stream=None):
     microseconds with the library's bounded-wait helper, then sets
     SQ_FLAG_TIMEOUT in flags (see sq.h)."""
     _check(lib().sq_wait_selftest(int(limit_us), _ptr(flags), _stream(stream)), "sq_wait_selftest")
+
+
+# --------------------------------------------------------------------------- the paged 4-bit cache
+@dataclass
+class PagedKV4:
+    """Caller-owned pool of pages and the page table of a batch (see sq_kv4_cache in sq.h)."""
+
+    pages: torch.Tensor          # uint8 [n_pages, n_kv, page_tokens / 16, 16 d + 128]
+    table: torch.Tensor          # int32 [batch, pages_per_row]; the rows may be strided
+    n_kv: int
+    d: int
+    page_tokens: int
+
+    def __post_init__(self):
+        shape = (self.pages.shape[0], self.n_kv, self.page_tokens // 16, 16 * self.d + 128)
+        if self.pages.dtype != torch.uint8 or tuple(self.pages.shape) != shape or not self.pages.is_contiguous():
+            raise ValueError(f"pages: a contiguous uint8 tensor of shape {shape} is wanted")
+        if self.table.dtype != torch.int32 or self.table.dim() != 2 or (self.table.shape[1] > 1
+                                                                        and self.table.stride(1) != 1):
+            raise ValueError("table: an int32 tensor [batch, pages_per_row] with rows of stride 1 is wanted")
+
+    @property
+    def batch(self) -> int:
+        return self.table.shape[0]
+
+    def struct(self) -> sq_kv4_cache:
+        return sq_kv4_cache(self.pages.data_ptr(), self.table.data_ptr(), self.pages.shape[0],
+                            max(self.table.stride(0), self.table.shape[1]), self.table.shape[0], self.table.shape[1],
+                            self.n_kv, self.d, self.page_tokens)
+
+
+@dataclass
+class Rope:
+    """Rotation table float32 [n_pos, rot_dim]: cosines of rot_dim / 2 angles, then their sines."""
+
+    table: torch.Tensor
+    interleaved: bool = False
+
+    def __post_init__(self):
+        if self.table.dtype != torch.float32 or self.table.dim() != 2 or not self.table.is_contiguous():
+            raise ValueError("rotation table: a contiguous float32 tensor [n_pos, rot_dim] is wanted")
+
+    def struct(self) -> sq_rope:
+        return sq_rope(self.table.data_ptr(), self.table.shape[0], self.table.shape[1], int(self.interleaved))
+
+
+def rope_table(n_pos: int, rot_dim: int, theta: float = 10000.0, device="cuda") -> torch.Tensor:
+    """The rotation table of angles pos * theta^(-2i / rot_dim), formed in float64."""
+    i = torch.arange(0, rot_dim, 2, device=device, dtype=torch.float64)
+    ang = torch.arange(n_pos, device=device, dtype=torch.float64)[:, None] * theta ** (-i / rot_dim)
+    return torch.cat([torch.cos(ang), torch.sin(ang)], 1).float()
+
+
+def sq_kv4_page_bytes(n_kv, d, page_tokens) -> int:
+    return lib().sq_kv4_page_bytes(n_kv, d, page_tokens)
+
+
+def alloc_kv4(n_pages, n_kv, d, page_tokens, table, device="cuda") -> PagedKV4:
+    """A zeroed pool of n_pages pages behind the given page table."""
+    if sq_kv4_page_bytes(n_kv, d, page_tokens) == 0:
+        raise ValueError(f"unsupported paged cache: {n_kv} heads, head_dim {d}, {page_tokens} tokens a page")
+    return PagedKV4(torch.zeros(n_pages, n_kv, page_tokens // 16, 16 * d + 128, dtype=torch.uint8, device=device),
+                    table, n_kv, d, page_tokens)
+
+
+def _kv4_here(*tensors):
+    """The tensors of one call live on the current device: a kernel cannot read the others."""
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.get_device() != dev):
+            raise ValueError(f"every tensor must be on the current device (cuda:{dev}), got one on {t.device}")
+
+
+def _kv4_ints(name, t, n):
+    if t is not None and (t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous()):
+        raise ValueError(f"{name}: a contiguous int32 tensor of {n} elements is wanted")
+
+
+def _kv4_heads(name, t, heads, d, rows=None, dtype=None):
+    if (t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d or t.stride(2) != 1 or t.dtype not in DTYPE_CODE
+            or (rows is not None and t.shape[0] != rows) or (dtype is not None and t.dtype != dtype)):
+        raise ValueError(f"{name}: a tensor [{'tokens' if rows is None else rows}, {heads}, {d}] of stride 1 along the "
+                         f"last axis{'' if dtype is None else f' and type {dtype}'} is wanted")
+
+
+def _kv4_out(out, lse, q):
+    if tuple(out.shape) != tuple(q.shape) or not out.is_contiguous() or out.dtype not in DTYPE_CODE:
+        raise ValueError("out: a contiguous tensor of q's shape is wanted")
+    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != tuple(q.shape[:2])
+                            or not lse.is_contiguous()):
+        raise ValueError("lse: a contiguous float32 tensor [tokens, n_q_heads] is wanted")
+
+
+def _ref(s):
+    return None if s is None else ctypes.byref(s)
+
+
+def _nbytes(ws):
+    return ws.numel() * ws.element_size() if ws is not None else 0
+
+
+def sq_kv4_append(cache, k, v, start, cu=None, rope=None, flags=None, stream=None):
+    """Append k, v [tokens, n_kv, d] (any strides but the last axis's) at positions start[b] + i (see sq.h)."""
+    _kv4_here(cache.pages, cache.table, k, v, start, cu, flags, rope.table if rope else None)
+    _kv4_heads("k", k, cache.n_kv, cache.d)
+    _kv4_heads("v", v, cache.n_kv, cache.d, k.shape[0], k.dtype)
+    _kv4_ints("start", start, cache.batch)
+    _kv4_ints("cu", cu, cache.batch + 1)
+    _check(lib().sq_kv4_append(ctypes.byref(cache.struct()), _ptr(k), _ptr(v), DTYPE_CODE[k.dtype], k.stride(0),
+                               k.stride(1), v.stride(0), v.stride(1), k.shape[0], _ptr(cu), _ptr(start),
+                               _ref(rope.struct() if rope else None), _ptr(flags), _stream(stream)), "sq_kv4_append")
+
+
+def sq_kv4_read(cache, start, cu, k_out, v_out, flags=None, stream=None):
+    """The tokens at positions start[b] + i, as the cache holds them, into k_out, v_out [tokens, n_kv, d]."""
+    _kv4_here(cache.pages, cache.table, k_out, v_out, start, cu, flags)
+    _kv4_heads("k_out", k_out, cache.n_kv, cache.d)
+    _kv4_heads("v_out", v_out, cache.n_kv, cache.d, k_out.shape[0], k_out.dtype)
+    _kv4_ints("start", start, cache.batch)
+    _kv4_ints("cu", cu, cache.batch + 1)
+    _check(lib().sq_kv4_read(ctypes.byref(cache.struct()), _ptr(k_out), _ptr(v_out), DTYPE_CODE[k_out.dtype],
+                             k_out.stride(0), k_out.stride(1), v_out.stride(0), v_out.stride(1), k_out.shape[0],
+                             _ptr(cu), _ptr(start), _ptr(flags), _stream(stream)), "sq_kv4_read")
+
+
+def sq_kv4_attn_workspace(batch, n_q_heads, n_kv_heads, d, max_ctx) -> int:
+    return lib().sq_kv4_attn_workspace(batch, n_q_heads, n_kv_heads, d, max_ctx)
+
+
+def sq_kv4_attn_decode(cache, seq_lens, q, scale, out, max_ctx, ws, rope=None, window=0, lse=None, flags=None,
+                       stream=None):
+    """Attention of q [batch, n_q_heads, d] over the first seq_lens[b] tokens of every sequence (see sq.h)."""
+    _kv4_here(cache.pages, cache.table, q, out, seq_lens, lse, ws, flags, rope.table if rope else None)
+    _kv4_heads("q", q, q.shape[1] if q.dim() == 3 else 0, cache.d, cache.batch)
+    _kv4_out(out, lse, q)
+    _kv4_ints("seq_lens", seq_lens, cache.batch)
+    _check(lib().sq_kv4_attn_decode(ctypes.byref(cache.struct()), _ptr(seq_lens), q.shape[1], max_ctx, _ptr(q),
+                                    DTYPE_CODE[q.dtype], q.stride(0), q.stride(1),
+                                    _ref(rope.struct() if rope else None), float(scale), int(window), _ptr(out),
+                                    DTYPE_CODE[out.dtype], _ptr(lse), _ptr(ws), _nbytes(ws), _ptr(flags),
+                                    _stream(stream)), "sq_kv4_attn_decode")
+
+
+def sq_kv4_decode_step(cache, k, v, q, pos, scale, out, max_ctx, ws, rope=None, window=0, lse=None, flags=None,
+                       stream=None):
+    """Append one token a sequence at pos[b], then attend over pos[b] + 1 tokens (see sq.h)."""
+    _kv4_here(cache.pages, cache.table, k, v, q, out, pos, lse, ws, flags, rope.table if rope else None)
+    _kv4_heads("q", q, q.shape[1] if q.dim() == 3 else 0, cache.d, cache.batch)
+    _kv4_heads("k", k, cache.n_kv, cache.d, cache.batch, q.dtype)
+    _kv4_heads("v", v, cache.n_kv, cache.d, cache.batch, q.dtype)
+    _kv4_out(out, lse, q)
+    _kv4_ints("pos", pos, cache.batch)
+    _check(lib().sq_kv4_decode_step(ctypes.byref(cache.struct()), _ptr(k), _ptr(v), _ptr(q), DTYPE_CODE[q.dtype],
+                                    k.stride(0), k.stride(1), v.stride(0), v.stride(1), q.stride(0), q.stride(1),
+                                    _ptr(pos), q.shape[1], max_ctx, _ref(rope.struct() if rope else None),
+                                    float(scale), int(window), _ptr(out), DTYPE_CODE[out.dtype], _ptr(lse), _ptr(ws),
+                                    _nbytes(ws), _ptr(flags), _stream(stream)), "sq_kv4_decode_step")
+
+
+def sq_kv4_attn_prefill_workspace(batch, n_q_heads, n_kv_heads, d, n_tok) -> int:
+    return lib().sq_kv4_attn_prefill_workspace(batch, n_q_heads, n_kv_heads, d, n_tok)
+
+
+def sq_kv4_attn_prefill(cache, start, cu, q, scale, out, ws, rope=None, window=0, lse=None, flags=None, stream=None):
+    """Causal attention of q [tokens, n_q_heads, d], token cu[b] + i at position start[b] + i (see sq.h)."""
+    _kv4_here(cache.pages, cache.table, q, out, start, cu, lse, ws, flags, rope.table if rope else None)
+    _kv4_heads("q", q, q.shape[1] if q.dim() == 3 else 0, cache.d)
+    _kv4_out(out, lse, q)
+    _kv4_ints("start", start, cache.batch)
+    _kv4_ints("cu", cu, cache.batch + 1)
+    _check(lib().sq_kv4_attn_prefill(ctypes.byref(cache.struct()), _ptr(cu), _ptr(start), q.shape[1], q.shape[0],
+                                     _ptr(q), DTYPE_CODE[q.dtype], q.stride(0), q.stride(1),
+                                     _ref(rope.struct() if rope else None), float(scale), int(window), _ptr(out),
+                                     DTYPE_CODE[out.dtype], _ptr(lse), _ptr(ws), _nbytes(ws), _ptr(flags),
+                                     _stream(stream)), "sq_kv4_attn_prefill")

@@ -69,6 +69,8 @@ typedef enum { SQ_F32 = 0, SQ_F16 = 1, SQ_BF16 = 2 } sq_dtype;
 #define SQ_FLAG_CAPACITY 1u   /* start_pos + n_tok > cap (or start_pos < 0): row skipped */
 #define SQ_FLAG_RECORD 2u     /* record magic/version/d/words do not match the call      */
 #define SQ_FLAG_SEQLEN 4u     /* seq_len > max_ctx or > cap, or < 0: row clamped          */
+#define SQ_FLAG_PAGE 8u       /* paged cache: a page number outside the pool: its tokens skipped */
+#define SQ_FLAG_ROPE 16u      /* paged cache: a position past the rotation table: token skipped  */
 /* A pipeline wait of the tensor-core compress (an mbarrier phase that did not
  * complete within 2 s) gave up: the kernel stopped its remaining tiles, drained
  * the copies it had issued, freed its tensor memory and returned; the records
@@ -503,6 +505,148 @@ sq_status sq_attn_decode_noalloc(const void* calib_k, const void* calib_v, const
                                  int n_kv_heads, int d, int64_t max_ctx, const void* q, sq_dtype q_dtype,
                                  float scale, void* out, sq_dtype out_dtype, float* scores_out,
                                  uint32_t* d_flags, sq_stream stream);
+
+/*
+ * The paged 4-bit cache: keys and values of a serving batch in a pool of pages,
+ * four bits a coordinate, for callers whose sequences grow, end and share pages,
+ * and who have no calibration records. (The SpectralQuant sources describe no such
+ * cache; it counts 4 + 32 / d bits a coordinate.)
+ * Types: fp16 and bf16 (append and read also float); head_dim 64, 128 or 256.
+ *
+ *  pages        device bytes [n_pages][n_kv_heads][page_tokens / 16][16 d + 128],
+ *               16-byte aligned; sq_kv4_page_bytes() bytes a page.
+ *  table        device int32 [batch][table_stride]: entry p of a row is the page
+ *               of the sequence's positions p * page_tokens and up. Rows may share
+ *               pages. Entries past a sequence's end are not looked at.
+ *  pages_per_row  entries of a row that may be used (<= table_stride); a sequence
+ *               holds at most pages_per_row * page_tokens tokens.
+ *  page_tokens  16, 32, 64, ... 1024 (a power of two).
+ *
+ * A vector x (one head of one token) is held as codes c and a pair (s, m), and
+ * reads as m + s c: m = min(x) rounded down to bf16, s = (max(x) - m) / 15 (in
+ * float) rounded up to bf16 (at least the smallest normal float, 0 when max(x) =
+ * m), c = (x - m) / s rounded to nearest, ties to even. A vector with a value that
+ * is not finite reads as NaN throughout. Each block of 16 tokens of one head is
+ * 16 d + 128 bytes: 16 rows of key codes (d / 2 bytes each), 16 of value codes, 16
+ * key pairs, 16 value pairs. Byte j of a code row holds coordinate 2j in its low
+ * and 2j + 1 in its high half; the 16-byte chunk at place p of token t's row is
+ * chunk p ^ x(t), x(t) = (t * d / 256) mod (d / 32). A pair is a 32-bit word, s in
+ * the low half and m in the high one.
+ */
+typedef struct {
+  uint8_t* pages;
+  const int32_t* table;
+  int64_t n_pages;
+  int64_t table_stride;
+  int batch;
+  int pages_per_row;
+  int n_kv_heads;
+  int d;
+  int page_tokens;
+} sq_kv4_cache;
+
+/*
+ * Rotation of positions: device float [n_pos][rot_dim], 16-byte aligned; row p
+ * holds the cosines of position p's rot_dim / 2 angles, then their sines (times
+ * whatever factor the model's scaling puts on them). rot_dim: a multiple of 16, at
+ * most d; the first rot_dim coordinates of a head are rotated, as pairs (i, i +
+ * rot_dim / 2), or (2i, 2i + 1) when interleaved: y_a = a cos - b sin, y_b = b cos
+ * + a sin, every operation rounded to float, the result to the input's type.
+ */
+typedef struct {
+  const float* table;
+  int64_t n_pos;
+  int rot_dim;
+  int interleaved;
+} sq_rope;
+
+/* Bytes of one page (0 for an unsupported shape). */
+size_t sq_kv4_page_bytes(int n_kv_heads, int d, int page_tokens);
+
+/*
+ * Appends keys and values to their sequences' pages, rotating the keys on the way.
+ *  k, v         device, dtype; element i of head h of token t at k + t *
+ *               k_stride_tok + h * k_stride_head + i (views into a fused
+ *               projection need no copy). 16-byte aligned, strides multiples of 8.
+ *  n_tok        token rows of k and v.
+ *  d_cu         device int32[batch + 1], rising: tokens d_cu[b] .. d_cu[b + 1] - 1
+ *               belong to sequence b; rows from d_cu[batch] on (a padded batch) are
+ *               left alone. NULL: token b belongs to sequence b.
+ *  d_start      device int32[batch]: position of each sequence's first new token.
+ *  rope         NULL: no rotation. The values are never rotated.
+ *  d_flags      SQ_FLAG_CAPACITY (a position the row's pages do not reach, or a
+ *               negative one), SQ_FLAG_PAGE, SQ_FLAG_ROPE; such tokens are skipped.
+ * Two tokens of one call must not name the same place of the same page.
+ */
+sq_status sq_kv4_append(const sq_kv4_cache* cache, const void* k, const void* v, sq_dtype dtype, int64_t k_stride_tok,
+                        int64_t k_stride_head, int64_t v_stride_tok, int64_t v_stride_head, int64_t n_tok,
+                        const int32_t* d_cu, const int32_t* d_start, const sq_rope* rope, uint32_t* d_flags,
+                        sq_stream stream);
+
+/*
+ * Reads the tokens of a call back: the same addressing as sq_kv4_append (d_cu,
+ * d_start), keys as they are held (rotated). k_out, v_out are written at the given
+ * strides; rows of tokens that are skipped (see above) are left as they were.
+ */
+sq_status sq_kv4_read(const sq_kv4_cache* cache, void* k_out, void* v_out, sq_dtype dtype, int64_t k_stride_tok,
+                      int64_t k_stride_head, int64_t v_stride_tok, int64_t v_stride_head, int64_t n_tok,
+                      const int32_t* d_cu, const int32_t* d_start, uint32_t* d_flags, sq_stream stream);
+
+/* Workspace bytes of sq_kv4_attn_decode and sq_kv4_decode_step (0 if unsupported). */
+size_t sq_kv4_attn_workspace(int batch, int n_q_heads, int n_kv_heads, int d, int64_t max_ctx);
+
+/*
+ * Attention of one query a sequence over the paged cache: dense softmax attention
+ * over the vectors as sq_kv4_read gives them (unrounded), query head h reading KV
+ * head h / (n_q_heads / n_kv_heads).
+ *  d_seq_lens   device int32[batch]: tokens attended, the query's own among them:
+ *               the query sits at position d_seq_lens[b] - 1, which is also the
+ *               position that `rope` turns it by. 0: outputs are zeros.
+ *  max_ctx      host bound on the lengths (longer ones are cut, SQ_FLAG_SEQLEN).
+ *  q            device, dtype (SQ_F16 or SQ_BF16), strides as above, rounded to
+ *               dtype after the rotation.
+ *  scale        > 0, or <= 0 for 1 / sqrt(d).
+ *  window       0, or the number of last positions attended.
+ *  out          device, out_dtype (any) [batch][n_q_heads][d]; 16-byte aligned.
+ *  lse_out      device float [batch][n_q_heads] (may be NULL): natural logarithm of
+ *               the sum of exp(score); -inf where nothing was attended.
+ *  ws           16-byte aligned; needs no particular contents, and may be shared by
+ *               calls that do not overlap.
+ *  d_flags      SQ_FLAG_SEQLEN (also for a negative length, taken as 0),
+ *               SQ_FLAG_PAGE (the page's tokens are left out), SQ_FLAG_ROPE (the
+ *               row's outputs are zeros).
+ */
+sq_status sq_kv4_attn_decode(const sq_kv4_cache* cache, const int32_t* d_seq_lens, int n_q_heads, int64_t max_ctx,
+                             const void* q, sq_dtype dtype, int64_t q_stride_row, int64_t q_stride_head,
+                             const sq_rope* rope, float scale, int window, void* out, sq_dtype out_dtype,
+                             float* lse_out, void* ws, size_t ws_bytes, uint32_t* d_flags, sq_stream stream);
+
+/*
+ * One decode step: sq_kv4_append of one token a sequence at d_pos[b], then
+ * sq_kv4_attn_decode over d_pos[b] + 1 tokens.
+ */
+sq_status sq_kv4_decode_step(const sq_kv4_cache* cache, const void* k, const void* v, const void* q, sq_dtype dtype,
+                             int64_t k_stride_tok, int64_t k_stride_head, int64_t v_stride_tok, int64_t v_stride_head,
+                             int64_t q_stride_row, int64_t q_stride_head, const int32_t* d_pos, int n_q_heads,
+                             int64_t max_ctx, const sq_rope* rope, float scale, int window, void* out,
+                             sq_dtype out_dtype, float* lse_out, void* ws, size_t ws_bytes, uint32_t* d_flags,
+                             sq_stream stream);
+
+/* Workspace bytes of sq_kv4_attn_prefill (0 if unsupported). */
+size_t sq_kv4_attn_prefill_workspace(int batch, int n_q_heads, int n_kv_heads, int d, int64_t n_tok);
+
+/*
+ * Causal attention of ragged chunks of queries: query d_cu[b] + i sits at position
+ * d_start[b] + i of sequence b and attends to the positions up to its own (the
+ * chunk appended first), the last `window` of them when window > 0. Other arguments
+ * as above, out [n_tok][n_q_heads][d], lse_out [n_tok][n_q_heads]; output rows of
+ * tokens from d_cu[batch] on are left as they were.
+ */
+sq_status sq_kv4_attn_prefill(const sq_kv4_cache* cache, const int32_t* d_cu, const int32_t* d_start, int n_q_heads,
+                              int64_t n_tok, const void* q, sq_dtype dtype, int64_t q_stride_tok,
+                              int64_t q_stride_head, const sq_rope* rope, float scale, int window, void* out,
+                              sq_dtype out_dtype, float* lse_out, void* ws, size_t ws_bytes, uint32_t* d_flags,
+                              sq_stream stream);
 
 /*
  * Self-test of the bounded waits (no fault, no hang): one GPU thread waits on

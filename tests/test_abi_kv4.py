@@ -1,0 +1,145 @@
+"""Refusals of the paged 4-bit cache's entry points: they need no GPU."""
+
+import ctypes
+
+import pytest
+import torch
+
+from compressed_attention_head_b200 import build as sqbuild
+from compressed_attention_head_b200 import sq
+
+AT = 1 << 20      # an aligned address that nothing dereferences
+
+
+@pytest.fixture(scope="module")
+def L():
+    sqbuild.build()
+    return sq.lib()
+
+
+def _cache(**kw):
+    f = dict(pages=AT, table=AT, n_pages=8, table_stride=4, batch=2, pages_per_row=4, n_kv_heads=2, d=128,
+             page_tokens=16)
+    f.update(kw)
+    return sq.sq_kv4_cache(*[f[n] for n, _ in sq.sq_kv4_cache._fields_])
+
+
+def _rope(**kw):
+    f = dict(table=AT, n_pos=64, rot_dim=128, interleaved=0)
+    f.update(kw)
+    return sq.sq_rope(*[f[n] for n, _ in sq.sq_rope._fields_])
+
+
+def _stream_call(L, name, cache, k=AT, v=AT, dtype=sq.SQ_F16, strides=(256, 128, 256, 128), n=4, cu=None, start=AT,
+                 rope=None, flags=None):
+    args = [ctypes.byref(cache) if cache else None, k, v, dtype, *strides, n, cu, start]
+    if name == "sq_kv4_append":
+        args.append(ctypes.byref(rope) if rope else None)
+    return getattr(L, name)(*args, flags, None)
+
+
+BAD_CACHES = [dict(pages=0), dict(pages=AT + 8), dict(table=0), dict(table=AT + 2), dict(n_pages=0), dict(batch=0),
+              dict(pages_per_row=0), dict(table_stride=3), dict(n_kv_heads=0), dict(page_tokens=8),
+              dict(page_tokens=48), dict(page_tokens=2048), dict(pages_per_row=1 << 27, table_stride=1 << 27)]
+BAD_ROPES = [dict(table=0), dict(table=AT + 4), dict(n_pos=0), dict(rot_dim=8), dict(rot_dim=24), dict(rot_dim=144)]
+
+
+@pytest.mark.parametrize("name", ["sq_kv4_append", "sq_kv4_read"])
+def test_stream_refusals(L, name):
+    for bad in BAD_CACHES:
+        assert _stream_call(L, name, _cache(**bad)) == sq.SQ_ERR_ARG, bad
+    assert _stream_call(L, name, None) == sq.SQ_ERR_ARG
+    assert _stream_call(L, name, _cache(d=96)) == sq.SQ_ERR_UNSUPPORTED
+    assert _stream_call(L, name, _cache(), dtype=7) == sq.SQ_ERR_UNSUPPORTED
+    for kw in (dict(k=None), dict(v=None), dict(k=AT + 2), dict(v=AT + 8), dict(strides=(255, 128, 256, 128)),
+               dict(strides=(256, 4, 256, 128)), dict(strides=(-256, 128, 256, 128)), dict(n=-1), dict(start=None),
+               dict(start=AT + 1), dict(cu=AT + 2), dict(flags=AT + 1)):
+        assert _stream_call(L, name, _cache(), **kw) == sq.SQ_ERR_ARG, kw
+    assert _stream_call(L, name, _cache(), k=None, v=None, n=0) == sq.SQ_OK
+
+
+def test_append_rotation_refusals(L):
+    for bad in BAD_ROPES:
+        assert _stream_call(L, "sq_kv4_append", _cache(), rope=_rope(**bad)) == sq.SQ_ERR_ARG, bad
+    assert _stream_call(L, "sq_kv4_append", _cache(d=64), rope=_rope()) == sq.SQ_ERR_ARG     # 128 of 64 coordinates
+
+
+def _decode(L, cache, lens=AT, n_q=8, ctx=64, q=AT, dtype=sq.SQ_F16, strides=(1024, 128), rope=None, window=0, out=AT,
+            od=sq.SQ_F16, lse=None, ws=AT, nws=1 << 40, flags=None):
+    return L.sq_kv4_attn_decode(ctypes.byref(cache) if cache else None, lens, n_q, ctx, q, dtype, *strides,
+                                ctypes.byref(rope) if rope else None, 0.0, window, out, od, lse, ws, nws, flags, None)
+
+
+def _prefill(L, cache, cu=AT, start=AT, n_q=8, n=4, q=AT, dtype=sq.SQ_F16, strides=(1024, 128), rope=None, window=0,
+             out=AT, od=sq.SQ_F16, lse=None, ws=AT, nws=1 << 40, flags=None):
+    return L.sq_kv4_attn_prefill(ctypes.byref(cache) if cache else None, cu, start, n_q, n, q, dtype, *strides,
+                                 ctypes.byref(rope) if rope else None, 0.0, window, out, od, lse, ws, nws, flags, None)
+
+
+def _step(L, cache, k=AT, v=AT, q=AT, dtype=sq.SQ_F16, kv=(256, 128, 256, 128), strides=(1024, 128), pos=AT, n_q=8,
+          ctx=64, rope=None, window=0, out=AT, od=sq.SQ_F16, lse=None, ws=AT, nws=1 << 40, flags=None):
+    return L.sq_kv4_decode_step(ctypes.byref(cache) if cache else None, k, v, q, dtype, *kv, *strides, pos, n_q, ctx,
+                                ctypes.byref(rope) if rope else None, 0.0, window, out, od, lse, ws, nws, flags, None)
+
+
+COMMON = [dict(n_q=7), dict(n_q=0), dict(q=None), dict(q=AT + 2), dict(strides=(1020, 128)), dict(window=-1),
+          dict(out=None), dict(out=AT + 4), dict(lse=AT + 2), dict(ws=None), dict(ws=AT + 8), dict(flags=AT + 2)]
+
+
+@pytest.mark.parametrize("call", [_decode, _prefill, _step])
+def test_attention_refusals(L, call):
+    for bad in BAD_CACHES:
+        assert call(L, _cache(**bad)) == sq.SQ_ERR_ARG, bad
+    for bad in BAD_ROPES:
+        assert call(L, _cache(), rope=_rope(**bad)) == sq.SQ_ERR_ARG, bad
+    for kw in COMMON:
+        assert call(L, _cache(), **kw) == sq.SQ_ERR_ARG, kw
+    assert call(L, None) == sq.SQ_ERR_ARG
+    assert call(L, _cache(d=32)) == sq.SQ_ERR_UNSUPPORTED
+    assert call(L, _cache(), dtype=sq.SQ_F32) == sq.SQ_ERR_UNSUPPORTED
+    assert call(L, _cache(), od=9) == sq.SQ_ERR_UNSUPPORTED
+    assert call(L, _cache(), nws=0) == sq.SQ_ERR_WORKSPACE
+
+
+def test_own_refusals_of_each_call(L):
+    assert _decode(L, _cache(), lens=None) == sq.SQ_ERR_ARG
+    assert _decode(L, _cache(), lens=AT + 2) == sq.SQ_ERR_ARG
+    assert _decode(L, _cache(), ctx=0) == sq.SQ_ERR_ARG
+    assert _prefill(L, _cache(), cu=None) == sq.SQ_ERR_ARG
+    assert _prefill(L, _cache(), start=None) == sq.SQ_ERR_ARG
+    assert _prefill(L, _cache(), n=-1) == sq.SQ_ERR_ARG
+    assert _prefill(L, _cache(), n=0) == sq.SQ_OK
+    assert _step(L, _cache(), k=None) == sq.SQ_ERR_ARG
+    assert _step(L, _cache(), pos=None) == sq.SQ_ERR_ARG
+    assert _step(L, _cache(), kv=(252, 128, 256, 128)) == sq.SQ_ERR_ARG
+
+
+def test_sizes(L):
+    assert L.sq_kv4_page_bytes(2, 128, 32) == 2 * 2 * (16 * 128 + 128)
+    assert L.sq_kv4_page_bytes(8, 64, 16) == 8 * (16 * 64 + 128)
+    for bad in ((0, 128, 16), (2, 96, 16), (2, 128, 8), (2, 128, 24), (2, 128, 2048)):
+        assert L.sq_kv4_page_bytes(*bad) == 0
+    assert L.sq_kv4_attn_workspace(4, 8, 2, 128, 100) > 0 and L.sq_kv4_attn_prefill_workspace(4, 8, 2, 128, 100) > 0
+    for bad in ((0, 8, 2, 128, 100), (4, 7, 2, 128, 100), (4, 8, 2, 32, 100), (4, 8, 2, 128, 0)):
+        assert L.sq_kv4_attn_workspace(*bad) == 0 and L.sq_kv4_attn_prefill_workspace(*bad) == 0
+
+
+def test_binding_refuses_wrong_tensors():
+    table = torch.zeros(2, 4, dtype=torch.int32)
+    pages = torch.zeros(8, 2, 1, 16 * 128 + 128, dtype=torch.uint8)
+    c = sq.PagedKV4(pages, table, 2, 128, 16)
+    assert c.struct().table_stride == 4 and c.batch == 2
+    for bad in (dict(pages=pages.float()), dict(pages=pages[:, :1]), dict(table=table.long()), dict(table=table[0]),
+                dict(d=64), dict(page_tokens=32)):
+        with pytest.raises(ValueError):
+            sq.PagedKV4(**{**dict(pages=pages, table=table, n_kv=2, d=128, page_tokens=16), **bad})
+    with pytest.raises(ValueError):
+        sq.Rope(torch.zeros(4, 16, dtype=torch.float64))
+    k = torch.zeros(2, 2, 128, dtype=torch.float16)
+    start = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="current device"):            # host tensors never reach a kernel
+        sq.sq_kv4_append(c, k, k, start)
+    with pytest.raises(ValueError, match="current device"):
+        sq.sq_kv4_attn_decode(c, start, k, 0.0, k, 64, torch.zeros(1 << 10, dtype=torch.uint8))
+    with pytest.raises(ValueError):
+        sq.alloc_kv4(4, 2, 96, 16, table, device="cpu")

@@ -1,0 +1,528 @@
+"""The paged 4-bit cache on the GPU against its oracle (float64).
+
+What the cache holds is compared bit for bit: the rotation, the pair and the codes are defined operation
+by operation (include/sq.h). Attention is compared under a bound that is added up per output value, in
+units of the roundings that a kernel may make:
+
+* score: the codes and the query (rounded to its type) are exact factors of exact products; a float sum of d
+  of them, scaled, is off by at most delta = (d + 16) 2^-24 scale (s sum |q_i| c_i + |m| sum |q_i|), to which
+  base-2 exponentials add 2^-20 of relative error: an error eps = delta + 2^-20 in every exponent;
+* probabilities times value steps may be rounded to fp16 (half a step is 2^-11) against codes centred on 8:
+  2^-11 sum_t p_t s_t max(|c_t - 8|, 1/2), plus fp16's smallest steps, at most 2^-30 of the largest s;
+* both factors of the softmax (numerator, denominator): 2 eps sum_t p_t |x_t|;
+* the output's own rounding: finfo(type).eps / 2 relative.
+"""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import kv4
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+from compressed_attention_head_b200 import sq  # noqa: E402
+
+F16, BF16, F32 = torch.float16, torch.bfloat16, torch.float32
+
+
+def rounder(dtype):
+    return lambda y: torch.from_numpy(np.ascontiguousarray(y, dtype=np.float32)).to(dtype).float().numpy()
+
+
+def make_table(need, seed, spare=2, per_row=None, shared=()):
+    """(page table int32 [batch, per_row] with -1 past each sequence, pages in all)."""
+    total = sum(need) + spare
+    perm = np.random.default_rng(seed).permutation(total)
+    table = np.full((len(need), per_row or max(1, max(need))), -1, np.int32)
+    at = 0
+    for b, n in enumerate(need):
+        table[b, :n] = perm[at:at + n]
+        at += n
+    for b, src, p in shared:
+        table[b, p] = table[src, p]
+    return table, total
+
+
+def random_pool(n_pages, n_kv, page, d, seed, device="cuda"):
+    """A pool of random codes and pairs s in about 2^-4..2^0, m in about -8..8."""
+    g = torch.Generator(device="cpu").manual_seed(seed)
+    p = torch.randint(0, 256, (n_pages, n_kv, page // 16, 16 * d + 128), generator=g, dtype=torch.uint8)
+    shape = (n_pages, n_kv, page // 16, 32)
+    s = (torch.rand(shape, generator=g) * 0.9 + 0.07).to(BF16)
+    m = (torch.randn(shape, generator=g) * 0.5 - 7.5 * s.float()).to(BF16)
+    p[..., 16 * d:] = torch.stack([s, m], -1).contiguous().view(torch.uint8).reshape(*shape[:3], 128)
+    return p.to(device)
+
+
+def rows_of(pool_np, table, b, head, n, page, side):
+    got = [kv4.load(pool_np, table[b, t // page], head, t % page, side) for t in range(n)]
+    d = (pool_np.shape[-1] - 128) // 16
+    codes = np.stack([x[0] for x in got]) if n else np.zeros((0, d), np.uint8)
+    return codes, np.array([x[1] for x in got], np.uint32), np.array([x[2] for x in got], np.uint32)
+
+
+def check_attention(out, lse, q, pos, pool, table, page, n_q, n_kv, d, dtype, rope=None, inter=False, window=0,
+                    scale=None, skip=None):
+    """out [tokens, n_q, d], lse [tokens, n_q], q [tokens, n_q, d]; pos: list of (sequence, position) per token."""
+    scale = scale or 1.0 / math.sqrt(d)
+    pool_np, out, lse = pool.cpu().numpy(), out.double().cpu().numpy(), None if lse is None else lse.double().cpu().numpy()
+    step = torch.finfo(dtype).eps / 2
+    q = q.float().cpu().numpy()
+    cache = {}
+    worst = 0.0
+    for i, (b, p) in enumerate(pos):
+        if b < 0:
+            continue
+        qr = kv4.rotate(q[i], rope, max(p, 0), inter, rounder(Q_TYPE[0])).astype(np.float64)
+        lo = max(0, p - window + 1) if window else 0
+        for h in range(n_q):
+            g = h // (n_q // n_kv)
+            key = (b, g)
+            if key not in cache:
+                n = max([pp for bb, pp in pos if bb == b]) + 1
+                cache[key] = [rows_of(pool_np, table, b, g, n, page, side) for side in (0, 1)]
+            (kc, ks, km), (vc, vs, vm) = cache[key]
+            sel = np.arange(lo, p + 1) if p >= 0 else np.arange(0)
+            if skip is not None:
+                sel = sel[[t // page not in skip.get(b, ()) for t in sel]] if len(sel) else sel
+            keys, vals = kv4.values(kc[sel], ks[sel], km[sel]), kv4.values(vc[sel], vs[sel], vm[sel])
+            s64, m64, v64 = (kv4.bf16_value(x[sel]).astype(np.float64) for x in (ks, km, vs))
+            o, l, spread = kv4.attend(qr[h], keys, vals, scale, v64[:, None] * np.maximum(np.abs(vc[sel] - 8.0), 0.5))
+            if len(sel) == 0:
+                assert not out[i, h].any() and (lse is None or lse[i, h] == -math.inf)
+                continue
+            aq = np.abs(qr[h])
+            delta = float(((d + 16) * 2.0 ** -24 * scale * (s64 * (kc[sel] @ aq) + np.abs(m64) * aq.sum())).max())
+            eps = delta + 2.0 ** -20
+            _, _, size = kv4.attend(qr[h], keys, vals, scale, np.abs(vals))
+            bound = step * np.abs(o) + 2.0 ** -11 * spread + 2.0 ** -30 * v64.max() + 2 * eps * size + 1e-30
+            err = np.abs(out[i, h] - o)
+            worst = max(worst, float((err / bound).max()))
+            assert np.all(err <= bound), (i, b, p, h, float((err / bound).max()))
+            if lse is not None:
+                assert abs(lse[i, h] - l) <= eps + 2.0 ** -22 * abs(l) + 2.0 ** -22, (i, h, lse[i, h], l)
+    return worst
+
+
+Q_TYPE = [F16]
+
+
+# ------------------------------------------------------------------ append and read
+def append_oracle(pool_np, table, page, k, v, start, cu, rope, inter, dtype):
+    for b in range(len(start)):
+        lo, hi = (cu[b], cu[b + 1]) if cu is not None else (b, b + 1)
+        for i in range(lo, hi):
+            p = start[b] + i - lo
+            kr = kv4.rotate(k[i].float().numpy(), rope, p, inter, rounder(dtype))
+            for side, x in ((0, kr), (1, v[i].float().numpy())):
+                c, sb, mb = kv4.quantize(x)
+                for h in range(x.shape[0]):
+                    kv4.store(pool_np, table[b, p // page], h, p % page, side, c[h], sb[h], mb[h])
+
+
+@pytest.mark.parametrize("d,dtype,page,n_kv,rot,inter", [
+    (64, F16, 16, 1, 64, False), (64, BF16, 32, 3, 32, True), (128, F16, 16, 2, 128, False), (128, BF16, 64, 1, 64, False),
+    (128, F32, 16, 2, 128, True), (256, BF16, 16, 2, 256, False), (256, F16, 32, 1, 16, True), (256, F32, 128, 2, 0, False)])
+def test_append_writes_the_defined_bytes_and_nothing_else(d, dtype, page, n_kv, rot, inter):
+    start, cu = [5, 0, 40, 17], [0, 23, 23, 24, 61]               # an empty sequence, a single token, a padded tail
+    n_tok = 66
+    g = torch.Generator().manual_seed(d + page)
+    qkv = torch.randn(n_tok, 3 * n_kv * d + 8, generator=g) * torch.exp(torch.randn(n_tok, 1, generator=g))
+    qkv = qkv.to(dtype)
+    k, v = (qkv[:, i * n_kv * d:(i + 1) * n_kv * d].unflatten(1, (n_kv, d)) for i in (1, 2))
+    table, total = make_table([-(-(s + b - a) // page) for s, a, b in zip(start, cu, cu[1:])], 3)
+    pool = torch.randint(0, 256, (total, n_kv, page // 16, 16 * d + 128), generator=g, dtype=torch.uint8)
+    want = pool.numpy().copy()
+    rope = kv4.rope_table(64, rot) if rot else None
+    append_oracle(want, table, page, k, v, start, cu, rope, inter, dtype)
+    dev = qkv.cuda()
+    kd, vd = (dev[:, i * n_kv * d:(i + 1) * n_kv * d].unflatten(1, (n_kv, d)) for i in (1, 2))
+    cache = sq.PagedKV4(pool.cuda(), torch.from_numpy(table).cuda(), n_kv, d, page)
+    st, cud = torch.tensor(start, dtype=torch.int32).cuda(), torch.tensor(cu, dtype=torch.int32).cuda()
+    flags = torch.zeros(1, dtype=torch.int32, device="cuda")
+    sq.sq_kv4_append(cache, kd, vd, st, cud, rope=sq.Rope(torch.from_numpy(rope).cuda(), inter) if rot else None,
+                     flags=flags)
+    assert flags.item() == 0
+    assert np.array_equal(cache.pages.cpu().numpy(), want)
+    ko = torch.full((n_tok, n_kv, d), 7.0, device="cuda", dtype=dtype)
+    vo = torch.full((n_kv, n_tok, d), 7.0, device="cuda", dtype=dtype).transpose(0, 1)       # head-major rows
+    sq.sq_kv4_read(cache, st, cud, ko, vo, flags)
+    assert flags.item() == 0
+    for b in range(4):
+        for i in range(cu[b], cu[b + 1]):
+            p = start[b] + i - cu[b]
+            for side, got in ((0, ko), (1, vo)):
+                for h in range(n_kv):
+                    c, sb, mb = kv4.load(want, table[b, p // page], h, p % page, side)
+                    x = torch.from_numpy(kv4.values(c, np.uint32(sb), np.uint32(mb))).float().to(dtype)
+                    assert torch.equal(got[i, h].cpu(), x)
+    assert (ko[cu[-1]:] == 7).all() and (vo[cu[-1]:] == 7).all()
+
+
+def test_append_of_values_at_borders_and_not_finite():
+    d, page = 64, 16
+    g = torch.Generator().manual_seed(0)
+    rows = [torch.zeros(d), torch.full((d,), -3.3), torch.arange(d) * 0.5, torch.arange(d) % 16 + 0.5 * (torch.arange(d) % 2),
+            torch.randn(d, generator=g) * 1e-38, torch.randn(d, generator=g) * 1e38, 1000 + torch.randn(d, generator=g) * 1e-3,
+            torch.cat([torch.tensor([math.inf]), torch.ones(d - 1)]), torch.cat([torch.tensor([math.nan]), torch.ones(d - 1)]),
+            torch.cat([torch.tensor([-math.inf]), torch.ones(d - 1)]), torch.tensor([3.4e38, -3.4e38]).repeat(d // 2),
+            torch.tensor([1e-45, 0.0]).repeat(d // 2), -torch.rand(d, generator=g)]
+    x = torch.stack([r.float() for r in rows])[:, None]
+    n = len(rows)
+    for dtype in (F32, BF16, F16):
+        y = x.to(dtype)
+        table, total = make_table([1], 0)
+        cache = sq.alloc_kv4(total, 1, d, page, torch.from_numpy(table).cuda())
+        want = cache.pages.cpu().numpy().copy()
+        append_oracle(want, table, page, y, y, [0], [0, n], None, False, dtype)
+        sq.sq_kv4_append(cache, y.cuda(), y.cuda(), torch.zeros(1, dtype=torch.int32).cuda(),
+                         torch.tensor([0, n], dtype=torch.int32).cuda())
+        assert np.array_equal(cache.pages.cpu().numpy(), want), dtype
+
+
+def test_append_skips_and_flags_what_it_cannot_place():
+    d, page, n_kv = 128, 16, 1
+    k = torch.randn(6, n_kv, d, device="cuda", dtype=F16)
+    rope = sq.Rope(sq.rope_table(40, d))
+    table = torch.tensor([[0, 1], [7, 1], [-1, 2], [3, 3], [4, 5], [5, 4]], dtype=torch.int32, device="cuda")
+    start = torch.tensor([32, 3, 1, -1, 3, 2 ** 31 - 1], dtype=torch.int32, device="cuda")
+    want = {0: sq.SQ_FLAG_CAPACITY, 1: sq.SQ_FLAG_PAGE, 2: sq.SQ_FLAG_PAGE, 3: sq.SQ_FLAG_CAPACITY, 4: 0,
+            5: sq.SQ_FLAG_CAPACITY}
+    for row, bit in want.items():
+        cache = sq.alloc_kv4(6, n_kv, d, page, table[row:row + 1])
+        flags = torch.zeros(1, dtype=torch.int32, device="cuda")
+        sq.sq_kv4_append(cache, k[:1], k[:1], start[row:row + 1].clone(), rope=rope, flags=flags)
+        assert flags.item() == bit
+        assert bool(cache.pages.any()) == (bit == 0)
+    cache = sq.alloc_kv4(6, n_kv, d, page, torch.arange(4, dtype=torch.int32, device="cuda")[None])
+    flags = torch.zeros(1, dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, 6], dtype=torch.int32, device="cuda")
+    sq.sq_kv4_append(cache, k, k, torch.tensor([37], dtype=torch.int32, device="cuda"), cu, rope=rope, flags=flags)
+    assert flags.item() == sq.SQ_FLAG_ROPE                          # positions 40.. have no row in the table
+    ko, vo = torch.full_like(k, 9.0), torch.full_like(k, 9.0)
+    sq.sq_kv4_read(cache, torch.tensor([37], dtype=torch.int32, device="cuda"), cu, ko, vo)
+    assert not (vo[:3] == 9).all(-1).any() and not vo[3:].any()
+
+
+def test_pools_beyond_four_gigabytes():
+    d, page, n_kv = 128, 128, 8
+    n_pages = (1 << 32) // sq.sq_kv4_page_bytes(n_kv, d, page) + 40
+    pages = torch.empty(n_pages, n_kv, page // 16, 16 * d + 128, dtype=torch.uint8, device="cuda")
+    table = torch.tensor([[n_pages - 1, 3], [n_pages - 2, n_pages - 3]], dtype=torch.int32, device="cuda")
+    cache = sq.PagedKV4(pages, table, n_kv, d, page)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    k, v = (torch.randn(300, n_kv, d, generator=g, device="cuda").to(F16) for _ in range(2))
+    cu = torch.tensor([0, 150, 300], dtype=torch.int32, device="cuda")
+    start = torch.zeros(2, dtype=torch.int32, device="cuda")
+    sq.sq_kv4_append(cache, k, v, start, cu)
+    ko, vo = torch.empty_like(k), torch.empty_like(v)
+    sq.sq_kv4_read(cache, start, cu, ko, vo)
+    for x, y in ((k, ko), (v, vo)):
+        span = x.float().amax(-1) - x.float().amin(-1)
+        assert ((x.float() - y.float()).abs().amax(-1) <= span / 30 * 1.05 + 0.01).all()
+    lens = torch.tensor([150, 150], dtype=torch.int32, device="cuda")
+    q = torch.randn(2, n_kv, d, generator=g, device="cuda").to(F16)
+    out = torch.empty(2, n_kv, d, device="cuda")
+    ws = torch.empty(sq.sq_kv4_attn_workspace(2, n_kv, n_kv, d, 150), dtype=torch.uint8, device="cuda")
+    sq.sq_kv4_attn_decode(cache, lens, q, 0.0, out, 150, ws)
+    s = torch.einsum("bhd,bthd->bht", q.double(), ko.double().view(2, 150, n_kv, d)) / math.sqrt(d)
+    ref = torch.einsum("bht,bthd->bhd", s.softmax(-1), vo.double().view(2, 150, n_kv, d))
+    assert (out - ref).abs().max() < 5e-3
+
+
+# ------------------------------------------------------------------ attention of single tokens
+def decode_case(d, group, n_kv, dtype, out_dtype, page, lens, window=0, rot=0, inter=False, seed=0, max_ctx=None,
+                skip=None, poison=False, q_scale=1.0):
+    Q_TYPE[0] = dtype
+    batch = len(lens)
+    table, total = make_table([-(-n // page) for n in lens], seed)
+    pool = random_pool(total, n_kv, page, d, seed)
+    if poison:                                  # 0xff bytes (NaN pairs) in every place past the sequences' ends
+        used = torch.zeros(total, page, dtype=torch.bool)
+        for b, n in enumerate(lens):
+            for t in range(n):
+                used[table[b, t // page], t % page] = True
+        pn = pool.view(total, n_kv, page // 16, 16 * d + 128)
+        bad = ~used.view(total, page // 16, 16)
+        pairs = pn[..., 16 * d:].view(torch.int32).view(total, n_kv, page // 16, 2, 16)
+        pairs.masked_fill_(bad[:, None, :, None].cuda(), -1)
+        for side in (0, 1):
+            rows = pn[..., side * 8 * d:(side + 1) * 8 * d].view(total, n_kv, page // 16, 16, d // 2)
+            rows.masked_fill_(bad[:, None, :, :, None].cuda(), 255)
+    g = torch.Generator().manual_seed(seed + 1)
+    n_q = group * n_kv
+    wide = (torch.randn(batch, n_q + 2, d, generator=g) * q_scale).to(dtype).cuda()
+    q = wide[:, 1:1 + n_q]
+    rope = kv4.rope_table(max(lens + [1]), rot) if rot else None
+    tab = torch.from_numpy(table).cuda()
+    if skip:
+        for b, ps in skip.items():
+            for p in ps:
+                tab[b, p] = total + 5
+    cache = sq.PagedKV4(pool, tab, n_kv, d, page)
+    max_ctx = max_ctx or max(lens + [1])
+    out = torch.full((batch, n_q, d), 3.0, dtype=out_dtype, device="cuda")
+    lse = torch.full((batch, n_q), 3.0, device="cuda")
+    ws = torch.full((sq.sq_kv4_attn_workspace(batch, n_q, n_kv, d, max_ctx),), 255, dtype=torch.uint8, device="cuda")
+    flags = torch.zeros(1, dtype=torch.int32, device="cuda")
+    sq.sq_kv4_attn_decode(cache, torch.tensor(lens, dtype=torch.int32).cuda(), q, 0.0, out, max_ctx, ws,
+                          rope=sq.Rope(torch.from_numpy(rope).cuda(), inter) if rot else None, window=window, lse=lse,
+                          flags=flags)
+    assert flags.item() == (sq.SQ_FLAG_PAGE if skip else 0)
+    return check_attention(out, lse, q, [(b, n - 1) for b, n in enumerate(lens)], pool, table, page, n_q, n_kv, d,
+                           out_dtype, rope, inter, window, skip=skip)
+
+
+LENS = [1, 0, 2, 15, 16, 17, 31, 33, 64, 100, 129, 257]
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("group,dtype,out_dtype,page", [(1, F16, F16, 16), (3, BF16, BF16, 32), (4, F16, F32, 64),
+                                                        (5, BF16, F16, 16), (8, F16, BF16, 128), (11, BF16, F32, 32)])
+def test_decode_lengths(d, group, dtype, out_dtype, page):
+    decode_case(d, group, 2, dtype, out_dtype, page, LENS, rot=d if group % 2 else 0, inter=group == 3, poison=True)
+
+
+@pytest.mark.parametrize("d,group,lens,window", [(128, 4, [1300, 700, 5, 0, 2049], 0), (64, 2, [3001], 0), (256, 2, [900, 1500], 0),
+                                                 (128, 6, [700, 40, 1], 33), (64, 1, [500, 16], 1), (256, 8, [300, 257], 128),
+                                                 (128, 1, [5000], 0), (128, 16, [800, 90], 0)])
+def test_decode_longer_and_windows(d, group, lens, window):
+    decode_case(d, group, 1, BF16 if group % 2 else F16, F16, 16 if window else 32, lens, window=window, rot=64, seed=4)
+
+
+@pytest.mark.parametrize("q_scale", [1e-4, 30.0, 2000.0])
+def test_decode_small_and_large_queries(q_scale):
+    decode_case(128, 4, 1, BF16, F16, 16, [70, 300], q_scale=q_scale)
+
+
+def test_decode_leaves_pages_outside_the_pool_out():
+    decode_case(128, 4, 2, F16, F32, 16, [100, 40, 16], skip={0: (0, 3), 2: (0,)})
+    decode_case(64, 2, 1, F16, F32, 64, [300, 70], skip={0: (1,), 1: (1,)})
+
+
+def small_cache(d=128, n_kv=1, page=16, tokens=64, batch=1, seed=0):
+    need = -(-tokens // page)
+    table, total = make_table([need] * batch, seed)
+    return sq.PagedKV4(random_pool(total, n_kv, page, d, seed), torch.from_numpy(table).cuda(), n_kv, d, page), table
+
+
+def test_decode_cuts_and_flags_lengths():
+    cache, _ = small_cache()
+    ws = torch.empty(sq.sq_kv4_attn_workspace(1, 4, 1, 128, 64), dtype=torch.uint8, device="cuda")
+    q = torch.randn(1, 4, 128, device="cuda", dtype=F16)
+    outs = {}
+    for n, ctx, bit in ((64, 64, 0), (65, 80, sq.SQ_FLAG_SEQLEN), (2 ** 31 - 1, 80, sq.SQ_FLAG_SEQLEN), (30, 30, 0),
+                        (64, 30, sq.SQ_FLAG_SEQLEN), (-1, 64, sq.SQ_FLAG_SEQLEN), (-2 ** 31, 64, sq.SQ_FLAG_SEQLEN)):
+        out, flags = torch.full((1, 4, 128), 9.0, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+        sq.sq_kv4_attn_decode(cache, torch.tensor([n], dtype=torch.int32, device="cuda"), q, 0.0, out, ctx, ws, flags=flags)
+        assert flags.item() == bit, n
+        outs[n, ctx] = out
+    assert torch.equal(outs[65, 80], outs[64, 64]) and torch.equal(outs[2 ** 31 - 1, 80], outs[64, 64])
+    assert torch.equal(outs[64, 30], outs[30, 30])
+    assert not outs[-1, 64].any() and not outs[-2 ** 31, 64].any()
+    rope = sq.Rope(sq.rope_table(40, 128))
+    out, lse = torch.full((1, 4, 128), 9.0, device="cuda"), torch.zeros(1, 4, device="cuda")
+    flags = torch.zeros(1, dtype=torch.int32, device="cuda")
+    sq.sq_kv4_attn_decode(cache, torch.tensor([41], dtype=torch.int32, device="cuda"), q, 0.0, out, 64, ws, rope=rope, lse=lse,
+                          flags=flags)
+    assert flags.item() == sq.SQ_FLAG_ROPE and not out.any() and (lse == -math.inf).all()
+
+
+def test_not_finite_tokens_reach_only_the_rows_that_attend_them():
+    cache, table = small_cache(tokens=64, batch=2)
+    k = torch.randn(1, 1, 128, device="cuda", dtype=F16)
+    k[0, 0, 5] = math.nan
+    one = lambda x: torch.tensor([x], dtype=torch.int32, device="cuda")  # noqa: E731
+    row0 = sq.PagedKV4(cache.pages, cache.table[:1], 1, 128, 16)
+    q = torch.randn(2, 4, 128, device="cuda", dtype=F16)
+    ws = torch.empty(sq.sq_kv4_attn_workspace(2, 4, 1, 128, 64), dtype=torch.uint8, device="cuda")
+    for kk, vv in ((k, torch.zeros_like(k)), (torch.zeros_like(k), k)):
+        sq.sq_kv4_append(row0, kk, vv, one(40))
+        for n, nan in ((40, False), (41, True), (64, True)):
+            out = torch.empty(2, 4, 128, device="cuda")
+            sq.sq_kv4_attn_decode(cache, torch.tensor([n, 64], dtype=torch.int32, device="cuda"), q, 0.0, out, 64, ws)
+            assert bool(torch.isnan(out[0]).all()) == nan and not torch.isnan(out[1]).any()
+            out = torch.empty(2, 4, 128, device="cuda")
+            sq.sq_kv4_attn_decode(cache, torch.tensor([n, 64], dtype=torch.int32, device="cuda"), q, 0.0, out, 64, ws, window=8)
+            assert bool(torch.isnan(out[0]).all()) == (n == 41) and not torch.isnan(out[1]).any()
+
+
+# ------------------------------------------------------------------ chunks of queries
+def prefill_case(d, group, n_kv, dtype, out_dtype, page, start, new, window=0, rot=0, inter=False, seed=0, tail=3):
+    Q_TYPE[0] = dtype
+    table, total = make_table([-(-(s + n) // page) for s, n in zip(start, new)], seed)
+    pool = random_pool(total, n_kv, page, d, seed)
+    cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    n_tok, n_q = int(cu[-1]) + tail, group * n_kv
+    g = torch.Generator().manual_seed(seed + 1)
+    q = torch.randn(n_tok, n_q, d, generator=g).to(dtype).cuda()
+    rope = kv4.rope_table(max(s + n for s, n in zip(start, new)) + 1, rot) if rot else None
+    cache = sq.PagedKV4(pool, torch.from_numpy(table).cuda(), n_kv, d, page)
+    out = torch.full((n_tok, n_q, d), 3.0, dtype=out_dtype, device="cuda")
+    lse = torch.full((n_tok, n_q), 3.0, device="cuda")
+    ws = torch.full((sq.sq_kv4_attn_prefill_workspace(len(new), n_q, n_kv, d, n_tok),), 255, dtype=torch.uint8, device="cuda")
+    flags = torch.zeros(1, dtype=torch.int32, device="cuda")
+    sq.sq_kv4_attn_prefill(cache, torch.tensor(start, dtype=torch.int32).cuda(), torch.from_numpy(cu).cuda(), q, 0.0, out, ws,
+                           rope=sq.Rope(torch.from_numpy(rope).cuda(), inter) if rot else None, window=window, lse=lse,
+                           flags=flags)
+    assert flags.item() == 0
+    pos = [(b, start[b] + i) for b in range(len(new)) for i in range(new[b])] + [(-1, 0)] * tail
+    check_attention(out, lse, q, pos, pool, table, page, n_q, n_kv, d, out_dtype, rope, inter, window)
+    assert (out[cu[-1]:] == 3).all() and (lse[cu[-1]:] == 3).all()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("group,dtype,out_dtype,page", [(1, F16, F16, 16), (4, BF16, BF16, 32), (5, F16, F32, 16), (8, BF16, F16, 128)])
+def test_prefill_ragged(d, group, dtype, out_dtype, page):
+    prefill_case(d, group, 1, dtype, out_dtype, page, [0, 7, 0, 130, 31], [3, 0, 1, 20, 40], rot=d if group != 4 else 0,
+                 inter=group == 5)
+
+
+@pytest.mark.parametrize("d,group,start,new,window", [(128, 4, [0], [300], 0), (64, 2, [500], [150], 0), (256, 2, [0, 260], [140, 70], 0),
+                                                      (128, 2, [100, 0], [130, 260], 17), (64, 8, [0], [129], 1),
+                                                      (128, 1, [1000], [140], 600), (128, 16, [200], [20], 0)])
+def test_prefill_longer_and_windows(d, group, start, new, window):
+    prefill_case(d, group, 1, F16, F16, 16 if window else 64, start, new, window=window, rot=32, seed=9)
+
+
+def test_prefill_takes_nothing_from_places_that_are_masked():
+    """NaN in every place past a query's own position leaves its output what it was."""
+    d, page, n = 128, 16, 150
+    cache, _ = small_cache(d=d, page=page, tokens=n)
+    cu, start = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0, 40], [60]))
+    q = torch.randn(40, 4, d, device="cuda", dtype=F16)
+    ws = torch.empty(sq.sq_kv4_attn_prefill_workspace(1, 4, 1, d, 40), dtype=torch.uint8, device="cuda")
+    a, b = (torch.empty(40, 4, d, device="cuda", dtype=F16) for _ in range(2))
+    sq.sq_kv4_attn_prefill(cache, start, cu, q, 0.0, a, ws)
+    bad = torch.full((50, 1, d), math.nan, device="cuda", dtype=F16)
+    sq.sq_kv4_append(cache, bad, bad, torch.tensor([100], dtype=torch.int32, device="cuda"),
+                     torch.tensor([0, 50], dtype=torch.int32, device="cuda"))
+    sq.sq_kv4_attn_prefill(cache, start, cu, q, 0.0, b, ws)
+    assert torch.equal(a, b)
+    sq.sq_kv4_append(cache, bad[:1], bad[:1], torch.tensor([80], dtype=torch.int32, device="cuda"))
+    sq.sq_kv4_attn_prefill(cache, start, cu, q, 0.0, b, ws)
+    assert torch.equal(a[:20], b[:20]) and torch.isnan(b[20:]).all()
+
+
+def test_prefill_of_wrong_offsets_stays_in_bounds():
+    """Offsets and starts that name no tokens of the call: nothing is written for them."""
+    cache, _ = small_cache(batch=3)
+    q = torch.randn(8, 4, 128, device="cuda", dtype=F16)
+    ws = torch.empty(sq.sq_kv4_attn_prefill_workspace(3, 4, 1, 128, 8), dtype=torch.uint8, device="cuda")
+    for cu, start, bit in (([0, 4, 2, 8], [0, 0, 0], None), ([0, 400, 500, 600], [0, 0, 0], None), ([-5, 2, 4, 8], [0, 0, 0], None),
+                           ([0, 2, 4, 8], [-3, 0, 0], sq.SQ_FLAG_SEQLEN), ([0, 2, 4, 8], [0, 0, 62], sq.SQ_FLAG_SEQLEN),
+                           ([0, 2, 4, 8], [0, 0, 2 ** 31 - 1], sq.SQ_FLAG_SEQLEN)):
+        out = torch.full((8, 4, 128), 3.0, device="cuda", dtype=F16)
+        flags = torch.zeros(1, dtype=torch.int32, device="cuda")
+        sq.sq_kv4_attn_prefill(cache, torch.tensor(start, dtype=torch.int32, device="cuda"),
+                               torch.tensor(cu, dtype=torch.int32, device="cuda"), q, 0.0, out, ws, flags=flags)
+        torch.cuda.synchronize()
+        if bit is not None:
+            assert flags.item() == bit
+
+
+# ------------------------------------------------------------------ together
+@pytest.mark.parametrize("d,dtype,group", [(64, BF16, 2), (128, F16, 5), (256, BF16, 1)])
+def test_prompt_then_steps_match_the_oracle(d, dtype, group):
+    """Two prompts appended and attended, then four decode steps of the batch: every output against the oracle's
+    attention over what the oracle's own append holds."""
+    Q_TYPE[0] = dtype
+    n_kv, page, prompts, steps = 2, 16, [21, 50], 4
+    n_q = group * n_kv
+    g = torch.Generator().manual_seed(11)
+    rope = kv4.rope_table(80, d)
+    r = sq.Rope(torch.from_numpy(rope).cuda())
+    table, total = make_table([-(-(n + steps) // page) for n in prompts], 5)
+    cache = sq.alloc_kv4(total, n_kv, d, page, torch.from_numpy(table).cuda())
+    want = cache.pages.cpu().numpy().copy()
+    cu = [0, prompts[0], sum(prompts)]
+    qkv = torch.randn(sum(prompts), (n_q + 2 * n_kv), d, generator=g).to(dtype)
+    cut = lambda t: (t[:, :n_q], t[:, n_q:n_q + n_kv], t[:, n_q + n_kv:])  # noqa: E731
+    _, k, v = cut(qkv)
+    append_oracle(want, table, page, k, v, [0, 0], cu, rope, False, dtype)
+    q, k, v = cut(qkv.cuda())
+    zero, cud = torch.zeros(2, dtype=torch.int32, device="cuda"), torch.tensor(cu, dtype=torch.int32, device="cuda")
+    sq.sq_kv4_append(cache, k, v, zero, cud, rope=r)
+    assert np.array_equal(cache.pages.cpu().numpy(), want)
+    out, lse = torch.empty(sum(prompts), n_q, d, dtype=dtype, device="cuda"), torch.empty(sum(prompts), n_q, device="cuda")
+    ws = torch.empty(sq.sq_kv4_attn_prefill_workspace(2, n_q, n_kv, d, sum(prompts)), dtype=torch.uint8, device="cuda")
+    sq.sq_kv4_attn_prefill(cache, zero, cud, q, 0.0, out, ws, rope=r, lse=lse)
+    pos = [(b, i) for b in range(2) for i in range(prompts[b])]
+    check_attention(out, lse, q, pos, cache.pages, table, page, n_q, n_kv, d, dtype, rope)
+    ws = torch.empty(sq.sq_kv4_attn_workspace(2, n_q, n_kv, d, 80), dtype=torch.uint8, device="cuda")
+    for i in range(steps):
+        at = [n + i for n in prompts]
+        qkv = torch.randn(2, n_q + 2 * n_kv, d, generator=g).to(dtype)
+        _, k, v = cut(qkv)
+        append_oracle(want, table, page, k, v, at, None, rope, False, dtype)
+        q, k, v = cut(qkv.cuda())
+        out, lse = torch.empty(2, n_q, d, dtype=dtype, device="cuda"), torch.empty(2, n_q, device="cuda")
+        sq.sq_kv4_decode_step(cache, k, v, q, torch.tensor(at, dtype=torch.int32, device="cuda"), 0.0, out, 80, ws, rope=r,
+                              lse=lse)
+        assert np.array_equal(cache.pages.cpu().numpy(), want)
+        check_attention(out, lse, q, [(0, at[0]), (1, at[1])], cache.pages, table, page, n_q, n_kv, d, dtype, rope)
+
+
+def test_step_is_append_then_decode_and_shared_prefix_pages_are_read():
+    d, page, n_kv, n_q = 128, 16, 2, 8
+    table, total = make_table([3, 3, 3], 2, shared=((1, 0, 0), (1, 0, 1), (2, 0, 0)))
+    pool = random_pool(total, n_kv, page, d, 3)
+    g = torch.Generator(device="cuda").manual_seed(0)
+    k, v = (torch.randn(3, n_kv, d, generator=g, device="cuda").to(F16) for _ in range(2))
+    q = torch.randn(3, n_q, d, generator=g, device="cuda").to(F16)
+    pos = torch.tensor([40, 33, 20], dtype=torch.int32, device="cuda")
+    ws = torch.empty(sq.sq_kv4_attn_workspace(3, n_q, n_kv, d, 48), dtype=torch.uint8, device="cuda")
+    rope = sq.Rope(sq.rope_table(64, d))
+    a = sq.PagedKV4(pool.clone(), torch.from_numpy(table).cuda(), n_kv, d, page)
+    b = sq.PagedKV4(pool.clone(), torch.from_numpy(table).cuda(), n_kv, d, page)
+    oa, ob = (torch.empty(3, n_q, d, device="cuda") for _ in range(2))
+    sq.sq_kv4_decode_step(a, k, v, q, pos, 0.0, oa, 48, ws, rope=rope)
+    sq.sq_kv4_append(b, k, v, pos, rope=rope)
+    sq.sq_kv4_attn_decode(b, pos + 1, q, 0.0, ob, 48, ws, rope=rope)
+    assert torch.equal(a.pages, b.pages) and torch.equal(oa, ob)
+
+
+def test_graphs_that_share_a_workspace_and_other_streams():
+    d, n_q = 128, 8
+    cache, _ = small_cache(d=d, n_kv=2, tokens=1200, batch=3, seed=7)
+    g = torch.Generator(device="cuda").manual_seed(0)
+    q = [torch.randn(3, n_q, d, generator=g, device="cuda").to(F16) for _ in range(2)]
+    lens = [torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([1200, 0, 700], [3, 1100, 900])]
+    ws = torch.full((sq.sq_kv4_attn_workspace(3, n_q, 2, d, 1200),), 255, dtype=torch.uint8, device="cuda")
+    eager = []
+    for i in range(2):
+        o = torch.empty(3, n_q, d, device="cuda")
+        sq.sq_kv4_attn_decode(cache, lens[i], q[i], 0.0, o, 1200, ws)
+        eager.append(o)
+    graphs, outs = [], []
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for i in range(2):
+        gr, o = torch.cuda.CUDAGraph(), torch.zeros(3, n_q, d, device="cuda")
+        with torch.cuda.stream(side):
+            sq.sq_kv4_attn_decode(cache, lens[i], q[i], 0.0, o, 1200, ws)
+        torch.cuda.synchronize()
+        assert torch.equal(o, eager[i])                              # the side stream's own result
+        o.zero_()
+        with torch.cuda.graph(gr):
+            sq.sq_kv4_attn_decode(cache, lens[i], q[i], 0.0, o, 1200, ws)
+        graphs.append(gr)
+        outs.append(o)
+    for _ in range(3):
+        for o in outs:
+            o.zero_()
+        for gr in graphs:
+            gr.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, e) for o, e in zip(outs, eager))
+    lens[0].copy_(torch.tensor([5, 1200, 64], dtype=torch.int32))    # a replay follows the lengths on the device
+    graphs[0].replay()
+    ref = torch.empty(3, n_q, d, device="cuda")
+    sq.sq_kv4_attn_decode(cache, lens[0], q[0], 0.0, ref, 1200, ws)
+    assert torch.equal(outs[0], ref)
