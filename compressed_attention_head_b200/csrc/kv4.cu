@@ -1,12 +1,14 @@
 // Host entry points of the paged 4-bit cache: argument checks and launches.
 // The contract (arguments, layout, errors) is in include/sq.h.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "sq_common.cuh"
 
 #include "kv4_append.cuh"
 #include "kv4_attn.cuh"
+#include "kv4_decode.cuh"
 
 namespace sq {
 namespace kv4 {
@@ -138,6 +140,99 @@ sq_status run_attn(const Pool& c, const RopeArgs& r, const void* q, sq_dtype dty
   return cuda_ok(cudaGetLastError());
 }
 
+// ---------------------------------------------------------------- single tokens
+int sms() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+      n < 1) {
+    cudaGetLastError();
+    return 148;              // a B200's, for size queries on a host without a GPU
+  }
+  return n;
+}
+
+// More than 48 KB of dynamic shared memory has to be asked for, once a kernel and device.
+template <typename K> cudaError_t allow_smem(K* kernel, int bytes, std::atomic<uint64_t>* done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev < 64 && (done->load() & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) done->fetch_or(bit);
+  return e;
+}
+
+// Launch whose prologue may overlap the kernel before it on the stream (it waits for that kernel itself).
+template <typename... KA, typename... A>
+cudaError_t launch_overlapped(void (*kernel)(KA...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, A... args) {
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, KA(args)...);
+}
+
+int head_passes(int group) { return group <= 4 ? 1 : (group + 7) / 8; }
+
+// Blocks: two an SM, fewer where the bound on the lengths leaves less than a block's eight tiles each.
+int decode_blocks(int batch, int n_kv, int group, int d, int64_t max_ctx) {
+  const int tt = d == 256 ? 16 : 32;
+  const int64_t tiles = (max_ctx + tt - 1) / tt + 1;
+  const int64_t units = (tiles + dec::W - 1) / dec::W;
+  const double all = (double)batch * n_kv * head_passes(group) * (double)units;
+  const int most = 2 * sms();
+  return all < most ? (int)all : most;
+}
+
+size_t decode_ws(int blocks, int d) {
+  return (size_t)2 * blocks * dec::part_floats(d) * 4 + (size_t)blocks * sizeof(dec::Desc);
+}
+
+template <typename T, typename TO, int D, bool PAIR>
+cudaError_t launch_decode(const Pool& c, const RopeArgs& r, const void* q, void* out, const AttnArgs& a, void* ws,
+                          bool overlap, cudaStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  auto kernel = dec::k_decode4<T, TO, D, PAIR>;
+  cudaError_t e = allow_smem(kernel, dec::Smem<D>::TOTAL, &done);
+  if (e != cudaSuccess) return e;
+  const int blocks = decode_blocks(c.batch, c.n_kv, a.group, D, std::min<int64_t>(a.max_ctx, (int64_t)c.per_row << c.page_shift));
+  const int nsub = head_passes(a.group);
+  float* parts = (float*)ws;
+  dec::Desc* descs = (dec::Desc*)(parts + (size_t)2 * blocks * dec::part_floats(D));
+  if (overlap)
+    e = launch_overlapped(kernel, blocks, 32 * dec::W, dec::Smem<D>::TOTAL, st, c, r, (const T*)q, (TO*)out, a, nsub, parts, descs);
+  else
+    kernel<<<blocks, 32 * dec::W, dec::Smem<D>::TOTAL, st>>>(c, r, (const T*)q, (TO*)out, a, nsub, parts, descs);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const int hs = PAIR ? 4 : 8;
+  return launch_overlapped(dec::k_join4<TO, D>, dim3(blocks, std::min(hs, a.group)), 256, 0, st, parts, descs, (TO*)out, a, nsub, hs);
+}
+
+sq_status run_decode(const Pool& c, const RopeArgs& r, const void* q, sq_dtype dtype, void* out, sq_dtype out_dtype,
+                     const AttnArgs& a, void* ws, bool overlap, cudaStream_t st) {
+  cudaError_t e = cudaSuccess;
+#define SQ_CALL2(T, TO, DD) \
+  e = a.group <= 4 ? launch_decode<T, TO, DD, true>(c, r, q, out, a, ws, overlap, st) \
+                   : launch_decode<T, TO, DD, false>(c, r, q, out, a, ws, overlap, st)
+#define SQ_CALL(T, DD)                                   \
+  if (out_dtype == SQ_F32) SQ_CALL2(T, float, DD);       \
+  else if (out_dtype == SQ_F16) SQ_CALL2(T, __half, DD); \
+  else SQ_CALL2(T, __nv_bfloat16, DD)
+  if (dtype == SQ_F16) { SQ_KV4_D(__half, SQ_CALL) }
+  else { SQ_KV4_D(__nv_bfloat16, SQ_CALL) }
+#undef SQ_CALL
+#undef SQ_CALL2
+  return cuda_ok(e);
+}
+
 float scale_of(float scale, int d) { return scale > 0.0f ? scale : 1.0f / sqrtf((float)d); }
 
 }  // namespace
@@ -179,7 +274,7 @@ sq_status sq_kv4_read(const sq_kv4_cache* cache, void* k_out, void* v_out, sq_dt
 size_t sq_kv4_attn_workspace(int batch, int n_q_heads, int n_kv_heads, int d, int64_t max_ctx) {
   if (batch < 1 || n_q_heads < 1 || n_kv_heads < 1 || n_q_heads % n_kv_heads != 0 || !head_dim_ok(d) || max_ctx < 1)
     return 0;
-  return 256;
+  return decode_ws(decode_blocks(batch, n_kv_heads, n_q_heads / n_kv_heads, d, max_ctx), d);
 }
 
 sq_status sq_kv4_attn_decode(const sq_kv4_cache* cache, const int32_t* d_seq_lens, int n_q_heads, int64_t max_ctx,
@@ -192,9 +287,9 @@ sq_status sq_kv4_attn_decode(const sq_kv4_cache* cache, const int32_t* d_seq_len
   if (!d_seq_lens || !aligned(d_seq_lens, 4) || max_ctx < 1) return SQ_ERR_ARG;
   if (ws_bytes < sq_kv4_attn_workspace(cache->batch, n_q_heads, cache->n_kv_heads, cache->d, max_ctx))
     return SQ_ERR_WORKSPACE;
-  AttnArgs a{nullptr, d_seq_lens, -1, cache->batch, max_ctx, q_stride_row, q_stride_head, n_q_heads,
-             n_q_heads / cache->n_kv_heads, window, scale_of(scale, cache->d), lse_out, d_flags};
-  return run_attn(pool_of(cache), rope_of(rope), q, dtype, out, out_dtype, a, (cudaStream_t)stream);
+  const AttnArgs a{nullptr, d_seq_lens, -1, cache->batch, max_ctx, q_stride_row, q_stride_head, n_q_heads,
+                   n_q_heads / cache->n_kv_heads, window, scale_of(scale, cache->d), lse_out, d_flags};
+  return run_decode(pool_of(cache), rope_of(rope), q, dtype, out, out_dtype, a, ws, false, (cudaStream_t)stream);
 }
 
 sq_status sq_kv4_decode_step(const sq_kv4_cache* cache, const void* k, const void* v, const void* q, sq_dtype dtype,
@@ -216,9 +311,9 @@ sq_status sq_kv4_decode_step(const sq_kv4_cache* cache, const void* k, const voi
   const RopeArgs r = rope_of(rope);
   s = run_append(c, r, k, v, dtype, ap, (cudaStream_t)stream);
   if (s != SQ_OK) return s;
-  AttnArgs a{nullptr, d_pos, 0, cache->batch, max_ctx, q_stride_row, q_stride_head, n_q_heads,
-             n_q_heads / cache->n_kv_heads, window, scale_of(scale, cache->d), lse_out, d_flags};
-  return run_attn(c, r, q, dtype, out, out_dtype, a, (cudaStream_t)stream);
+  const AttnArgs a{nullptr, d_pos, 0, cache->batch, max_ctx, q_stride_row, q_stride_head, n_q_heads,
+                   n_q_heads / cache->n_kv_heads, window, scale_of(scale, cache->d), lse_out, d_flags};
+  return run_decode(c, r, q, dtype, out, out_dtype, a, ws, true, (cudaStream_t)stream);
 }
 
 size_t sq_kv4_attn_prefill_workspace(int batch, int n_q_heads, int n_kv_heads, int d, int64_t n_tok) {
@@ -241,8 +336,8 @@ sq_status sq_kv4_attn_prefill(const sq_kv4_cache* cache, const int32_t* d_cu, co
     return SQ_ERR_ARG;
   if (ws_bytes < sq_kv4_attn_prefill_workspace(cache->batch, n_q_heads, cache->n_kv_heads, cache->d, n_tok))
     return SQ_ERR_WORKSPACE;
-  AttnArgs a{d_cu, d_start, 0, n_tok, 0x7fffffff, q_stride_tok, q_stride_head, n_q_heads,
-             n_q_heads / cache->n_kv_heads, window, scale_of(scale, cache->d), lse_out, d_flags};
+  const AttnArgs a{d_cu, d_start, 0, n_tok, 0x7fffffff, q_stride_tok, q_stride_head, n_q_heads,
+                   n_q_heads / cache->n_kv_heads, window, scale_of(scale, cache->d), lse_out, d_flags};
   return run_attn(pool_of(cache), rope_of(rope), q, dtype, out, out_dtype, a, (cudaStream_t)stream);
 }
 

@@ -1,25 +1,12 @@
-// Attention over the paged 4-bit cache, the plain kernel: one block a (query
+// Attention of chunks of queries over the paged 4-bit cache: one block a (query
 // token, query head), tiles of 128 keys; a thread forms one key's score, then one
 // coordinate's sum over the tile. Online softmax in base 2, everything in float.
 #pragma once
 
-#include "kv4.cuh"
+#include "kv4_decode.cuh"
 
 namespace sq {
 namespace kv4 {
-
-struct AttnArgs {
-  const int32_t* cu;      // chunks: token offsets of the sequences; NULL: one query a sequence
-  const int32_t* start;   // chunks: position of a sequence's first query; decode: see len_off
-  int len_off;            // position of the query = start + len_off (-1: start holds lengths)
-  int64_t n_tok;
-  int64_t max_ctx;        // bound on the attended positions
-  int64_t qs_tok, qs_head;
-  int n_q, group, window;
-  float scale;
-  float* lse;
-  uint32_t* flags;
-};
 
 constexpr int kPlainTile = 128;
 

@@ -1,0 +1,745 @@
+// Attention of one query a sequence over the paged 4-bit cache.
+//
+// Mathematics. With q' = q 2^e (a power of two a head, so that fp16 holds it) and
+// codes c, the score of token t is s_t (q . c_t) + m_t sum(q), and the output is
+// sum_t (p_t s_t) c_t + sum_t p_t m_t: the tensor cores multiply the codes
+// themselves, and the pairs act on scores and probabilities, one token at a time,
+// never on coordinates. A code of 4 bits masked out of its word in place is the
+// fp16 subnormal c 2^-24 (bits 0-3) or 16 c 2^-24 (bits 4-7) in each half of the
+// word: one AND makes two operands, exactly, and the 16 goes into q' or out of the
+// sum. ldmatrix (for the values, its transposed form) lays the words out so that
+// the two halves of a word are the two neighbours along k that mma.sync wants.
+//
+// Softmax: one pass, base 2. Each warp keeps a reference maximum a head, raised
+// when a score passes it by more than 2^4 (one vote a tile), and a reference step
+// (a power of two over all value steps it has met), so that p s, scaled to at most
+// 2^15, keeps fp16's full precision; it enters the product as a high and a low
+// half, 22 bits in all. With up to four query heads a KV head the halves take the
+// two columns a head has in the N = 8 of the product; with up to eight the low
+// halves are a second product into the same accumulators.
+//
+// Work. The tiles of all (sequence, KV head) pairs form one line that the resident
+// blocks (two an SM) share evenly, whatever the lengths; inside a block tile i goes
+// to warp i mod 8. A warp brings its tiles by bulk copies into a ring of its own and
+// meets the other warps only where a pair ends, to add up. Pairs cut by a block's
+// end leave partial sums that a second, overlapped launch joins, in order: results
+// do not depend on timing.
+#pragma once
+
+#include "kv4_append.cuh"
+#include "sm100.cuh"
+
+namespace sq {
+namespace kv4 {
+
+struct AttnArgs {
+  const int32_t* cu;      // chunks: token offsets of the sequences; NULL: one query a sequence
+  const int32_t* start;   // chunks: position of a sequence's first query; decode: see len_off
+  int len_off;            // position of the query = start + len_off (-1: start holds lengths)
+  int64_t n_tok;
+  int64_t max_ctx;        // bound on the attended positions
+  int64_t qs_tok, qs_head;
+  int n_q, group, window;
+  float scale;
+  float* lse;
+  uint32_t* flags;
+};
+
+namespace dec {
+
+constexpr int W = 8;                       // warps of a block
+constexpr int kMaxHeads = 8;               // query heads of one pass over a KV head
+constexpr float kSlack = 4.0f;             // log2 of what a probability may exceed 1 by
+constexpr float kTop = 2048.0f;            // 2^11: scale of p s / reference, at most 2^15 with the slack
+
+template <int D> struct Cfg {
+  static constexpr int NB = D == 256 ? 1 : 2;             // 16-token blocks of a tile
+  static constexpr int TT = 16 * NB;
+  static constexpr int STAGE = NB * blk_bytes(D);
+  static constexpr int NST = D == 64 ? 4 : 2;             // tiles in a warp's ring
+  static constexpr int QROW = 2 * D + 64;                 // bytes of a head's query operand (64 over: conflict-free)
+  static constexpr bool QREG = D <= 128;                  // the query operand stays in registers
+};
+
+template <int D> struct Smem {
+  static constexpr int RING = W * Cfg<D>::NST * Cfg<D>::STAGE;
+  static constexpr int MERGE = W * kMaxHeads * 64 * 4;
+  static constexpr int Q = kMaxHeads * Cfg<D>::QROW;
+  static constexpr int TOTAL = RING + MERGE + Q;
+};
+
+// One partial result: a pass's heads x D sums, then (max, sum) a head.
+__host__ __device__ constexpr int part_floats(int d) { return kMaxHeads * (d + 2); }
+struct Desc { int parts, row, hsub, pad; };       // parts 0: this block owns no cut pair
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
+}
+__device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
+}
+__device__ __forceinline__ uint32_t movm(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ void mma(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *(const uint32_t*)&h;
+}
+__device__ __forceinline__ float2 unpack_h2(uint32_t u) { return __half22float2(*(const __half2*)&u); }
+
+// Attended positions [lo, hi) of a row's query; hi = 0 where there is nothing to do.
+struct Span { int lo, hi; };
+__device__ __forceinline__ Span span_of(const Pool& c, const RopeArgs& r, const AttnArgs& a, int b, uint32_t* flags) {
+  const int64_t lim = min(c.cap(), a.max_ctx);
+  int64_t n = (int64_t)__ldg(a.start + b) + a.len_off + 1;
+  uint32_t bits = 0;
+  if (n > lim || n < 0) {
+    bits = SQ_FLAG_SEQLEN;
+    n = n < 0 ? 0 : lim;
+  }
+  if (r.table && n > r.n_pos) {
+    bits |= SQ_FLAG_ROPE;
+    n = 0;
+  }
+  if (bits && flags) atomicOr(flags, bits);
+  Span s;
+  s.hi = (int)n;
+  s.lo = a.window > 0 && n > a.window ? (int)(n - a.window) : 0;
+  return s;
+}
+template <int TT> __device__ __forceinline__ int tiles_of(Span s) {
+  return s.hi > 0 ? (s.hi - 1) / TT - s.lo / TT + 1 : 0;
+}
+
+// The line of tiles: `line` tiles in all (each pair's count rounded up to
+// `unit`), `quota` to a block.
+struct Plan {
+  int64_t line;
+  int quota, unit;
+  int row;                 // of the block's first tile
+  int64_t row_at;          // and where that row begins on the line
+};
+
+__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0;
+#pragma unroll
+  for (int i = 0; i < W; ++i) v += red[i];
+  return v;
+}
+
+template <int TT>
+__device__ Plan make_plan(const Pool& c, const RopeArgs& r, const AttnArgs& a, int per_row, int64_t* red) {
+  __shared__ int s_row;
+  __shared__ int64_t s_at;
+  const int tid = threadIdx.x, lane = tid & 31;
+  int64_t n = 0, padded = 0;
+  for (int b = tid; b < c.batch; b += 32 * W) {
+    const int t = tiles_of<TT>(span_of(c, r, a, b, nullptr));
+    n += t;
+    padded += (t + W - 1) / W * W;
+  }
+  n = block_sum(n, red) * per_row;
+  padded = block_sum(padded, red) * per_row;
+  Plan p;
+  // Few tiles: a block takes up to eight tiles of one pair, a warp one; no block crosses a pair.
+  // Many: equal shares of the line.
+  p.unit = padded <= (int64_t)gridDim.x * W ? W : 1;
+  p.line = p.unit == W ? padded : n;
+  p.quota = p.unit == W ? W : (int)((n + gridDim.x - 1) / gridDim.x);
+  const int64_t first = (int64_t)blockIdx.x * p.quota;
+  if (tid == 0) s_row = -1;
+  int64_t carry = 0;
+  for (int b0 = 0; b0 < c.batch; b0 += 32 * W) {
+    int64_t mine = 0;
+    if (b0 + tid < c.batch) {
+      const int t = tiles_of<TT>(span_of(c, r, a, b0 + tid, nullptr));
+      mine = (int64_t)((t + p.unit - 1) / p.unit * p.unit) * per_row;
+    }
+    int64_t inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    __syncthreads();
+    if (lane == 31) red[tid >> 5] = inc;
+    __syncthreads();
+    int64_t before = carry;
+    for (int i = 0; i < W; ++i) {
+      if (i < (tid >> 5)) before += red[i];
+      carry += red[i];
+    }
+    const int64_t at = before + inc - mine;
+    if (mine > 0 && at <= first && first < at + mine) {
+      s_row = b0 + tid;
+      s_at = at;
+    }
+    if (carry > first) break;
+  }
+  __syncthreads();
+  p.row = s_row;
+  p.row_at = s_at;
+  return p;
+}
+
+// Walks a warp's tiles along the line and fetches their page numbers one tile ahead of their copies.
+template <int D>
+struct Cursor {
+  int row, hsub, tile, nt;        // nt: the pair's tiles, rounded up
+  int lo, hi;
+  int64_t left;                   // tiles to the block's end, from this one
+  __device__ __forceinline__ void enter(const Pool& c, const RopeArgs& r, const AttnArgs& a, int unit) {
+    const Span s = span_of(c, r, a, row, nullptr);
+    lo = s.lo;
+    hi = s.hi;
+    nt = (tiles_of<Cfg<D>::TT>(s) + unit - 1) / unit * unit;
+  }
+  __device__ __forceinline__ void advance(const Pool& c, const RopeArgs& r, const AttnArgs& a, int unit, int per_row,
+                                          int by) {
+    left -= by;
+    if (left <= 0) return;
+    tile += by;
+    while (tile >= nt) {
+      tile -= nt;
+      if (++hsub == per_row) {
+        hsub = 0;
+        do {
+          ++row;
+          enter(c, r, a, unit);
+        } while (nt == 0);
+      }
+    }
+  }
+};
+
+template <typename T, typename TO, int D, bool PAIR>
+__global__ void __launch_bounds__(32 * W, 2)
+k_decode4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, AttnArgs a, int nsub, float* parts,
+          Desc* descs) {
+  using C = Cfg<D>;
+  constexpr int HS = PAIR ? 4 : 8;
+  constexpr int NC = D / 32;                    // 16-byte chunks of a code row
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(8) uint64_t bars[W][C::NST];
+  __shared__ uint32_t oks[W][C::NST];
+  __shared__ int64_t red[W];
+  __shared__ float s_q[kMaxHeads][2];           // score factor (of q . c) and m factor, a head
+  __shared__ float s_ml[W][kMaxHeads][4];       // a warp's max, sum, sum of p m, scale of its sums
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, cc = lane & 3;
+  uint8_t* ring = smem + warp * C::NST * C::STAGE;
+  float* merge = (float*)(smem + Smem<D>::RING);
+  uint8_t* qop = smem + Smem<D>::RING + Smem<D>::MERGE;
+  if (lane == 0) {
+    for (int i = 0; i < C::NST; ++i) sm100::mbar_init(&bars[warp][i], 1);
+    sm100::fence_mbar_init();
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int per_row = c.n_kv * nsub;
+  const Plan plan = make_plan<C::TT>(c, r, a, per_row, red);
+  asm volatile("griddepcontrol.wait;" ::: "memory");      // a decode step's append must be in the pool
+  // rows with nothing to attend
+  for (int b = blockIdx.x; b < c.batch; b += gridDim.x) {
+    const Span s = span_of(c, r, a, b, tid == 0 ? a.flags : nullptr);
+    if (s.hi > 0) continue;
+    for (int i = tid; i < a.n_q * D; i += 32 * W) out[(int64_t)b * a.n_q * D + i] = from_f<TO>(0.0f);
+    if (a.lse)
+      for (int i = tid; i < a.n_q; i += 32 * W) a.lse[(int64_t)b * a.n_q + i] = -INFINITY;
+  }
+  const int64_t first = (int64_t)blockIdx.x * plan.quota;
+  const int64_t last = min(first + plan.quota, plan.line);
+  if (tid == 0) descs[blockIdx.x].parts = 0;
+  if (first >= last) return;
+
+  // ---- the warp's copies
+  Cursor<D> ahead;
+  ahead.row = plan.row;
+  ahead.enter(c, r, a, plan.unit);
+  ahead.hsub = (int)((first - plan.row_at) / ahead.nt);
+  ahead.tile = (int)((first - plan.row_at) % ahead.nt);
+  const int row0 = ahead.row, hsub0 = ahead.hsub, tile0 = ahead.tile;
+  ahead.left = last - first;
+  ahead.advance(c, r, a, plan.unit, per_row, warp);
+  int pf_page = 0;
+  int64_t pf_off = 0;
+  bool pf_in = false;
+  // page number of the cursor's tile (lanes below NB: a 16-token block each)
+  auto look = [&]() {
+    pf_in = false;
+    if (ahead.left > 0 && lane < C::NB) {
+      const int t = (ahead.lo / C::TT + ahead.tile) * C::TT + 16 * lane;
+      if (t < ahead.hi && t + 16 > ahead.lo) {
+        pf_in = true;
+        pf_page = __ldg(c.table + ahead.row * c.table_stride + (t >> c.page_shift));
+        pf_off = ((((int64_t)(ahead.hsub / nsub)) << (c.page_shift - 4)) + ((t & ((1 << c.page_shift) - 1)) >> 4)) * blk_bytes(D);
+      }
+    }
+  };
+  const int64_t page_bytes = ((int64_t)c.n_kv << (c.page_shift - 4)) * blk_bytes(D);
+  auto issue = [&](int st) {
+    const bool ok = pf_in && pf_page >= 0 && pf_page < c.n_pages;
+    if (pf_in && !ok) raise(a.flags, SQ_FLAG_PAGE);
+    const uint32_t mask = __ballot_sync(0xffffffffu, ok);
+    if (lane == 0) {
+      oks[warp][st] = mask;
+      sm100::mbar_expect_tx(&bars[warp][st], __popc(mask) * blk_bytes(D));
+    }
+    __syncwarp();
+    if (ok)
+      sm100::bulk_load(ring + st * C::STAGE + lane * blk_bytes(D), c.pages + pf_page * page_bytes + pf_off,
+                       blk_bytes(D), &bars[warp][st]);
+  };
+  look();
+#pragma unroll
+  for (int i = 0; i < C::NST - 1; ++i) {
+    issue(i);
+    ahead.advance(c, r, a, plan.unit, per_row, W);
+    look();
+  }
+
+  // ---- fragment addresses inside a block
+  const int krow = (lane & 7) + ((lane >> 3) & 1) * 8, kch = lane >> 4;
+  const int vrow = (lane & 7) + (lane >> 4) * 8, vch = (lane >> 3) & 1;
+  const uint32_t koff = krow * (D / 2) + ((kch ^ swz(krow, D)) << 4);
+  const uint32_t voff = v_codes(D) + vrow * (D / 2) + ((vch ^ swz(vrow, D)) << 4);
+  const uint32_t ring_u = sm100::smem_u32(ring);
+
+  Cursor<D> at;                                  // the segment (pair) being summed, the same for all warps
+  at.row = row0;
+  at.enter(c, r, a, plan.unit);
+  at.hsub = hsub0;
+  at.tile = tile0;
+  int64_t seg = first;                           // line position of the segment's first tile in this block
+  int stage = 0;
+  uint32_t phase = 0;
+  bool dead = false;
+  int64_t mine = first + warp;
+
+  while (seg < last) {
+    const int64_t seg_end = min(last, seg + (at.nt - at.tile));
+    const int kvh = at.hsub / nsub, h0 = kvh * a.group + (at.hsub % nsub) * HS;
+    const int nh = min(HS, (kvh + 1) * a.group - h0);
+    // ---- the query operand: D / 8 threads a head
+    __syncthreads();
+    for (int base = 0; base < HS * (D / 8); base += 32 * W) {
+      const int i = base + tid, hh = i / (D / 8), j = i % (D / 8);
+      float x[8];
+      if (hh < nh) {
+        const T* src = q + (int64_t)at.row * a.qs_tok + (int64_t)(h0 + hh) * a.qs_head;
+        unpack8<T>(load8<T>(src + 8 * j), x);
+        if (r.table) {
+          float y[8];
+          const int pi = partner(8 * j, r);
+          if (pi != 8 * j) unpack8<T>(load8<T>(src + pi), y);
+          rotate8<T>(x, y, 8 * j, r, at.hi - 1);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = 0.0f;
+      }
+      float top = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[e]));
+#pragma unroll
+      for (int o = 1; o < D / 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      // 2^e with top 2^e in [2^14, 2^15); queries that are zero or not finite are taken as they are
+      int e2 = 0;
+      if (top > 0.0f && top < INFINITY) e2 = max(-100, min(100, 14 - ilogbf(top)));
+      const float up = ldexpf(1.0f, e2);
+      float sum = 0.0f;
+      uint32_t w[4];
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        // coordinates p and p + 4 are the two halves of nibble p; odd nibbles come times 16
+        const __half2 hv = __floats2half2_rn(x[p] * up, x[p + 4] * up);
+        const float2 f = __half22float2(hv);
+        sum += f.x + f.y;
+        const __half2 hs = (p & 1) ? __hmul2(hv, __float2half2_rn(0.0625f)) : hv;
+        w[p] = *(const uint32_t*)&hs;
+      }
+#pragma unroll
+      for (int o = 1; o < D / 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (hh < HS) {
+        *(uint4*)(qop + hh * C::QROW + j * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+        if (j == 0) {
+          const float f = a.scale * 1.4426950408889634f;
+          s_q[hh][0] = f * ldexpf(1.0f, 24 - e2);
+          s_q[hh][1] = f * ldexpf(sum, -e2);
+        }
+      }
+    }
+    __syncthreads();
+    // lane (g, cc): column g of the query operand; in pairs, the odd columns are empty
+    const int qhead = PAIR ? g >> 1 : g;
+    const uint32_t qkeep = PAIR && (g & 1) ? 0u : 0xffffffffu;
+    const uint8_t* qsrc = qop + qhead * C::QROW + cc * 16;
+    uint32_t qf[C::QREG ? NC : 1][4];
+    if constexpr (C::QREG) {
+#pragma unroll
+      for (int j = 0; j < NC; ++j) {
+        const uint4 u = *(const uint4*)(qsrc + j * 64);
+        qf[j][0] = u.x & qkeep;
+        qf[j][1] = u.y & qkeep;
+        qf[j][2] = u.z & qkeep;
+        qf[j][3] = u.w & qkeep;
+      }
+    }
+    constexpr int NHL = PAIR ? 1 : 2;            // heads a lane scores: cc, or 2 cc and 2 cc + 1
+    float fq[NHL], fm[NHL], mref[NHL], lsum[NHL], msum[NHL];
+#pragma unroll
+    for (int i = 0; i < NHL; ++i) {
+      const int hh = PAIR ? cc : 2 * cc + i;
+      fq[i] = s_q[hh][0];
+      fm[i] = s_q[hh][1];
+      mref[i] = -INFINITY;
+      lsum[i] = msum[i] = 0.0f;
+    }
+    float sref = 0.0f, sinv = 0.0f;              // reference step, and kTop over it
+    float acc[D / 16][4];
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
+
+    for (; mine < seg_end; mine += W) {
+      const int tile = at.tile + (int)(mine - seg);
+      // the next copy goes into the stage that the tile before this one has left
+      {
+        int st = stage + C::NST - 1;
+        st = st >= C::NST ? st - C::NST : st;
+        __syncwarp();
+        if (!dead && ahead.left > 0) issue(st);
+        if (ahead.left > 0) {
+          ahead.advance(c, r, a, plan.unit, per_row, W);
+          look();
+        }
+      }
+      if (!dead && !sm100::mbar_wait(&bars[warp][stage], (phase >> stage) & 1u, a.flags)) dead = true;
+      dead = __any_sync(0xffffffffu, dead);
+      phase ^= 1u << stage;
+      const uint32_t sb = ring_u + stage * C::STAGE;
+      const uint8_t* sp = ring + stage * C::STAGE;
+      const uint32_t okm = dead ? 0u : oks[warp][stage];
+      stage = stage + 1 == C::NST ? 0 : stage + 1;
+      const int t0 = (at.lo / C::TT + tile) * C::TT;
+      const bool edge = okm != (1u << C::NB) - 1u || t0 < at.lo || t0 + C::TT > at.hi;
+      if (okm == 0) continue;
+      // ---- scores
+      float t[C::NB][2][NHL], vs[C::NB][2], vm[C::NB][2];
+#pragma unroll
+      for (int n = 0; n < C::NB; ++n) {
+        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < NC; j += 2) {
+          uint32_t w[4];
+          ldsm4(sb + n * blk_bytes(D) + (koff ^ (j << 4)), w);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            uint32_t b[4];
+            if constexpr (C::QREG) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) b[e] = qf[j + k][e];
+            } else {
+              const uint4 u = *(const uint4*)(qsrc + (j + k) * 64);
+              b[0] = u.x & qkeep;
+              b[1] = u.y & qkeep;
+              b[2] = u.z & qkeep;
+              b[3] = u.w & qkeep;
+            }
+            const uint32_t x = w[2 * k], y = w[2 * k + 1], xs = x >> 8, ys = y >> 8;
+            mma(s, x & 0x000f000fu, y & 0x000f000fu, x & 0x00f000f0u, y & 0x00f000f0u, b[0], b[1]);
+            mma(s, xs & 0x000f000fu, ys & 0x000f000fu, xs & 0x00f000f0u, ys & 0x00f000f0u, b[2], b[3]);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t kw = *(const uint32_t*)(sp + n * blk_bytes(D) + k_pairs(D) + (g + 8 * e) * 4);
+          const uint32_t vw = *(const uint32_t*)(sp + n * blk_bytes(D) + v_pairs(D) + (g + 8 * e) * 4);
+          const float ks = __uint_as_float(kw << 16), km = __uint_as_float(kw & 0xffff0000u);
+          vs[n][e] = __uint_as_float(vw << 16);
+          vm[n][e] = __uint_as_float(vw & 0xffff0000u);
+#pragma unroll
+          for (int i = 0; i < NHL; ++i) t[n][e][i] = fmaf(ks, s[2 * e + i] * fq[i], km * fm[i]);
+        }
+      }
+      if (edge) {
+#pragma unroll
+        for (int n = 0; n < C::NB; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int p = t0 + 16 * n + 8 * e + g;
+            if (p < at.lo || p >= at.hi || !((okm >> n) & 1u)) {
+              vs[n][e] = vm[n][e] = 0.0f;
+#pragma unroll
+              for (int i = 0; i < NHL; ++i) t[n][e][i] = -INFINITY;
+            }
+          }
+      }
+      // ---- the references
+      bool over = false;
+#pragma unroll
+      for (int n = 0; n < C::NB; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          over |= vs[n][e] > sref;
+#pragma unroll
+          for (int i = 0; i < NHL; ++i) over |= !(t[n][e][i] <= mref[i] + kSlack);
+        }
+      if (__any_sync(0xffffffffu, over)) {
+        float st = 0.0f;
+#pragma unroll
+        for (int n = 0; n < C::NB; ++n) st = fmaxf(st, fmaxf(vs[n][0], vs[n][1]));
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) st = fmaxf(st, __shfl_xor_sync(0xffffffffu, st, o));
+        float down = 1.0f;
+        if (st > sref) {
+          // the power of two at or above the step, kept where its reciprocal stays a float
+          const uint32_t u = (__float_as_uint(st) + 0x7fffffu) & 0x7f800000u;
+          const float ns = fminf(fmaxf(__uint_as_float(u), 0x1p-100f), 0x1p126f);
+          down = sref / ns;
+          sref = ns;
+          sinv = kTop / ns;
+        }
+#pragma unroll
+        for (int i = 0; i < NHL; ++i) {
+          float mx = -INFINITY;
+#pragma unroll
+          for (int n = 0; n < C::NB; ++n) mx = fmaxf(mx, fmaxf(t[n][0][i], t[n][1][i]));
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+          float f = 1.0f;
+          if (mx > mref[i]) {
+            f = ex2(mref[i] - mx);             // 0 the first time
+            mref[i] = mx;
+            lsum[i] *= f;
+            msum[i] *= f;
+          }
+          f *= down;
+#pragma unroll
+          for (int m = 0; m < D / 16; ++m) {
+            if constexpr (PAIR) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) acc[m][j] *= f;
+            } else {
+              acc[m][i] *= f;
+              acc[m][2 + i] *= f;
+            }
+          }
+        }
+      }
+      // ---- probabilities, and the values' product
+#pragma unroll
+      for (int n = 0; n < C::NB; ++n) {
+        uint32_t bh[2], bl[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float ps[2];
+#pragma unroll
+          for (int i = 0; i < NHL; ++i) {
+            const float base = mref[i] == -INFINITY ? 0.0f : mref[i];
+            const float p = ex2(t[n][e][i] - base);
+            lsum[i] += p;
+            msum[i] = fmaf(p, vm[n][e], msum[i]);
+            ps[i] = p * (vs[n][e] * sinv);
+          }
+          if constexpr (PAIR) {
+            const __half hi = __float2half_rn(ps[0]);
+            const __half lo = __float2half_rn(ps[0] - __half2float(hi));
+            const __half2 hl = __halves2half2(hi, lo);
+            bh[e] = movm(*(const uint32_t*)&hl);
+          } else {
+            const uint32_t hi = pack_h2(ps[0], ps[1]);
+            const float2 f = unpack_h2(hi);
+            bh[e] = movm(hi);
+            bl[e] = movm(pack_h2(ps[0] - f.x, ps[1] - f.y));
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < NC; j += 2) {
+          uint32_t w[4];
+          ldsm4t(sb + n * blk_bytes(D) + (voff ^ (j << 4)), w);
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            const uint32_t mask = (p & 1) ? 0x00f000f0u : 0x000f000fu;
+            const int sh = p < 2 ? 0 : 8;
+            const uint32_t a0 = (w[0] >> sh) & mask, a1 = (w[1] >> sh) & mask, a2 = (w[2] >> sh) & mask,
+                           a3 = (w[3] >> sh) & mask;
+            mma(acc[2 * j + p], a0, a1, a2, a3, bh[0], bh[1]);
+            if constexpr (!PAIR) mma(acc[2 * j + p], a0, a1, a2, a3, bl[0], bl[1]);
+          }
+        }
+      }
+    }
+
+    // ---- the segment's sums of the eight warps
+#pragma unroll
+    for (int i = 0; i < NHL; ++i) {
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) {
+        lsum[i] += __shfl_xor_sync(0xffffffffu, lsum[i], o);
+        msum[i] += __shfl_xor_sync(0xffffffffu, msum[i], o);
+      }
+      if (g == 0) {
+        float* ml = s_ml[warp][PAIR ? cc : 2 * cc + i];
+        ml[0] = mref[i];
+        ml[1] = lsum[i];
+        ml[2] = msum[i];
+      }
+    }
+    __syncthreads();
+    float fw[NHL];
+#pragma unroll
+    for (int i = 0; i < NHL; ++i) {
+      const int hh = PAIR ? cc : 2 * cc + i;
+      float top = -INFINITY;
+      for (int w = 0; w < W; ++w) top = fmaxf(top, s_ml[w][hh][0]);
+      fw[i] = mref[i] == -INFINITY ? (lsum[i] == 0.0f ? 0.0f : 1.0f) : ex2(mref[i] - top);
+      fw[i] *= 0x1p13f;                          // 2^24 of the codes over kTop; the reference step follows
+    }
+    const bool starts = at.tile == 0, ends = seg + (at.nt - at.tile) <= last;
+    float* slot = parts + ((int64_t)2 * blockIdx.x + (starts ? 1 : 0)) * part_floats(D);
+#pragma unroll
+    for (int jr = 0; jr < NC / 2; ++jr) {
+      // 64 coordinates a round: 64 jr + 4 g + p, and 32 further
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int i = 0; i < NHL; ++i) {
+          const int hh = PAIR ? cc : 2 * cc + i;
+          float4 o4;
+          float* o = (float*)&o4;
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            const float* x = acc[4 * jr + p];
+            const float v = PAIR ? x[2 * half] + x[2 * half + 1] : x[2 * half + i];
+            o[p] = v * fw[i] * sref * ((p & 1) ? 0.0625f : 1.0f);
+          }
+          *(float4*)(merge + (warp * HS + hh) * 64 + 32 * half + 4 * g) = o4;
+        }
+      __syncthreads();
+      for (int i = tid; i < HS * 64; i += 32 * W) {
+        const int hh = i >> 6, x = i & 63;
+        if (hh < nh) {
+          float top = -INFINITY, l = 0.0f, o = 0.0f;
+#pragma unroll
+          for (int w = 0; w < W; ++w) top = fmaxf(top, s_ml[w][hh][0]);
+#pragma unroll
+          for (int w = 0; w < W; ++w) {
+            const float* ml = s_ml[w][hh];
+            const float f = ml[0] == -INFINITY ? (ml[1] == 0.0f ? 0.0f : 1.0f) : ex2(ml[0] - top);
+            l = fmaf(f, ml[1], l);
+            o += fmaf(f, ml[2], merge[(w * HS + hh) * 64 + x]);
+          }
+          const int dim = 64 * jr + x;
+          if (starts && ends) {
+            const int64_t at_out = (int64_t)at.row * a.n_q + h0 + hh;
+            out[at_out * D + dim] = from_f<TO>(l == 0.0f ? 0.0f : o / l);
+            if (a.lse && dim == 0) a.lse[at_out] = l == 0.0f ? -INFINITY : (top + log2f(l)) * 0.69314718055994531f;
+          } else {
+            slot[hh * D + dim] = o;
+            if (dim == 0) {
+              slot[kMaxHeads * D + 2 * hh] = top;
+              slot[kMaxHeads * D + 2 * hh + 1] = l;
+            }
+          }
+        }
+      }
+      __syncthreads();
+    }
+    if (starts && !ends && tid == 0) {
+      const int64_t end = seg + at.nt;           // line position behind the pair
+      descs[blockIdx.x] = Desc{(int)((end - 1) / plan.quota) - (int)blockIdx.x + 1, at.row, at.hsub, 0};
+    }
+    // ---- the next pair
+    seg = seg_end;
+    if (seg < last) {
+      at.tile = 0;
+      if (++at.hsub == per_row) {
+        at.hsub = 0;
+        do {
+          ++at.row;
+          at.enter(c, r, a, plan.unit);
+        } while (at.nt == 0);
+      }
+    }
+  }
+}
+
+// Joins the partial sums of a pair that several blocks of k_decode4 share: block
+// (i, h) those of the pair that block i began, for its h-th head; a warp a partial.
+template <typename TO, int D>
+__global__ void __launch_bounds__(256)
+k_join4(const float* __restrict__ parts, const Desc* __restrict__ descs, TO* __restrict__ out, AttnArgs a, int nsub,
+        int hs) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Desc ds = descs[blockIdx.x];
+  if (ds.parts == 0) return;
+  const int kvh = ds.hsub / nsub, hh = blockIdx.y, h = kvh * a.group + (ds.hsub % nsub) * hs + hh;
+  if (hh >= hs || h >= (kvh + 1) * a.group) return;
+  __shared__ float s_m[8], s_l[8];
+  __shared__ float s_o[8][D];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float top = -INFINITY, l = 0.0f, o[D / 32];
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) o[i] = 0.0f;
+  for (int p = warp; p < ds.parts; p += 8) {
+    const float* s = parts + ((int64_t)2 * (blockIdx.x + p) + (p == 0 ? 1 : 0)) * part_floats(D);
+    const float m = s[kMaxHeads * D + 2 * hh], pl = s[kMaxHeads * D + 2 * hh + 1];
+    float x[D / 32];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) x[i] = s[hh * D + 32 * i + lane];
+    const float nt = fmaxf(top, m), base = nt == -INFINITY ? 0.0f : nt;
+    const float fa = top == -INFINITY ? (l == 0.0f ? 0.0f : 1.0f) : ex2(top - base);
+    const float fb = m == -INFINITY ? (pl == 0.0f ? 0.0f : 1.0f) : ex2(m - base);
+    l = l * fa + pl * fb;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) o[i] = o[i] * fa + x[i] * fb;
+    top = nt;
+  }
+  if (lane == 0) {
+    s_m[warp] = top;
+    s_l[warp] = l;
+  }
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) s_o[warp][32 * i + lane] = o[i];
+  __syncthreads();
+  const int x = threadIdx.x;
+  if (x >= D) return;
+  float all = -INFINITY, sum = 0.0f, v = 0.0f;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) all = fmaxf(all, s_m[w]);
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    const float f = s_m[w] == -INFINITY ? (s_l[w] == 0.0f ? 0.0f : 1.0f) : ex2(s_m[w] - all);
+    sum = fmaf(f, s_l[w], sum);
+    v = fmaf(f, s_o[w][x], v);
+  }
+  const int64_t at = (int64_t)ds.row * a.n_q + h;
+  out[at * D + x] = from_f<TO>(sum == 0.0f ? 0.0f : v / sum);
+  if (a.lse && x == 0) a.lse[at] = sum == 0.0f ? -INFINITY : (all + log2f(sum)) * 0.69314718055994531f;
+}
+
+}  // namespace dec
+}  // namespace kv4
+}  // namespace sq
