@@ -18,7 +18,7 @@ LIB = os.path.join(HERE, "libsq.so")
 SOURCES = ["api.cu", "kv4.cu", "codebook.cpp"]
 HEADERS = ["sq_common.cuh", "sm100.cuh", "calibrate.cuh", "codec.cuh", "blk_compress.cuh", "attention.cuh",
            "tc_compress.cuh", "fast_attn.cuh", "tc_decode.cuh", "decode_step.cuh", "kv4.cuh", "kv4_append.cuh",
-           "kv4_decode.cuh", "kv4_attn.cuh"]
+           "kv4_decode.cuh", "kv4_prefill.cuh"]
 
 NVCC_FLAGS = [
     "-std=c++17", "-O3", "-lineinfo",

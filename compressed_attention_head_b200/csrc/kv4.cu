@@ -7,8 +7,8 @@
 #include "sq_common.cuh"
 
 #include "kv4_append.cuh"
-#include "kv4_attn.cuh"
 #include "kv4_decode.cuh"
+#include "kv4_prefill.cuh"
 
 namespace sq {
 namespace kv4 {
@@ -123,23 +123,6 @@ sq_status attn_args_ok(const sq_kv4_cache* c, int n_q, const void* q, sq_dtype d
   return SQ_OK;
 }
 
-template <typename T, typename TO, int D>
-void launch_plain(const Pool& c, const RopeArgs& r, const void* q, void* out, const AttnArgs& a, cudaStream_t st) {
-  k_attn4_plain<T, TO, D><<<dim3((unsigned)a.n_tok, a.n_q), kPlainTile, 0, st>>>(c, r, (const T*)q, (TO*)out, a);
-}
-
-sq_status run_attn(const Pool& c, const RopeArgs& r, const void* q, sq_dtype dtype, void* out, sq_dtype out_dtype,
-                   const AttnArgs& a, cudaStream_t st) {
-#define SQ_CALL(T, DD)                                                                          \
-  if (out_dtype == SQ_F32) launch_plain<T, float, DD>(c, r, q, out, a, st);                     \
-  else if (out_dtype == SQ_F16) launch_plain<T, __half, DD>(c, r, q, out, a, st);               \
-  else launch_plain<T, __nv_bfloat16, DD>(c, r, q, out, a, st)
-  if (dtype == SQ_F16) { SQ_KV4_D(__half, SQ_CALL) }
-  else { SQ_KV4_D(__nv_bfloat16, SQ_CALL) }
-#undef SQ_CALL
-  return cuda_ok(cudaGetLastError());
-}
-
 // ---------------------------------------------------------------- single tokens
 int sms() {
   int dev = 0, n = 0;
@@ -233,6 +216,62 @@ sq_status run_decode(const Pool& c, const RopeArgs& r, const void* q, sq_dtype d
   return cuda_ok(e);
 }
 
+// ---------------------------------------------------------------- chunks
+pre::Shape prefill_shape(int batch, int n_kv, int group, int d, int64_t n_tok) {
+  pre::Shape s;
+  s.nsub = (group + pre::M - 1) / pre::M;
+  s.gt = (group + s.nsub - 1) / s.nsub;
+  s.tpm = pre::M / s.gt;
+  s.tpu = s.tpm * (d == 256 ? 1 : 2);
+  s.sms = sms();
+  // Units longer than an even share of the keys are cut, so fewer than `sms` are, into fewer than 2 `sms` pieces.
+  s.cap_slots = 2 * s.sms;
+  const int64_t units = (int64_t)n_kv * s.nsub * ((n_tok + s.tpu - 1) / s.tpu + batch) + s.cap_slots;
+  s.cap_units = units > 0x7fffffff ? 0 : (int)units;
+  return s;
+}
+
+constexpr size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+size_t prefill_layout(const pre::Shape& s, int d, uint8_t* ws, pre::Plan* p) {
+  const size_t units = 256, joins = units + up256((size_t)s.cap_units * sizeof(pre::Unit));
+  const size_t parts = joins + up256((size_t)s.sms * sizeof(pre::Join));
+  const size_t rows = (size_t)s.cap_slots * pre::part_rows(d == 256 ? 1 : 2);
+  if (p) *p = pre::Plan{(pre::Head*)ws, (pre::Unit*)(ws + units), (pre::Join*)(ws + joins), (float*)(ws + parts)};
+  return parts + rows * (d + 2) * sizeof(float);
+}
+
+template <typename T, typename TO, int D>
+cudaError_t launch_prefill(const Pool& c, const RopeArgs& r, const void* q, void* out, const AttnArgs& a, const pre::Shape& s,
+                           const pre::Plan& p, cudaStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  auto kernel = pre::k_prefill4<T, TO, D>;
+  constexpr int smem = pre::Cfg<D>::TOTAL;
+  cudaError_t e = allow_smem(kernel, smem, &done);
+  if (e != cudaSuccess) return e;
+  pre::k_plan4<<<1, pre::kPlanThreads, 0, st>>>(c, r, a, s, p);
+  e = cudaGetLastError();
+  if (e == cudaSuccess)
+    e = launch_overlapped(kernel, s.cap_units, pre::kThreads, smem, st, c, r, (const T*)q, (TO*)out, a, s, p);
+  if (e == cudaSuccess) e = launch_overlapped(pre::k_prejoin4<TO, D>, dim3(s.sms, 8), 256, 0, st, p, (TO*)out, a, s);
+  return e;
+}
+
+sq_status run_prefill(const Pool& c, const RopeArgs& r, const void* q, sq_dtype dtype, void* out, sq_dtype out_dtype,
+                      const AttnArgs& a, const pre::Shape& s, uint8_t* ws, cudaStream_t st) {
+  pre::Plan p;
+  prefill_layout(s, c.d, ws, &p);
+  cudaError_t e = cudaSuccess;
+#define SQ_CALL(T, DD)                                                                           \
+  if (out_dtype == SQ_F32) e = launch_prefill<T, float, DD>(c, r, q, out, a, s, p, st);          \
+  else if (out_dtype == SQ_F16) e = launch_prefill<T, __half, DD>(c, r, q, out, a, s, p, st);    \
+  else e = launch_prefill<T, __nv_bfloat16, DD>(c, r, q, out, a, s, p, st)
+  if (dtype == SQ_F16) { SQ_KV4_D(__half, SQ_CALL) }
+  else { SQ_KV4_D(__nv_bfloat16, SQ_CALL) }
+#undef SQ_CALL
+  return cuda_ok(e);
+}
+
 float scale_of(float scale, int d) { return scale > 0.0f ? scale : 1.0f / sqrtf((float)d); }
 
 }  // namespace
@@ -320,7 +359,8 @@ size_t sq_kv4_attn_prefill_workspace(int batch, int n_q_heads, int n_kv_heads, i
   if (batch < 1 || n_q_heads < 1 || n_kv_heads < 1 || n_q_heads % n_kv_heads != 0 || !head_dim_ok(d) || n_tok < 1 ||
       n_tok > 0x7fffffff)
     return 0;
-  return 256;
+  const pre::Shape s = prefill_shape(batch, n_kv_heads, n_q_heads / n_kv_heads, d, n_tok);
+  return s.cap_units ? prefill_layout(s, d, nullptr, nullptr) : 0;
 }
 
 sq_status sq_kv4_attn_prefill(const sq_kv4_cache* cache, const int32_t* d_cu, const int32_t* d_start, int n_q_heads,
@@ -338,7 +378,9 @@ sq_status sq_kv4_attn_prefill(const sq_kv4_cache* cache, const int32_t* d_cu, co
     return SQ_ERR_WORKSPACE;
   const AttnArgs a{d_cu, d_start, 0, n_tok, 0x7fffffff, q_stride_tok, q_stride_head, n_q_heads,
                    n_q_heads / cache->n_kv_heads, window, scale_of(scale, cache->d), lse_out, d_flags};
-  return run_attn(pool_of(cache), rope_of(rope), q, dtype, out, out_dtype, a, (cudaStream_t)stream);
+  const pre::Shape sh = prefill_shape(cache->batch, cache->n_kv_heads, a.group, cache->d, n_tok);
+  if (!sh.cap_units) return SQ_ERR_ARG;
+  return run_prefill(pool_of(cache), rope_of(rope), q, dtype, out, out_dtype, a, sh, (uint8_t*)ws, (cudaStream_t)stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,844 @@
+// Causal attention of chunks of queries over the paged 4-bit cache (tcgen05).
+//
+// Mathematics. A key is x^ = m + s c = (m + 8 s) + s (c - 8). s has 8 significant
+// bits and c - 8 three, or is a power of two, so s (c - 8) is an fp16 number exactly
+// once a power of two a tile puts s in range: the tile is unpacked into fp16 without
+// a rounding. The rest, sum(q) (m + 8 s), is one more step of 16 along the product's
+// k: three fp16 parts of sum(q) against m and against 8 s, both exact. A score is
+// therefore what the cache holds, to float's roundings. For the values s (c - 8) is
+// unpacked in the same way against the rounded probabilities, and sum p (m + 8 s) is
+// kept in float beside the running sum: only the part that varies within a vector
+// meets a probability of 11 bits.
+//
+// Split. A block takes one KV head, 128 / group tokens with their query heads as the
+// rows of one accumulator (two of them up to head_dim 128) and 128 keys at a time.
+// Four warps a row tile hold the softmax, a thread a row; four unpack keys and
+// values; one thread issues the products. Scores and probabilities share tensor
+// memory, probabilities are the A operand from there. With two row tiles one's
+// softmax runs beside the other's products; with one (short chunks, head_dim 256)
+// the scores of the next keys are formed meanwhile.
+//
+// The maximum a row refers to is raised, and its sums scaled, only when a score
+// passes it by 2^4. Pieces: a small kernel first lists the units, longest first, and
+// cuts those that would outlast an even share of all the work; the cut ones leave
+// partial sums that a last kernel joins in order.
+#pragma once
+
+#include "kv4_decode.cuh"
+
+namespace sq {
+namespace kv4 {
+namespace pre {
+
+constexpr int KT = 128;                       // keys of a tile
+constexpr int M = 128;                        // rows of an accumulator
+constexpr int kSoft = 128;                    // threads of a row tile's softmax
+constexpr int kThreads = 416;                 // 2 x 4 softmax warps, 4 unpacking, 1 issuing
+constexpr int kInfo = 4;                      // tiles whose factors are kept
+constexpr float kSlack = 4.0f;                // log2 of what a probability may exceed 1 by
+constexpr float kUp = 11.0f;                  // log2 of the probabilities' scale: 2^15 at most with the slack
+
+template <int D> struct Cfg {
+  static constexpr int NS = D == 256 ? 1 : 2;          // row tiles of a block
+  static constexpr int NKV = D == 256 ? 1 : 2;         // stages of unpacked keys and values
+  static constexpr int MAIN = (D / 64) * 16384;        // 128 rows x D fp16, 64 coordinates a slab
+  static constexpr int OP = MAIN + 4096;               // and the step that carries the offsets
+  static constexpr int Q = 0;
+  static constexpr int K = Q + NS * OP;
+  static constexpr int V = K + NKV * OP;
+  static constexpr int MEAN = V + NKV * MAIN;
+  static constexpr int USED = MEAN + kInfo * KT * 4;
+  static constexpr int TOTAL = (USED > 118784 ? USED : 118784) + 1024;   // one block an SM: it takes all tensor memory
+};
+
+// One piece of work.
+struct Unit {
+  int64_t pos;         // position of the first token
+  int row, hs;         // sequence, KV head x pass
+  int tok, n;          // first token of the call, tokens
+  int t0, nt;          // key tiles
+  int slot;            // of the partial sums, -1: the whole of it, -2: nothing to do
+  int pad;
+};
+struct Join { int unit, slot, parts, pad; };
+struct Head { int units, joins, slots, pad; };
+
+struct Shape {
+  int gt, nsub, tpm, tpu;      // heads of a pass, passes, tokens of a row tile, of a unit
+  int cap_units, cap_slots, sms;
+};
+
+struct Plan {
+  Head* head;
+  Unit* units;
+  Join* joins;
+  float* parts;
+};
+
+__host__ __device__ inline size_t part_rows(int ns) { return (size_t)ns * M; }
+
+// First and last key of a unit's tokens, empty when hi < lo.
+__device__ __forceinline__ void unit_keys(const Pool& c, const RopeArgs& r, const AttnArgs& a, int64_t pos, int n,
+                                          int64_t* lo, int64_t* hi) {
+  const int64_t cap = c.cap();
+  const int64_t first = min(pos, cap - 1);
+  int64_t last = min(pos + n - 1, cap - 1);
+  if (r.table) last = min(last, r.n_pos - 1);
+  *hi = last;
+  *lo = a.window > 0 && first - a.window + 1 > 0 ? first - a.window + 1 : 0;
+}
+
+constexpr int kPlanThreads = 512;
+
+__global__ void __launch_bounds__(kPlanThreads)
+k_plan4(Pool c, RopeArgs r, AttnArgs a, Shape s, Plan p) {
+  __shared__ unsigned long long s_tiles;
+  __shared__ int s_longest, s_hist[64], s_at[64], s_slots, s_joins;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int heads = c.n_kv * s.nsub;
+  if (tid < 64) s_hist[tid] = 0;
+  if (tid == 0) {
+    s_tiles = 0;
+    s_longest = s_slots = s_joins = 0;
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __syncthreads();
+  int pass_cut = 0x7fffffff, longest = 1;
+  // three passes over the units: their lengths, the lengths' classes, the list
+  for (int pass = 0; pass < 3; ++pass) {
+    unsigned long long tiles = 0;
+    int most = 0;
+    for (int b = warp; b < c.batch; b += kPlanThreads / 32) {
+      const int64_t t_lo = max(0, __ldg(a.cu + b)), t_hi = min((int64_t)__ldg(a.cu + b + 1), a.n_tok);
+      if (t_hi <= t_lo) continue;
+      const int64_t start = (int64_t)__ldg(a.start + b) + (t_lo - __ldg(a.cu + b));
+      const int64_t n_units = (t_hi - t_lo + s.tpu - 1) / s.tpu;
+      if (pass == 0 && lane == 0 && a.flags) {
+        const int64_t last = start + (t_hi - t_lo) - 1;
+        uint32_t bits = 0;
+        if (last >= c.cap() || start < -1) bits |= SQ_FLAG_SEQLEN;
+        if (r.table && min(last, c.cap() - 1) >= r.n_pos) bits |= SQ_FLAG_ROPE;
+        if (bits) atomicOr(a.flags, bits);
+      }
+      for (int64_t u = lane; u < n_units; u += 32) {
+        Unit w;
+        w.pos = start + u * s.tpu;
+        w.row = b;
+        w.tok = (int)(t_lo + u * s.tpu);
+        w.n = (int)min((int64_t)s.tpu, t_hi - w.tok);
+        int64_t lo, hi;
+        unit_keys(c, r, a, w.pos, w.n, &lo, &hi);
+        const int len = hi < lo ? 0 : (int)(hi / KT - lo / KT) + 1;
+        if (pass == 0) {
+          tiles += (unsigned long long)len * heads;
+          most = max(most, len);
+          continue;
+        }
+        const int parts = len > pass_cut ? (len + pass_cut - 1) / pass_cut : 1;
+        const int piece = (len + parts - 1) / parts;
+        const int cls = 63 - (int)((int64_t)piece * 63 / longest);
+        if (pass == 1) {
+          atomicAdd(&s_hist[cls], parts * heads);
+          continue;
+        }
+        int at = atomicAdd(&s_at[cls], parts * heads);
+        for (int h = 0; h < heads; ++h) {
+          int slot = -1, join = 0;
+          if (parts > 1) {
+            slot = atomicAdd(&s_slots, parts);
+            if (slot + parts <= s.cap_slots) {
+              join = atomicAdd(&s_joins, 1);
+              p.joins[join] = Join{at, slot, parts, 0};
+            } else {
+              slot = -2;
+            }
+          }
+          w.hs = h;
+          w.pad = 0;
+          int t = (int)(lo / KT);
+          for (int i = 0; i < parts; ++i, ++at) {
+            w.t0 = t;
+            w.nt = len / parts + (i < len % parts ? 1 : 0);
+            w.slot = slot < 0 ? slot : slot + i;
+            t += w.nt;
+            if (at < s.cap_units) p.units[at] = w;
+          }
+        }
+      }
+    }
+    if (pass == 0) {
+      atomicAdd(&s_tiles, tiles);
+      atomicMax(&s_longest, most);
+      __syncthreads();
+      // An even share of the work; a unit is cut when it is longer than that by more than a quarter
+      // (below that the cut's own cost, a prologue and partial sums of every row, is more).
+      const int share = max(4, (int)((s_tiles + s.sms - 1) / s.sms));
+      longest = max(1, s_longest);
+      if (longest > share + share / 4) {
+        pass_cut = share;
+        longest = share;
+      }
+    } else if (pass == 1) {
+      __syncthreads();
+      if (tid == 0) {
+        int at = 0;
+        for (int i = 0; i < 64; ++i) {
+          s_at[i] = at;
+          at += s_hist[i];
+        }
+        p.head->units = min(at, s.cap_units);
+      }
+      __syncthreads();
+    }
+  }
+  __syncthreads();
+  if (tid == 0) p.head->joins = s_joins;
+}
+
+// ---------------------------------------------------------------- tensor memory, packed floats
+__device__ __forceinline__ void ld32(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+// The registers of a load may be used behind this.
+__device__ __forceinline__ void ld_wait(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])::"memory");
+}
+__device__ __forceinline__ void st16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]) : "memory");
+}
+typedef unsigned long long f2;                 // two floats
+__device__ __forceinline__ f2 f2_of(uint32_t lo, uint32_t hi) { return (f2)lo | ((f2)hi << 32); }
+__device__ __forceinline__ f2 f2_of(float lo, float hi) { return f2_of(__float_as_uint(lo), __float_as_uint(hi)); }
+__device__ __forceinline__ float f2_lo(f2 x) { return __uint_as_float((uint32_t)x); }
+__device__ __forceinline__ float f2_hi(f2 x) { return __uint_as_float((uint32_t)(x >> 32)); }
+__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c) {
+  f2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ f2 f2_add(f2 a, f2 b) {
+  f2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// The power of two at or above x >= 0, within the floats whose reciprocals are normal too.
+__device__ __forceinline__ float pow2_up(float x) {
+  const uint32_t u = (__float_as_uint(x) + 0x7fffffu) & 0x7f800000u;
+  return fminf(fmaxf(__uint_as_float(u), 0x1p-100f), 0x1p127f);
+}
+
+// Descriptors of an operand in shared memory: keys and queries (coordinates run
+// along k, 64 of a row's in a 128-byte swizzled line), their last step (no swizzle,
+// 16-byte rows of 8 by 8 cores), values (coordinates run along n, tokens along k).
+__device__ __forceinline__ uint64_t desc_of(uint32_t addr, uint32_t lead, uint32_t stride, uint32_t swizzle) {
+  return (uint64_t)((addr >> 4) & 0x3fffu) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(stride >> 4) << 32 |
+         (uint64_t)1u << 46 | (uint64_t)swizzle << 61;
+}
+
+// Eight codes of a word, centred and scaled: 16 bytes in the order 0 4 1 5 2 6 3 7,
+// which the queries follow for the keys and the epilogue undoes for the values. A
+// code or'ed into the low bits of fp16 1024 is 1024 + c; both operations are exact.
+__device__ __forceinline__ uint4 unpack_codes(uint32_t w, __half2 s, __half2 s16) {
+  const uint32_t x = w >> 8;
+  const uint32_t u0 = (w & 0x000f000fu) | 0x64006400u, u1 = (w & 0x00f000f0u) | 0x64006400u;
+  const uint32_t u2 = (x & 0x000f000fu) | 0x64006400u, u3 = (x & 0x00f000f0u) | 0x64006400u;
+  const __half2 lo = __float2half2_rn(-1032.0f), hi = __float2half2_rn(-1152.0f);
+  const __half2 r0 = __hmul2(__hadd2(*(const __half2*)&u0, lo), s);
+  const __half2 r1 = __hmul2(__hadd2(*(const __half2*)&u1, hi), s16);
+  const __half2 r2 = __hmul2(__hadd2(*(const __half2*)&u2, lo), s);
+  const __half2 r3 = __hmul2(__hadd2(*(const __half2*)&u3, hi), s16);
+  return make_uint4(*(const uint32_t*)&r0, *(const uint32_t*)&r1, *(const uint32_t*)&r2, *(const uint32_t*)&r3);
+}
+
+// What the softmax needs to know of a tile of keys.
+struct Info {
+  float kf;              // score factor
+  float vref;            // reference step of the values so far
+  uint32_t ok[4];        // keys that exist
+};
+
+template <typename T, typename TO, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+k_prefill4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, AttnArgs a, Shape sh, Plan plan) {
+  using C = Cfg<D>;
+  constexpr int NS = C::NS, NKV = C::NKV, TPR = D / 8, CH = D / 32;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t b_q, b_fin, b_s[2], b_p[2], b_o[NS], b_kf[NKV], b_ke[NKV], b_vf[NKV], b_ve[NKV], b_i[kInfo];
+  __shared__ uint32_t s_tmem;
+  __shared__ Info s_info[kInfo];
+  __shared__ float s_fq[NS][M];
+  __shared__ uint32_t s_red[2][4][2];
+  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if ((int)blockIdx.x >= plan.head->units) return;
+  const Unit u = plan.units[blockIdx.x];
+  if (u.slot == -2) return;
+  const int ns = u.n > sh.tpm ? NS : 1, nt = u.nt;
+  if (warp == 12) sm100::tmem_alloc(&s_tmem, 512);
+  if (tid == 0) {
+    sm100::mbar_init(&b_q, ns * kSoft);
+    sm100::mbar_init(&b_fin, 1);
+    for (int i = 0; i < 2; ++i) {
+      sm100::mbar_init(&b_s[i], 1);
+      sm100::mbar_init(&b_p[i], kSoft);
+    }
+    for (int i = 0; i < NS; ++i) sm100::mbar_init(&b_o[i], 1);
+    for (int i = 0; i < NKV; ++i) {
+      sm100::mbar_init(&b_kf[i], 128);
+      sm100::mbar_init(&b_ke[i], 1);
+      sm100::mbar_init(&b_vf[i], 128);
+      sm100::mbar_init(&b_ve[i], 1);
+    }
+    for (int i = 0; i < kInfo; ++i) sm100::mbar_init(&b_i[i], 128);
+    sm100::fence_mbar_init();
+  }
+  sm100::tc_fence_before();
+  __syncthreads();
+  sm100::tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  const int64_t cap = c.cap();
+  const int kvh = u.hs / sh.nsub, h0 = kvh * a.group + (u.hs % sh.nsub) * sh.gt;
+  const int nh = min(sh.gt, (kvh + 1) * a.group - h0);
+
+  if (warp < 8) {
+    // ------------------------------------------------------------ queries, softmax, outputs
+    const int i = warp >> 2, wt = tid & 127;
+    if (i < ns) {
+      uint8_t* qop = smem + C::Q + i * C::OP;
+      constexpr int RP = kSoft / TPR, BATCH = 4;
+      const int j = wt % TPR;
+      for (int r0 = 0; r0 < M; r0 += RP * BATCH) {
+        Vec8<T> own[BATCH], part[BATCH];
+        int64_t pos[BATCH];
+        bool has[BATCH];
+        const int pi = partner(8 * j, r);
+#pragma unroll
+        for (int n = 0; n < BATCH; ++n) {
+          const int row = r0 + n * RP + wt / TPR, ti = i * sh.tpm + row / sh.gt, hh = row % sh.gt;
+          pos[n] = min(u.pos + ti, cap - 1);
+          has[n] = row < sh.tpm * sh.gt && ti < u.n && hh < nh && pos[n] >= 0 && !(r.table && pos[n] >= r.n_pos);
+          if (has[n]) {
+            const T* x = q + (int64_t)(u.tok + ti) * a.qs_tok + (int64_t)(h0 + hh) * a.qs_head;
+            own[n] = load8<T>(x + 8 * j);
+            if (r.table && pi != 8 * j) part[n] = load8<T>(x + pi);
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < BATCH; ++n) {
+          const int row = r0 + n * RP + wt / TPR;
+          float x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = 0.0f;
+          if (has[n]) {
+            unpack8<T>(own[n], x);
+            if (r.table) {
+              float y[8];
+              if (pi != 8 * j) unpack8<T>(part[n], y);
+              rotate8<T>(x, y, 8 * j, r, pos[n]);
+            }
+          }
+          float top = 0.0f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[e]));
+#pragma unroll
+          for (int o = 1; o < TPR; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          // 2^e with top 2^e in [2^6, 2^7): the sum over a head stays below 2^15
+          int e2 = 0;
+          if (top > 0.0f && top < INFINITY) e2 = max(-100, min(100, 6 - ilogbf(top)));
+          const float up = ldexpf(1.0f, e2);
+          float sum = 0.0f;
+          uint32_t w[4];
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            const __half2 hv = __floats2half2_rn(x[p] * up, x[p + 4] * up);
+            const float2 f = __half22float2(hv);
+            sum += f.x + f.y;
+            w[p] = *(const uint32_t*)&hv;
+          }
+#pragma unroll
+          for (int o = 1; o < TPR; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          *(uint4*)(qop + (j >> 3) * 16384 + row * 128 + (((j & 7) ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+          if (j == 0) {
+            const __half s0 = __float2half_rn(sum);
+            const float d1 = sum - __half2float(s0);
+            const __half s1 = __float2half_rn(d1), s2 = __float2half_rn(d1 - __half2float(s1));
+            const __half2 a0 = __halves2half2(s0, s1), a1 = __halves2half2(s2, s0), a2 = __halves2half2(s1, s2);
+            uint8_t* ext = qop + C::MAIN + (row >> 3) * 256 + (row & 7) * 16;
+            *(uint4*)ext = make_uint4(*(const uint32_t*)&a0, *(const uint32_t*)&a1, *(const uint32_t*)&a2, 0u);
+            *(uint4*)(ext + 128) = make_uint4(0u, 0u, 0u, 0u);
+            s_fq[i][row] = a.scale * 1.4426950408889634f * ldexpf(1.0f, -e2);
+          }
+        }
+      }
+      sm100::fence_async_smem();
+      sm100::mbar_arrive(&b_q);
+      sm100::named_bar(1 + i, kSoft);
+
+      const int ti = i * sh.tpm + wt / sh.gt, hh = wt % sh.gt;
+      const bool is_row = wt < sh.tpm * sh.gt && ti < u.n && hh < nh;
+      // keys [lo, hi] of the row; rows that are none take any, so that they ask for no masks
+      int lo = 0, hi = 0x7fffffff;
+      if (is_row) {
+        const int64_t p = min(u.pos + ti, cap - 1);
+        hi = p < 0 || (r.table && p >= r.n_pos) ? -1 : (int)p;
+        lo = a.window > 0 && p - a.window + 1 > 0 ? (int)(p - a.window + 1) : 0;
+      }
+      const int w_lo = __reduce_max_sync(0xffffffffu, lo), w_hi = __reduce_min_sync(0xffffffffu, hi);
+      const float fq = s_fq[i][wt];
+      const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+      const uint32_t t_o = tmem + lanes + 256 + i * D;
+      float mref = -INFINITY, vref = 0.0f;
+      f2 lsum = 0, msum = 0;
+      bool dead = false;
+      for (int k = 0; k < nt && !dead; ++k) {
+        const int sl = ns == 2 ? i : (k & 1);
+        const uint32_t t_s = tmem + lanes + 128 * sl;
+        const int ring = k % kInfo;
+        dead = !sm100::mbar_wait(&b_i[ring], (k / kInfo) & 1, a.flags);
+        if (!dead) dead = !sm100::mbar_wait(&b_s[sl], ns == 2 ? (k & 1) : ((k >> 1) & 1), a.flags);
+        dead = __any_sync(0xffffffffu, dead);
+        if (dead) break;
+        sm100::tc_fence_after();
+        const Info& in = s_info[ring];
+        const int key0 = (u.t0 + k) * KT;
+        const bool edge = (in.ok[0] & in.ok[1] & in.ok[2] & in.ok[3]) != 0xffffffffu || key0 < w_lo || key0 + KT - 1 > w_hi;
+        const float fk = fq * in.kf;
+        const float* mean = (const float*)(smem + C::MEAN) + ring * KT;
+        // ---- the largest score
+        float mx = -INFINITY;
+        uint32_t s[2][32];
+        // mask bits of 32 keys of this row
+        auto keep = [&](int ch) {
+          const int from = key0 + 32 * ch;
+          const int x = lo - from, y = hi - from;                        // keys x .. y of the 32
+          uint32_t m = in.ok[ch];
+          m &= x <= 0 ? 0xffffffffu : (x > 31 ? 0u : 0xffffffffu << x);
+          m &= y >= 31 ? 0xffffffffu : (y < 0 ? 0u : 0xffffffffu >> (31 - y));
+          return m;
+        };
+        ld32(t_s, s[0]);
+#pragma unroll
+        for (int ch = 0; ch < 4; ++ch) {
+          ld_wait(s[ch & 1]);
+          if (ch < 3) ld32(t_s + 32 * (ch + 1), s[(ch + 1) & 1]);
+          uint32_t* x = s[ch & 1];
+          if (edge) {
+            const uint32_t m = keep(ch);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if ((m >> e) & 1u) mx = fmaxf(mx, __uint_as_float(x[e]));
+          } else {
+            float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              m0 = fmaxf(m0, fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 1])));
+              m1 = fmaxf(m1, fmaxf(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])));
+            }
+            mx = fmaxf(mx, fmaxf(m0, m1));
+          }
+        }
+        const float top = mx * fk;
+        const float nv = in.vref;
+        if (__any_sync(0xffffffffu, !(top <= mref + kSlack) || nv != vref)) {
+          float f = 1.0f;
+          if (top > mref) {
+            f = dec::ex2(mref - top);            // 0 the first time
+            mref = top;
+          }
+          const f2 ff = f2_of(f, f);
+          lsum = f2_fma(lsum, ff, 0ull);
+          msum = f2_fma(msum, ff, 0ull);
+          if (k > 0) {
+            const float fo = f * (vref / nv);
+            dead = !sm100::mbar_wait(&b_o[i], (k - 1) & 1, a.flags);
+            dead = __any_sync(0xffffffffu, dead);
+            if (dead) break;
+            sm100::tc_fence_after();
+            const f2 fo2 = f2_of(fo, fo);
+#pragma unroll 1
+            for (int ch = 0; ch < D / 32; ++ch) {
+              uint32_t* x = s[1];
+              ld32(t_o + 32 * ch, x);
+              ld_wait(x);
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                const f2 y = f2_fma(f2_of(x[e], x[e + 1]), fo2, 0ull);
+                x[e] = (uint32_t)y;
+                x[e + 1] = (uint32_t)(y >> 32);
+              }
+              st16(t_o + 32 * ch, x);
+              st16(t_o + 32 * ch + 16, x + 16);
+            }
+            sm100::tmem_wait_st();
+          }
+          vref = nv;
+        }
+        // ---- probabilities
+        ld32(t_s, s[0]);
+        const float base = (mref == -INFINITY ? 0.0f : mref) - kUp;
+        const f2 fk2 = f2_of(fk, fk), nb2 = f2_of(-base, -base);
+#pragma unroll
+        for (int ch = 0; ch < 4; ++ch) {
+          ld_wait(s[ch & 1]);
+          if (ch < 3) ld32(t_s + 32 * (ch + 1), s[(ch + 1) & 1]);
+          uint32_t* x = s[ch & 1];
+          uint32_t pk[16];
+          const uint32_t m = edge ? keep(ch) : 0xffffffffu;
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 mu = *(const float4*)(mean + 32 * ch + e);
+            const float mv[4] = {mu.x, mu.y, mu.z, mu.w};
+#pragma unroll
+            for (int h = 0; h < 4; h += 2) {
+              const f2 t = f2_fma(f2_of(x[e + h], x[e + h + 1]), fk2, nb2);
+              float t0 = f2_lo(t), t1 = f2_hi(t), m0 = mv[h], m1 = mv[h + 1];
+              if (edge) {
+                const bool k0 = (m >> (e + h)) & 1u, k1 = (m >> (e + h + 1)) & 1u;
+                t0 = k0 ? t0 : -INFINITY;
+                t1 = k1 ? t1 : -INFINITY;
+                m0 = k0 ? m0 : 0.0f;
+                m1 = k1 ? m1 : 0.0f;
+              }
+              const float p0 = dec::ex2(t0), p1 = dec::ex2(t1);
+              const f2 p = f2_of(p0, p1);
+              lsum = f2_add(lsum, p);
+              msum = f2_fma(p, f2_of(m0, m1), msum);
+              pk[(e + h) / 2] = dec::pack_h2(p0, p1);
+            }
+          }
+          st16(t_s + 16 * ch, pk);
+        }
+        sm100::tmem_wait_st();
+        sm100::tc_fence_before();
+        sm100::mbar_arrive(&b_p[sl]);
+      }
+      // ---- outputs
+      if (nt > 0 && !dead) dead = !sm100::mbar_wait(&b_o[i], (nt - 1) & 1, a.flags);
+      dead = __any_sync(0xffffffffu, dead);
+      if (!dead) {
+        sm100::tc_fence_after();
+        const float l = f2_lo(lsum) + f2_hi(lsum), mv = f2_lo(msum) + f2_hi(msum);
+        const float vf = vref * 0x1p-12f;
+        const bool whole = u.slot < 0;
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const int64_t at = (int64_t)(u.tok + ti) * a.n_q + h0 + hh;
+        const int64_t pr = whole ? 0 : (int64_t)u.slot * part_rows(NS) + i * M + wt;
+        float* po = plan.parts + pr * D;
+#pragma unroll 1
+        for (int ch = 0; ch < D / 32; ++ch) {
+          uint32_t x[32];
+          if (nt > 0) {
+            ld32(t_o + 32 * ch, x);
+            ld_wait(x);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e] = 0u;
+          }
+          if (is_row) {
+          float o[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const int to = (e & ~7) + ((e & 1) << 2) + ((e & 7) >> 1);   // the codes' order undone
+            o[to] = fmaf(__uint_as_float(x[e]), vf, mv);
+          }
+          if (whole) {
+            TO y[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) y[e] = from_f<TO>(l == 0.0f ? 0.0f : o[e] * inv);
+#pragma unroll
+            for (int e = 0; e < 2 * (int)sizeof(TO); ++e)
+              *(uint4*)((uint8_t*)(out + at * D + 32 * ch) + 16 * e) = *(const uint4*)((const uint8_t*)y + 16 * e);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) *(float4*)(po + 32 * ch + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          }
+          }
+          __syncwarp();
+        }
+        if (is_row) {
+          if (whole) {
+            if (a.lse) a.lse[at] = l == 0.0f ? -INFINITY : (mref + (log2f(l) - kUp)) * 0.69314718055994531f;
+          } else {
+            float* ml = plan.parts + (size_t)sh.cap_slots * part_rows(NS) * D + pr * 2;
+            ml[0] = mref;
+            ml[1] = l;
+          }
+        }
+      }
+    }
+  } else if (warp < 12) {
+    // ------------------------------------------------------------ unpacking: a thread a key
+    const int dt = tid - 256, uw = warp - 8;
+    int64_t ulo, uhi;
+    unit_keys(c, r, a, u.pos, u.n, &ulo, &uhi);
+    const int64_t page_bytes = ((int64_t)c.n_kv << (c.page_shift - 4)) * blk_bytes(D);
+    const int64_t head_off = ((int64_t)kvh << (c.page_shift - 4)) * blk_bytes(D);
+    const int in_page = (1 << c.page_shift) - 1;
+    const int t16 = dt & 15, sw = swz(t16, D);
+    // page numbers two tiles ahead, codes one tile ahead
+    auto page_of = [&](int k) {
+      const int64_t t = (int64_t)(u.t0 + k) * KT + dt;
+      if (k >= nt || t < ulo || t > uhi) return -2;
+      const int pg = __ldg(c.table + u.row * c.table_stride + (t >> c.page_shift));
+      if (pg < 0 || pg >= c.n_pages) {
+        raise(a.flags, SQ_FLAG_PAGE);
+        return -2;
+      }
+      return pg;
+    };
+    auto block_of = [&](int k, int pg) {
+      const int t = ((u.t0 + k) * KT + dt) & in_page;
+      return c.pages + pg * page_bytes + head_off + (int64_t)(t >> 4) * blk_bytes(D);
+    };
+    uint4 kc[CH], vc[CH];
+    uint32_t kw = 0, vw = 0;
+    int pg = page_of(0), pg_v = pg, pg_next;
+    auto load_k = [&](int k, int page) {
+      kw = vw = 0;
+      if (page >= 0) {
+        const uint8_t* blk = block_of(k, page);
+        kw = __ldg((const uint32_t*)(blk + k_pairs(D) + 4 * t16));
+        vw = __ldg((const uint32_t*)(blk + v_pairs(D) + 4 * t16));
+#pragma unroll
+        for (int p = 0; p < CH; ++p) kc[p] = __ldg((const uint4*)(blk + t16 * (D / 2) + ((p ^ sw) << 4)));
+      } else {
+#pragma unroll
+        for (int p = 0; p < CH; ++p) kc[p] = make_uint4(0, 0, 0, 0);
+      }
+    };
+    auto load_v = [&](int k, int page) {
+      if (page >= 0) {
+        const uint8_t* blk = block_of(k, page) + v_codes(D) + t16 * (D / 2);
+#pragma unroll
+        for (int p = 0; p < CH; ++p) vc[p] = __ldg((const uint4*)(blk + ((p ^ sw) << 4)));
+      } else {
+#pragma unroll
+        for (int p = 0; p < CH; ++p) vc[p] = make_uint4(0, 0, 0, 0);
+      }
+    };
+    load_k(0, pg);
+    load_v(0, pg);
+    pg_next = page_of(1);
+    float sref = 0.0f;
+    __half vs_cur = __float2half(0.0f);
+    bool dead = false;
+    // keys of tile k, then values of tile k - 1: each is unpacked while the products of the other run
+    for (int k = 0; k <= nt; ++k) {
+      __half vs_next = __float2half(0.0f);
+      if (k < nt) {
+        const int st = k % NKV;
+        const float ks = __uint_as_float(kw << 16), km = __uint_as_float(kw & 0xffff0000u);
+        const float vs = __uint_as_float(vw << 16), vm = __uint_as_float(vw & 0xffff0000u);
+        // largest offset or step (what is NaN is not greater), as unsigned words
+        const uint32_t km_top = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fabsf(km), fmaxf(8.0f * ks, 0.0f))));
+        const uint32_t vs_top = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(vs, 0.0f)));
+        const uint32_t ok = __ballot_sync(0xffffffffu, pg >= 0);
+        if (lane == 0) {
+          s_red[k & 1][uw][0] = km_top;
+          s_red[k & 1][uw][1] = vs_top;
+        }
+        sm100::named_bar(3, 128);
+        uint32_t kt = 0, vt = 0;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          kt = max(kt, s_red[k & 1][w][0]);
+          vt = max(vt, s_red[k & 1][w][1]);
+        }
+        const float kref = pow2_up(__uint_as_float(kt));
+        sref = fmaxf(sref, pow2_up(__uint_as_float(vt)));
+        const float kmul = 0x1p13f / kref, vmul = 0x1p12f / sref;
+        dead = dead || !sm100::mbar_wait(&b_ke[st], ((k / NKV) & 1) ^ 1, a.flags);
+        const int ring = k % kInfo;
+        if (dt == 0) {
+          s_info[ring].kf = kref * 0x1p-13f;
+          s_info[ring].vref = sref;
+        }
+        if (lane == 0) s_info[ring].ok[uw] = ok;
+        ((float*)(smem + C::MEAN))[ring * KT + dt] = fmaf(8.0f, vs, vm);
+        sm100::mbar_arrive(&b_i[ring]);
+        vs_next = __float2half_rn(vs * vmul);
+        const __half ksh = __float2half_rn(ks * kmul), kmh = __float2half_rn(km * kmul), ks8 = __float2half_rn(8.0f * ks * kmul);
+        const __half2 s2 = __half2half2(ksh), s16 = __half2half2(__float2half_rn(ks * kmul * 0.0625f));
+        uint8_t* kop = smem + C::K + st * C::OP;
+#pragma unroll
+        for (int p = 0; p < CH; ++p) {
+          const uint32_t w[4] = {kc[p].x, kc[p].y, kc[p].z, kc[p].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int chunk = 4 * p + e;
+            *(uint4*)(kop + (chunk >> 3) * 16384 + dt * 128 + (((chunk & 7) ^ (dt & 7)) << 4)) = unpack_codes(w[e], s2, s16);
+          }
+        }
+        const __half2 e0 = __half2half2(kmh), e1 = __halves2half2(kmh, ks8), e2 = __half2half2(ks8);
+        uint8_t* ext = kop + C::MAIN + (dt >> 3) * 256 + (dt & 7) * 16;
+        *(uint4*)ext = make_uint4(*(const uint32_t*)&e0, *(const uint32_t*)&e1, *(const uint32_t*)&e2, 0u);
+        *(uint4*)(ext + 128) = make_uint4(0u, 0u, 0u, 0u);
+        sm100::fence_async_smem();
+        sm100::mbar_arrive(&b_kf[st]);
+      }
+      // ---- the next tile's keys are on their way while the values are unpacked
+      if (k + 1 < nt) {
+        pg = pg_next;
+        load_k(k + 1, pg);
+        pg_next = page_of(k + 2);
+      }
+      if (k > 0) {
+        const int v = k - 1, st = v % NKV;
+        dead = dead || !sm100::mbar_wait(&b_ve[st], ((v / NKV) & 1) ^ 1, a.flags);
+        const __half2 s2 = __half2half2(vs_cur), s16 = __half2half2(__float2half_rn(__half2float(vs_cur) * 0.0625f));
+        uint8_t* vop = smem + C::V + st * C::MAIN;
+#pragma unroll
+        for (int p = 0; p < CH; ++p) {
+          const uint32_t w[4] = {vc[p].x, vc[p].y, vc[p].z, vc[p].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int chunk = 4 * p + e;
+            *(uint4*)(vop + (chunk >> 3) * 16384 + dt * 128 + (((chunk & 7) ^ (dt & 7)) << 4)) = unpack_codes(w[e], s2, s16);
+          }
+        }
+        sm100::fence_async_smem();
+        sm100::mbar_arrive(&b_vf[st]);
+        if (k < nt) load_v(k, pg_v);
+      }
+      vs_cur = vs_next;
+      pg_v = pg;
+    }
+  } else {
+    // ------------------------------------------------------------ products
+    if (lane == 0 && nt > 0) {
+      const uint32_t base = sm100::smem_u32(smem);
+      constexpr uint32_t id_s = sm100::idesc_f16(M, KT), id_o = sm100::idesc_f16(M, D) | (1u << 16);   // values: n-major
+      bool dead = !sm100::mbar_wait(&b_q, 0, a.flags);
+      auto scores = [&](int i, int k) {
+        const uint32_t qa = base + C::Q + i * C::OP, ka = base + C::K + (k % NKV) * C::OP;
+        const uint32_t d = tmem + 128 * (ns == 2 ? i : (k & 1));
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) {
+          const uint32_t off = (s >> 2) * 16384 + (s & 3) * 32;
+          sm100::mma_f16(d, desc_of(qa + off, 16, 1024, 2), desc_of(ka + off, 16, 1024, 2), id_s, s > 0 ? 1u : 0u);
+        }
+        sm100::mma_f16(d, desc_of(qa + C::MAIN, 128, 256, 0), desc_of(ka + C::MAIN, 128, 256, 0), id_s, 1u);
+        sm100::mma_commit(&b_s[ns == 2 ? i : (k & 1)]);
+      };
+      auto sums = [&](int i, int k) {
+        const uint32_t va = base + C::V + (k % NKV) * C::MAIN;
+        const uint32_t p = tmem + 128 * (ns == 2 ? i : (k & 1)), d = tmem + 256 + i * D;
+#pragma unroll
+        for (int s = 0; s < KT / 16; ++s)
+          sm100::mma_f16_ts(d, p + 8 * s, desc_of(va + 2048 * s, 16384, 1024, 2), id_o, (k | s) ? 1u : 0u);
+        sm100::mma_commit(&b_o[i]);
+      };
+      auto wait_k = [&](int k) {
+        dead = dead || !sm100::mbar_wait(&b_kf[k % NKV], (k / NKV) & 1, a.flags);
+        sm100::tc_fence_after();
+      };
+      auto wait_pv = [&](int i, int k) {
+        dead = dead || !sm100::mbar_wait(&b_vf[k % NKV], (k / NKV) & 1, a.flags);
+        dead = dead || !sm100::mbar_wait(&b_p[ns == 2 ? i : (k & 1)], ns == 2 ? (k & 1) : ((k >> 1) & 1), a.flags);
+        sm100::tc_fence_after();
+      };
+      wait_k(0);
+      if (!dead) {
+        for (int i = 0; i < ns; ++i) scores(i, 0);
+        sm100::mma_commit(&b_ke[0]);
+      }
+      for (int k = 0; k < nt && !dead; ++k) {
+        if (ns == 1) {
+          if (k + 1 < nt) {
+            wait_k(k + 1);
+            if (dead) break;
+            scores(0, k + 1);
+            sm100::mma_commit(&b_ke[(k + 1) % NKV]);
+          }
+          wait_pv(0, k);
+          if (dead) break;
+          sums(0, k);
+        } else {
+          for (int i = 0; i < 2; ++i) {
+            wait_pv(i, k);
+            if (dead) break;
+            sums(i, k);
+            if (k + 1 < nt) {
+              if (i == 0) wait_k(k + 1);
+              if (dead) break;
+              scores(i, k + 1);
+            }
+          }
+          if (dead) break;
+          if (k + 1 < nt) sm100::mma_commit(&b_ke[(k + 1) % NKV]);
+        }
+        sm100::mma_commit(&b_ve[k % NKV]);
+      }
+      // nothing of this block is in flight when it gives its tensor memory back
+      sm100::mma_commit(&b_fin);
+      sm100::mbar_wait(&b_fin, 0, a.flags);
+    }
+    __syncwarp();
+  }
+  sm100::tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    sm100::tc_fence_after();
+    sm100::tmem_relinquish();
+    sm100::tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the pieces of a cut unit, a warp a row.
+template <typename TO, int D>
+__global__ void __launch_bounds__(256)
+k_prejoin4(Plan plan, TO* __restrict__ out, AttnArgs a, Shape sh) {
+  constexpr int NS = Cfg<D>::NS;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if ((int)blockIdx.x >= plan.head->joins) return;
+  const Join j = plan.joins[blockIdx.x];
+  const Unit u = plan.units[j.unit];
+  const int kvh = u.hs / sh.nsub, h0 = kvh * a.group + (u.hs % sh.nsub) * sh.gt;
+  const int nh = min(sh.gt, (kvh + 1) * a.group - h0);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const float* ml = plan.parts + (size_t)sh.cap_slots * part_rows(NS) * D;
+  for (int row = blockIdx.y * 8 + warp; row < NS * M; row += gridDim.y * 8) {
+    const int i = row / M, wt = row % M, ti = i * sh.tpm + wt / sh.gt, hh = wt % sh.gt;
+    if (wt >= sh.tpm * sh.gt || ti >= u.n || hh >= nh) continue;
+    float top = -INFINITY;
+    for (int p = 0; p < j.parts; ++p) top = fmaxf(top, ml[((int64_t)(j.slot + p) * part_rows(NS) + row) * 2]);
+    const float base = top == -INFINITY ? 0.0f : top;
+    float l = 0.0f, o[D / 32];
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) o[e] = 0.0f;
+    for (int p = 0; p < j.parts; ++p) {
+      const int64_t pr = (int64_t)(j.slot + p) * part_rows(NS) + row;
+      const float f = ml[pr * 2] == -INFINITY ? (ml[pr * 2 + 1] == 0.0f ? 0.0f : 1.0f) : dec::ex2(ml[pr * 2] - base);
+      l = fmaf(f, ml[pr * 2 + 1], l);
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) o[e] = fmaf(f, plan.parts[pr * D + 32 * e + lane], o[e]);
+    }
+    const int64_t at = (int64_t)(u.tok + ti) * a.n_q + h0 + hh;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) out[at * D + 32 * e + lane] = from_f<TO>(l == 0.0f ? 0.0f : o[e] / l);
+    if (a.lse && lane == 0) a.lse[at] = l == 0.0f ? -INFINITY : (top + (log2f(l) - kUp)) * 0.69314718055994531f;
+  }
+}
+
+}  // namespace pre
+}  // namespace kv4
+}  // namespace sq
