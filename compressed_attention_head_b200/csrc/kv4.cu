@@ -252,7 +252,7 @@ cudaError_t launch_prefill(const Pool& c, const RopeArgs& r, const void* q, void
   pre::k_plan4<<<1, pre::kPlanThreads, 0, st>>>(c, r, a, s, p);
   e = cudaGetLastError();
   if (e == cudaSuccess)
-    e = launch_overlapped(kernel, s.cap_units, pre::kThreads, smem, st, c, r, (const T*)q, (TO*)out, a, s, p);
+    e = launch_overlapped(kernel, s.cap_units, pre::Cfg<D>::THREADS, smem, st, c, r, (const T*)q, (TO*)out, a, s, p);
   if (e == cudaSuccess) e = launch_overlapped(pre::k_prejoin4<TO, D>, dim3(s.sms, 8), 256, 0, st, p, (TO*)out, a, s);
   return e;
 }

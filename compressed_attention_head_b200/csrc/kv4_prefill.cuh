@@ -32,14 +32,17 @@ namespace pre {
 
 constexpr int KT = 128;                       // keys of a tile
 constexpr int M = 128;                        // rows of an accumulator
-constexpr int kSoft = 128;                    // threads of a row tile's softmax
-constexpr int kThreads = 416;                 // 2 x 4 softmax warps, 4 unpacking, 1 issuing
+constexpr int kGroup = 128;                   // threads of a warp group
 constexpr int kInfo = 4;                      // tiles whose factors are kept
 constexpr float kSlack = 4.0f;                // log2 of what a probability may exceed 1 by
 constexpr float kUp = 11.0f;                  // log2 of the probabilities' scale: 2^15 at most with the slack
 
 template <int D> struct Cfg {
   static constexpr int NS = D == 256 ? 1 : 2;          // row tiles of a block
+  static constexpr int NU = D == 256 ? 2 : 1;          // warp groups that unpack, each a share of the coordinates
+  static constexpr int THREADS = (NS + NU + 1) * kGroup;
+  // Registers a thread: the softmax's from what the others give up, 512 threads x 128 in all.
+  static constexpr int R_SOFT = 160, R_UNPACK = NU == 2 ? 144 : 128, R_MMA = 64;
   static constexpr int NKV = D == 256 ? 1 : 2;         // stages of unpacked keys and values
   static constexpr int MAIN = (D / 64) * 16384;        // 128 rows x D fp16, 64 coordinates a slab
   static constexpr int OP = MAIN + 4096;               // and the step that carries the offsets
@@ -237,6 +240,14 @@ __device__ __forceinline__ f2 f2_add(f2 a, f2 b) {
   return d;
 }
 
+// Registers a thread of this warp group (multiples of 8), which together stay within what the block started with.
+template <int N> __device__ __forceinline__ void set_regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N> __device__ __forceinline__ void set_regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // The power of two at or above x >= 0, within the floats whose reciprocals are normal too.
 __device__ __forceinline__ float pow2_up(float x) {
   const uint32_t u = (__float_as_uint(x) + 0x7fffffu) & 0x7f800000u;
@@ -273,17 +284,128 @@ struct Info {
   uint32_t ok[4];        // keys that exist
 };
 
+// Bits of the 32 keys from `from` on that are among a row's [lo, hi] and exist.
+__device__ __forceinline__ uint32_t keys_kept(uint32_t ok, int from, int lo, int hi) {
+  const int x = lo - from, y = hi - from;
+  ok &= x <= 0 ? 0xffffffffu : (x > 31 ? 0u : 0xffffffffu << x);
+  return ok & (y >= 31 ? 0xffffffffu : (y < 0 ? 0u : 0xffffffffu >> (31 - y)));
+}
+
+// The largest of a row's scores of one tile, as they lie in tensor memory.
+__device__ __forceinline__ float row_max(uint32_t t_s) {
+  uint32_t s[2][32];
+  float m0 = -INFINITY, m1 = -INFINITY;
+  ld32(t_s, s[0]);
+#pragma unroll
+  for (int ch = 0; ch < 4; ++ch) {
+    uint32_t* x = s[ch & 1];
+    ld_wait(x);
+    if (ch < 3) ld32(t_s + 32 * (ch + 1), s[(ch + 1) & 1]);
+#pragma unroll
+    for (int e = 0; e < 32; e += 4) {
+      m0 = fmaxf(m0, fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 1])));
+      m1 = fmaxf(m1, fmaxf(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])));
+    }
+  }
+  return fmaxf(m0, m1);
+}
+// The same of the keys that the row attends (few tiles: short code rather than fast).
+__device__ __forceinline__ float row_max_edge(uint32_t t_s, const Info* in, int key0, int lo, int hi) {
+  float m = -INFINITY;
+#pragma unroll 1
+  for (int ch = 0; ch < 4; ++ch) {
+    uint32_t x[32];
+    ld32(t_s + 32 * ch, x);
+    const uint32_t keep = keys_kept(in->ok[ch], key0 + 32 * ch, lo, hi);
+    ld_wait(x);
+#pragma unroll
+    for (int e = 0; e < 32; ++e) m = (keep >> e) & 1u ? fmaxf(m, __uint_as_float(x[e])) : m;
+  }
+  return m;
+}
+
+// Two probabilities: their sum, their sum with the offsets, and the pair in fp16.
+__device__ __forceinline__ uint32_t two_probs(f2 t, f2 mean, f2* lsum, f2* msum) {
+  const float p0 = dec::ex2(f2_lo(t)), p1 = dec::ex2(f2_hi(t));
+  const f2 p = f2_of(p0, p1);
+  *lsum = f2_add(*lsum, p);
+  *msum = f2_fma(p, mean, *msum);
+  return dec::pack_h2(p0, p1);
+}
+
+// Scores to probabilities 2^(s fk + nb), which take the place of the scores' first half.
+__device__ __forceinline__ void row_probs(uint32_t t_s, float fk, float nb, const float* mean, f2* lsum, f2* msum) {
+  const f2 fk2 = f2_of(fk, fk), nb2 = f2_of(nb, nb);
+  uint32_t s[2][32];
+  ld32(t_s, s[0]);
+#pragma unroll
+  for (int ch = 0; ch < 4; ++ch) {
+    uint32_t* x = s[ch & 1];
+    ld_wait(x);
+    if (ch < 3) ld32(t_s + 32 * (ch + 1), s[(ch + 1) & 1]);
+    uint32_t pk[16];
+#pragma unroll
+    for (int e = 0; e < 32; e += 4) {
+      const ulonglong2 mu = *(const ulonglong2*)(mean + 32 * ch + e);
+      pk[e / 2] = two_probs(f2_fma(f2_of(x[e], x[e + 1]), fk2, nb2), mu.x, lsum, msum);
+      pk[e / 2 + 1] = two_probs(f2_fma(f2_of(x[e + 2], x[e + 3]), fk2, nb2), mu.y, lsum, msum);
+    }
+    st16(t_s + 16 * ch, pk);
+  }
+}
+struct Sums { f2 l, m; };
+__device__ __forceinline__ Sums row_probs_edge(uint32_t t_s, float fk, float nb, const float* mean, Sums sum, const Info* in,
+                                            int key0, int lo, int hi) {
+#pragma unroll 1
+  for (int ch = 0; ch < 4; ++ch) {
+    uint32_t x[32], pk[16];
+    ld32(t_s + 32 * ch, x);
+    const uint32_t keep = keys_kept(in->ok[ch], key0 + 32 * ch, lo, hi);
+    ld_wait(x);
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+      const bool k0 = (keep >> e) & 1u, k1 = (keep >> (e + 1)) & 1u;
+      const float t0 = fmaf(__uint_as_float(x[e]), fk, nb), t1 = fmaf(__uint_as_float(x[e + 1]), fk, nb);
+      const float m0 = mean[32 * ch + e], m1 = mean[32 * ch + e + 1];
+      pk[e / 2] = two_probs(f2_of(k0 ? t0 : -INFINITY, k1 ? t1 : -INFINITY), f2_of(k0 ? m0 : 0.0f, k1 ? m1 : 0.0f), &sum.l,
+                            &sum.m);
+    }
+    st16(t_s + 16 * ch, pk);
+  }
+  return sum;
+}
+// Scales a row's sums in tensor memory.
+template <int D> __device__ __forceinline__ void row_scale(uint32_t t_o, float f) {
+  const f2 f2v = f2_of(f, f);
+#pragma unroll 1
+  for (int ch = 0; ch < D / 32; ++ch) {
+    uint32_t x[32];
+    ld32(t_o + 32 * ch, x);
+    ld_wait(x);
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+      const f2 y = f2_fma(f2_of(x[e], x[e + 1]), f2v, 0ull);
+      x[e] = (uint32_t)y;
+      x[e + 1] = (uint32_t)(y >> 32);
+    }
+    st16(t_o + 32 * ch, x);
+    st16(t_o + 32 * ch + 16, x + 16);
+  }
+  sm100::tmem_wait_st();
+}
+
 template <typename T, typename TO, int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
 k_prefill4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, AttnArgs a, Shape sh, Plan plan) {
   using C = Cfg<D>;
-  constexpr int NS = C::NS, NKV = C::NKV, TPR = D / 8, CH = D / 32;
+  constexpr int NS = C::NS, NU = C::NU, NKV = C::NKV, TPR = D / 8, CH = D / 32 / NU;
+  constexpr int kIssuer = (NS + NU) * 4;        // the warp that issues the products
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t b_q, b_fin, b_s[2], b_p[2], b_o[NS], b_kf[NKV], b_ke[NKV], b_vf[NKV], b_ve[NKV], b_i[kInfo];
   __shared__ uint32_t s_tmem;
   __shared__ Info s_info[kInfo];
   __shared__ float s_fq[NS][M];
-  __shared__ uint32_t s_red[2][4][2];
+  __shared__ uint32_t s_red[NU][2][4][2];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -293,22 +415,22 @@ k_prefill4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, At
   const Unit u = plan.units[blockIdx.x];
   if (u.slot == -2) return;
   const int ns = u.n > sh.tpm ? NS : 1, nt = u.nt;
-  if (warp == 12) sm100::tmem_alloc(&s_tmem, 512);
+  if (warp == kIssuer) sm100::tmem_alloc(&s_tmem, 512);
   if (tid == 0) {
-    sm100::mbar_init(&b_q, ns * kSoft);
+    sm100::mbar_init(&b_q, ns * kGroup);
     sm100::mbar_init(&b_fin, 1);
     for (int i = 0; i < 2; ++i) {
       sm100::mbar_init(&b_s[i], 1);
-      sm100::mbar_init(&b_p[i], kSoft);
+      sm100::mbar_init(&b_p[i], kGroup);
     }
     for (int i = 0; i < NS; ++i) sm100::mbar_init(&b_o[i], 1);
     for (int i = 0; i < NKV; ++i) {
-      sm100::mbar_init(&b_kf[i], 128);
+      sm100::mbar_init(&b_kf[i], NU * kGroup);
       sm100::mbar_init(&b_ke[i], 1);
-      sm100::mbar_init(&b_vf[i], 128);
+      sm100::mbar_init(&b_vf[i], NU * kGroup);
       sm100::mbar_init(&b_ve[i], 1);
     }
-    for (int i = 0; i < kInfo; ++i) sm100::mbar_init(&b_i[i], 128);
+    for (int i = 0; i < kInfo; ++i) sm100::mbar_init(&b_i[i], kGroup);
     sm100::fence_mbar_init();
   }
   sm100::tc_fence_before();
@@ -319,12 +441,13 @@ k_prefill4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, At
   const int kvh = u.hs / sh.nsub, h0 = kvh * a.group + (u.hs % sh.nsub) * sh.gt;
   const int nh = min(sh.gt, (kvh + 1) * a.group - h0);
 
-  if (warp < 8) {
+  if (warp < NS * 4) {
+    set_regs_up<C::R_SOFT>();
     // ------------------------------------------------------------ queries, softmax, outputs
     const int i = warp >> 2, wt = tid & 127;
     if (i < ns) {
       uint8_t* qop = smem + C::Q + i * C::OP;
-      constexpr int RP = kSoft / TPR, BATCH = 4;
+      constexpr int RP = kGroup / TPR, BATCH = 4;
       const int j = wt % TPR;
       for (int r0 = 0; r0 < M; r0 += RP * BATCH) {
         Vec8<T> own[BATCH], part[BATCH];
@@ -391,7 +514,7 @@ k_prefill4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, At
       }
       sm100::fence_async_smem();
       sm100::mbar_arrive(&b_q);
-      sm100::named_bar(1 + i, kSoft);
+      sm100::named_bar(1 + i, kGroup);
 
       const int ti = i * sh.tpm + wt / sh.gt, hh = wt % sh.gt;
       const bool is_row = wt < sh.tpm * sh.gt && ti < u.n && hh < nh;
@@ -407,7 +530,7 @@ k_prefill4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, At
       const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
       const uint32_t t_o = tmem + lanes + 256 + i * D;
       float mref = -INFINITY, vref = 0.0f;
-      f2 lsum = 0, msum = 0;
+      Sums sum{0ull, 0ull};
       bool dead = false;
       for (int k = 0; k < nt && !dead; ++k) {
         const int sl = ns == 2 ? i : (k & 1);
@@ -423,40 +546,7 @@ k_prefill4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, At
         const bool edge = (in.ok[0] & in.ok[1] & in.ok[2] & in.ok[3]) != 0xffffffffu || key0 < w_lo || key0 + KT - 1 > w_hi;
         const float fk = fq * in.kf;
         const float* mean = (const float*)(smem + C::MEAN) + ring * KT;
-        // ---- the largest score
-        float mx = -INFINITY;
-        uint32_t s[2][32];
-        // mask bits of 32 keys of this row
-        auto keep = [&](int ch) {
-          const int from = key0 + 32 * ch;
-          const int x = lo - from, y = hi - from;                        // keys x .. y of the 32
-          uint32_t m = in.ok[ch];
-          m &= x <= 0 ? 0xffffffffu : (x > 31 ? 0u : 0xffffffffu << x);
-          m &= y >= 31 ? 0xffffffffu : (y < 0 ? 0u : 0xffffffffu >> (31 - y));
-          return m;
-        };
-        ld32(t_s, s[0]);
-#pragma unroll
-        for (int ch = 0; ch < 4; ++ch) {
-          ld_wait(s[ch & 1]);
-          if (ch < 3) ld32(t_s + 32 * (ch + 1), s[(ch + 1) & 1]);
-          uint32_t* x = s[ch & 1];
-          if (edge) {
-            const uint32_t m = keep(ch);
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if ((m >> e) & 1u) mx = fmaxf(mx, __uint_as_float(x[e]));
-          } else {
-            float m0 = -INFINITY, m1 = -INFINITY;
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              m0 = fmaxf(m0, fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 1])));
-              m1 = fmaxf(m1, fmaxf(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])));
-            }
-            mx = fmaxf(mx, fmaxf(m0, m1));
-          }
-        }
-        const float top = mx * fk;
+        const float top = fk * (edge ? row_max_edge(t_s, &in, key0, lo, hi) : row_max(t_s));
         const float nv = in.vref;
         if (__any_sync(0xffffffffu, !(top <= mref + kSlack) || nv != vref)) {
           float f = 1.0f;
@@ -465,78 +555,32 @@ k_prefill4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, At
             mref = top;
           }
           const f2 ff = f2_of(f, f);
-          lsum = f2_fma(lsum, ff, 0ull);
-          msum = f2_fma(msum, ff, 0ull);
+          sum.l = f2_fma(sum.l, ff, 0ull);
+          sum.m = f2_fma(sum.m, ff, 0ull);
           if (k > 0) {
-            const float fo = f * (vref / nv);
             dead = !sm100::mbar_wait(&b_o[i], (k - 1) & 1, a.flags);
             dead = __any_sync(0xffffffffu, dead);
             if (dead) break;
             sm100::tc_fence_after();
-            const f2 fo2 = f2_of(fo, fo);
-#pragma unroll 1
-            for (int ch = 0; ch < D / 32; ++ch) {
-              uint32_t* x = s[1];
-              ld32(t_o + 32 * ch, x);
-              ld_wait(x);
-#pragma unroll
-              for (int e = 0; e < 32; e += 2) {
-                const f2 y = f2_fma(f2_of(x[e], x[e + 1]), fo2, 0ull);
-                x[e] = (uint32_t)y;
-                x[e + 1] = (uint32_t)(y >> 32);
-              }
-              st16(t_o + 32 * ch, x);
-              st16(t_o + 32 * ch + 16, x + 16);
-            }
-            sm100::tmem_wait_st();
+            row_scale<D>(t_o, f * (vref / nv));
           }
           vref = nv;
         }
-        // ---- probabilities
-        ld32(t_s, s[0]);
-        const float base = (mref == -INFINITY ? 0.0f : mref) - kUp;
-        const f2 fk2 = f2_of(fk, fk), nb2 = f2_of(-base, -base);
-#pragma unroll
-        for (int ch = 0; ch < 4; ++ch) {
-          ld_wait(s[ch & 1]);
-          if (ch < 3) ld32(t_s + 32 * (ch + 1), s[(ch + 1) & 1]);
-          uint32_t* x = s[ch & 1];
-          uint32_t pk[16];
-          const uint32_t m = edge ? keep(ch) : 0xffffffffu;
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const float4 mu = *(const float4*)(mean + 32 * ch + e);
-            const float mv[4] = {mu.x, mu.y, mu.z, mu.w};
-#pragma unroll
-            for (int h = 0; h < 4; h += 2) {
-              const f2 t = f2_fma(f2_of(x[e + h], x[e + h + 1]), fk2, nb2);
-              float t0 = f2_lo(t), t1 = f2_hi(t), m0 = mv[h], m1 = mv[h + 1];
-              if (edge) {
-                const bool k0 = (m >> (e + h)) & 1u, k1 = (m >> (e + h + 1)) & 1u;
-                t0 = k0 ? t0 : -INFINITY;
-                t1 = k1 ? t1 : -INFINITY;
-                m0 = k0 ? m0 : 0.0f;
-                m1 = k1 ? m1 : 0.0f;
-              }
-              const float p0 = dec::ex2(t0), p1 = dec::ex2(t1);
-              const f2 p = f2_of(p0, p1);
-              lsum = f2_add(lsum, p);
-              msum = f2_fma(p, f2_of(m0, m1), msum);
-              pk[(e + h) / 2] = dec::pack_h2(p0, p1);
-            }
-          }
-          st16(t_s + 16 * ch, pk);
-        }
+        const float nb = kUp - (mref == -INFINITY ? 0.0f : mref);
+        if (edge)
+          sum = row_probs_edge(t_s, fk, nb, mean, sum, &in, key0, lo, hi);
+        else
+          row_probs(t_s, fk, nb, mean, &sum.l, &sum.m);
         sm100::tmem_wait_st();
         sm100::tc_fence_before();
         sm100::mbar_arrive(&b_p[sl]);
       }
       // ---- outputs
-      if (nt > 0 && !dead) dead = !sm100::mbar_wait(&b_o[i], (nt - 1) & 1, a.flags);
+      if (nt > 0 && !dead) dead = !sm100::mbar_wait(&b_fin, 0, a.flags);
       dead = __any_sync(0xffffffffu, dead);
       if (!dead) {
         sm100::tc_fence_after();
-        const float l = f2_lo(lsum) + f2_hi(lsum), mv = f2_lo(msum) + f2_hi(msum);
+        const float l = f2_lo(sum.l) + f2_hi(sum.l), mv = f2_lo(sum.m) + f2_hi(sum.m);
         const float vf = vref * 0x1p-12f;
         const bool whole = u.slot < 0;
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
@@ -585,9 +629,10 @@ k_prefill4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, At
         }
       }
     }
-  } else if (warp < 12) {
-    // ------------------------------------------------------------ unpacking: a thread a key
-    const int dt = tid - 256, uw = warp - 8;
+  } else if (warp < kIssuer) {
+    // ------------------------------------------------------------ unpacking: a thread a key, a group its share of the chunks
+    if constexpr (C::R_UNPACK > 128) set_regs_up<C::R_UNPACK>();
+    const int dt = tid & 127, uw = warp & 3, share = (warp >> 2) - NS, ch0 = share * CH;
     int64_t ulo, uhi;
     unit_keys(c, r, a, u.pos, u.n, &ulo, &uhi);
     const int64_t page_bytes = ((int64_t)c.n_kv << (c.page_shift - 4)) * blk_bytes(D);
@@ -598,12 +643,15 @@ k_prefill4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, At
     auto page_of = [&](int k) {
       const int64_t t = (int64_t)(u.t0 + k) * KT + dt;
       if (k >= nt || t < ulo || t > uhi) return -2;
-      const int pg = __ldg(c.table + u.row * c.table_stride + (t >> c.page_shift));
-      if (pg < 0 || pg >= c.n_pages) {
+      return max(-1, __ldg(c.table + u.row * c.table_stride + (t >> c.page_shift)));
+    };
+    // (looked at when its codes are loaded, a tile after it was asked for)
+    auto checked = [&](int page) {
+      if (page == -1 || page >= c.n_pages) {
         raise(a.flags, SQ_FLAG_PAGE);
         return -2;
       }
-      return pg;
+      return page;
     };
     auto block_of = [&](int k, int pg) {
       const int t = ((u.t0 + k) * KT + dt) & in_page;
@@ -611,7 +659,7 @@ k_prefill4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, At
     };
     uint4 kc[CH], vc[CH];
     uint32_t kw = 0, vw = 0;
-    int pg = page_of(0), pg_v = pg, pg_next;
+    int pg = checked(page_of(0)), pg_v = pg, pg_next;
     auto load_k = [&](int k, int page) {
       kw = vw = 0;
       if (page >= 0) {
@@ -619,7 +667,7 @@ k_prefill4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, At
         kw = __ldg((const uint32_t*)(blk + k_pairs(D) + 4 * t16));
         vw = __ldg((const uint32_t*)(blk + v_pairs(D) + 4 * t16));
 #pragma unroll
-        for (int p = 0; p < CH; ++p) kc[p] = __ldg((const uint4*)(blk + t16 * (D / 2) + ((p ^ sw) << 4)));
+        for (int p = 0; p < CH; ++p) kc[p] = __ldg((const uint4*)(blk + t16 * (D / 2) + (((p + ch0) ^ sw) << 4)));
       } else {
 #pragma unroll
         for (int p = 0; p < CH; ++p) kc[p] = make_uint4(0, 0, 0, 0);
@@ -629,7 +677,7 @@ k_prefill4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, At
       if (page >= 0) {
         const uint8_t* blk = block_of(k, page) + v_codes(D) + t16 * (D / 2);
 #pragma unroll
-        for (int p = 0; p < CH; ++p) vc[p] = __ldg((const uint4*)(blk + ((p ^ sw) << 4)));
+        for (int p = 0; p < CH; ++p) vc[p] = __ldg((const uint4*)(blk + (((p + ch0) ^ sw) << 4)));
       } else {
 #pragma unroll
         for (int p = 0; p < CH; ++p) vc[p] = make_uint4(0, 0, 0, 0);
@@ -653,28 +701,30 @@ k_prefill4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, At
         const uint32_t vs_top = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(vs, 0.0f)));
         const uint32_t ok = __ballot_sync(0xffffffffu, pg >= 0);
         if (lane == 0) {
-          s_red[k & 1][uw][0] = km_top;
-          s_red[k & 1][uw][1] = vs_top;
+          s_red[share][k & 1][uw][0] = km_top;
+          s_red[share][k & 1][uw][1] = vs_top;
         }
-        sm100::named_bar(3, 128);
+        sm100::named_bar(3 + share, kGroup);
         uint32_t kt = 0, vt = 0;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          kt = max(kt, s_red[k & 1][w][0]);
-          vt = max(vt, s_red[k & 1][w][1]);
+          kt = max(kt, s_red[share][k & 1][w][0]);
+          vt = max(vt, s_red[share][k & 1][w][1]);
         }
         const float kref = pow2_up(__uint_as_float(kt));
         sref = fmaxf(sref, pow2_up(__uint_as_float(vt)));
         const float kmul = 0x1p13f / kref, vmul = 0x1p12f / sref;
         dead = dead || !sm100::mbar_wait(&b_ke[st], ((k / NKV) & 1) ^ 1, a.flags);
         const int ring = k % kInfo;
-        if (dt == 0) {
-          s_info[ring].kf = kref * 0x1p-13f;
-          s_info[ring].vref = sref;
+        if (share == 0) {
+          if (dt == 0) {
+            s_info[ring].kf = kref * 0x1p-13f;
+            s_info[ring].vref = sref;
+          }
+          if (lane == 0) s_info[ring].ok[uw] = ok;
+          ((float*)(smem + C::MEAN))[ring * KT + dt] = fmaf(8.0f, vs, vm);
+          sm100::mbar_arrive(&b_i[ring]);
         }
-        if (lane == 0) s_info[ring].ok[uw] = ok;
-        ((float*)(smem + C::MEAN))[ring * KT + dt] = fmaf(8.0f, vs, vm);
-        sm100::mbar_arrive(&b_i[ring]);
         vs_next = __float2half_rn(vs * vmul);
         const __half ksh = __float2half_rn(ks * kmul), kmh = __float2half_rn(km * kmul), ks8 = __float2half_rn(8.0f * ks * kmul);
         const __half2 s2 = __half2half2(ksh), s16 = __half2half2(__float2half_rn(ks * kmul * 0.0625f));
@@ -684,20 +734,22 @@ k_prefill4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, At
           const uint32_t w[4] = {kc[p].x, kc[p].y, kc[p].z, kc[p].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int chunk = 4 * p + e;
+            const int chunk = 4 * (p + ch0) + e;
             *(uint4*)(kop + (chunk >> 3) * 16384 + dt * 128 + (((chunk & 7) ^ (dt & 7)) << 4)) = unpack_codes(w[e], s2, s16);
           }
         }
+        if (share == NU - 1) {
         const __half2 e0 = __half2half2(kmh), e1 = __halves2half2(kmh, ks8), e2 = __half2half2(ks8);
         uint8_t* ext = kop + C::MAIN + (dt >> 3) * 256 + (dt & 7) * 16;
         *(uint4*)ext = make_uint4(*(const uint32_t*)&e0, *(const uint32_t*)&e1, *(const uint32_t*)&e2, 0u);
         *(uint4*)(ext + 128) = make_uint4(0u, 0u, 0u, 0u);
+        }
         sm100::fence_async_smem();
         sm100::mbar_arrive(&b_kf[st]);
       }
       // ---- the next tile's keys are on their way while the values are unpacked
       if (k + 1 < nt) {
-        pg = pg_next;
+        pg = checked(pg_next);
         load_k(k + 1, pg);
         pg_next = page_of(k + 2);
       }
@@ -711,7 +763,7 @@ k_prefill4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, At
           const uint32_t w[4] = {vc[p].x, vc[p].y, vc[p].z, vc[p].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int chunk = 4 * p + e;
+            const int chunk = 4 * (p + ch0) + e;
             *(uint4*)(vop + (chunk >> 3) * 16384 + dt * 128 + (((chunk & 7) ^ (dt & 7)) << 4)) = unpack_codes(w[e], s2, s16);
           }
         }
@@ -724,17 +776,19 @@ k_prefill4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, At
     }
   } else {
     // ------------------------------------------------------------ products
-    if (lane == 0 && nt > 0) {
+    set_regs_down<C::R_MMA>();
+    if (warp == kIssuer && lane == 0 && nt > 0) {
       const uint32_t base = sm100::smem_u32(smem);
       constexpr uint32_t id_s = sm100::idesc_f16(M, KT), id_o = sm100::idesc_f16(M, D) | (1u << 16);   // values: n-major
       bool dead = !sm100::mbar_wait(&b_q, 0, a.flags);
       auto scores = [&](int i, int k) {
         const uint32_t qa = base + C::Q + i * C::OP, ka = base + C::K + (k % NKV) * C::OP;
         const uint32_t d = tmem + 128 * (ns == 2 ? i : (k & 1));
-#pragma unroll
+        const uint64_t qd = desc_of(qa, 16, 1024, 2), kd = desc_of(ka, 16, 1024, 2);
+#pragma unroll 4
         for (int s = 0; s < D / 16; ++s) {
-          const uint32_t off = (s >> 2) * 16384 + (s & 3) * 32;
-          sm100::mma_f16(d, desc_of(qa + off, 16, 1024, 2), desc_of(ka + off, 16, 1024, 2), id_s, s > 0 ? 1u : 0u);
+          const uint64_t off = (uint64_t)((s >> 2) * 1024 + (s & 3) * 2);       // in units of 16 bytes
+          sm100::mma_f16(d, qd + off, kd + off, id_s, s > 0 ? 1u : 0u);
         }
         sm100::mma_f16(d, desc_of(qa + C::MAIN, 128, 256, 0), desc_of(ka + C::MAIN, 128, 256, 0), id_s, 1u);
         sm100::mma_commit(&b_s[ns == 2 ? i : (k & 1)]);
@@ -742,51 +796,78 @@ k_prefill4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, At
       auto sums = [&](int i, int k) {
         const uint32_t va = base + C::V + (k % NKV) * C::MAIN;
         const uint32_t p = tmem + 128 * (ns == 2 ? i : (k & 1)), d = tmem + 256 + i * D;
-#pragma unroll
-        for (int s = 0; s < KT / 16; ++s)
-          sm100::mma_f16_ts(d, p + 8 * s, desc_of(va + 2048 * s, 16384, 1024, 2), id_o, (k | s) ? 1u : 0u);
+        const uint64_t vd = desc_of(va, 16384, 1024, 2);
+#pragma unroll 4
+        for (int s = 0; s < KT / 16; ++s) sm100::mma_f16_ts(d, p + 8 * s, vd + 128 * s, id_o, (k | s) ? 1u : 0u);
         sm100::mma_commit(&b_o[i]);
       };
       auto wait_k = [&](int k) {
         dead = dead || !sm100::mbar_wait(&b_kf[k % NKV], (k / NKV) & 1, a.flags);
         sm100::tc_fence_after();
+        return !dead;
       };
-      auto wait_pv = [&](int i, int k) {
+      auto wait_v = [&](int k) {
         dead = dead || !sm100::mbar_wait(&b_vf[k % NKV], (k / NKV) & 1, a.flags);
-        dead = dead || !sm100::mbar_wait(&b_p[ns == 2 ? i : (k & 1)], ns == 2 ? (k & 1) : ((k >> 1) & 1), a.flags);
         sm100::tc_fence_after();
+        return !dead;
       };
-      wait_k(0);
-      if (!dead) {
-        for (int i = 0; i < ns; ++i) scores(i, 0);
-        sm100::mma_commit(&b_ke[0]);
-      }
-      for (int k = 0; k < nt && !dead; ++k) {
-        if (ns == 1) {
-          if (k + 1 < nt) {
-            wait_k(k + 1);
-            if (dead) break;
-            scores(0, k + 1);
-            sm100::mma_commit(&b_ke[(k + 1) % NKV]);
-          }
-          wait_pv(0, k);
-          if (dead) break;
+      // Scores may not take the place of probabilities before the product that reads those has ended: products
+      // of different accumulators are not ordered among each other, so the end is waited for.
+      if (ns == 1) {
+        for (int k = 0; k < 2 && k < nt; ++k) {
+          if (!wait_k(k)) break;
+          scores(0, k);
+          sm100::mma_commit(&b_ke[k % NKV]);
+        }
+        for (int k = 0; k < nt && !dead; ++k) {
+          dead = !sm100::mbar_wait(&b_p[k & 1], (k >> 1) & 1, a.flags);
+          if (!wait_v(k)) break;
           sums(0, k);
-        } else {
+          sm100::mma_commit(&b_ve[k % NKV]);
+          if (k + 2 < nt) {
+            dead = !sm100::mbar_wait(&b_o[0], k & 1, a.flags);
+            if (!wait_k(k + 2)) break;
+            scores(0, k + 2);
+            sm100::mma_commit(&b_ke[k % NKV]);
+          }
+        }
+      } else if (wait_k(0)) {
+        // Whichever row tile has its next operand is served: its probabilities, or the end of its last sum.
+        scores(0, 0);
+        scores(1, 0);
+        sm100::mma_commit(&b_ke[0]);
+        int at[2] = {0, 0};                       // tiles of a row tile
+        bool summing[2] = {false, false};         // it waits for the end of a sum
+        uint64_t since = 0;
+        for (uint32_t idle = 0; !dead && (at[0] < nt || at[1] < nt); ++idle) {
+#pragma unroll
           for (int i = 0; i < 2; ++i) {
-            wait_pv(i, k);
-            if (dead) break;
-            sums(i, k);
-            if (k + 1 < nt) {
-              if (i == 0) wait_k(k + 1);
-              if (dead) break;
+            const int k = at[i];
+            if (k >= nt || !sm100::mbar_test(summing[i] ? &b_o[i % NS] : &b_p[i], k & 1)) continue;
+            idle = 0;
+            if (!summing[i]) {
+              if (!wait_v(k)) break;
+              sums(i, k);
+              if (at[i ^ 1] > k || (at[i ^ 1] == k && summing[i ^ 1])) sm100::mma_commit(&b_ve[k % NKV]);     // the second to read them
+              summing[i] = true;
+              if (k + 1 == nt) at[i] = nt;
+            } else {
+              if (!wait_k(k + 1)) break;
               scores(i, k + 1);
+              if (at[i ^ 1] > k) sm100::mma_commit(&b_ke[(k + 1) % NKV]);
+              summing[i] = false;
+              at[i] = k + 1;
             }
           }
-          if (dead) break;
-          if (k + 1 < nt) sm100::mma_commit(&b_ke[(k + 1) % NKV]);
+          if ((idle & 1023u) == 1023u) {
+            const uint64_t now = sm100::global_ns();
+            if (idle == 1023u) since = now;
+            if (now - since > sm100::kTimeoutNs) {
+              raise(a.flags, SQ_FLAG_TIMEOUT);
+              dead = true;
+            }
+          }
         }
-        sm100::mma_commit(&b_ve[k % NKV]);
       }
       // nothing of this block is in flight when it gives its tensor memory back
       sm100::mma_commit(&b_fin);
@@ -796,7 +877,7 @@ k_prefill4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, At
   }
   sm100::tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == kIssuer) {
     sm100::tc_fence_after();
     sm100::tmem_relinquish();
     sm100::tmem_dealloc(tmem, 512);
