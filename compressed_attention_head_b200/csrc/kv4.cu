@@ -228,31 +228,37 @@ pre::Shape prefill_shape(int batch, int n_kv, int group, int d, int64_t n_tok) {
   s.cap_slots = 2 * s.sms;
   const int64_t units = (int64_t)n_kv * s.nsub * ((n_tok + s.tpu - 1) / s.tpu + batch) + s.cap_slots;
   s.cap_units = units > 0x7fffffff ? 0 : (int)units;
+  s.q_tiles = n_tok / s.tpm + batch + 1;      // one more: offsets that begin below 0 round up
   return s;
 }
 
 constexpr size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-size_t prefill_layout(const pre::Shape& s, int d, uint8_t* ws, pre::Plan* p) {
+size_t prefill_layout(const pre::Shape& s, int n_kv, int d, uint8_t* ws, pre::Plan* p) {
   const size_t units = 256, joins = units + up256((size_t)s.cap_units * sizeof(pre::Unit));
   const size_t parts = joins + up256((size_t)s.sms * sizeof(pre::Join));
   const size_t rows = (size_t)s.cap_slots * pre::part_rows(d == 256 ? 1 : 2);
-  if (p) *p = pre::Plan{(pre::Head*)ws, (pre::Unit*)(ws + units), (pre::Join*)(ws + joins), (float*)(ws + parts)};
-  return parts + rows * (d + 2) * sizeof(float);
+  const size_t q = parts + up256(rows * (d + 2) * sizeof(float));
+  const size_t image = d == 64 ? pre::Cfg<64>::QIMG : d == 128 ? pre::Cfg<128>::QIMG : pre::Cfg<256>::QIMG;
+  if (p)
+    *p = pre::Plan{(pre::Head*)ws, (pre::Unit*)(ws + units), (pre::Join*)(ws + joins), (float*)(ws + parts), ws + q, s.q_tiles};
+  return q + (size_t)n_kv * s.nsub * s.q_tiles * image;
 }
 
 template <typename T, typename TO, int D>
 cudaError_t launch_prefill(const Pool& c, const RopeArgs& r, const void* q, void* out, const AttnArgs& a, const pre::Shape& s,
                            const pre::Plan& p, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
-  auto kernel = pre::k_prefill4<T, TO, D>;
+  auto kernel = pre::k_prefill4<TO, D>;
   constexpr int smem = pre::Cfg<D>::TOTAL;
   cudaError_t e = allow_smem(kernel, smem, &done);
   if (e != cudaSuccess) return e;
-  pre::k_plan4<<<1, pre::kPlanThreads, 0, st>>>(c, r, a, s, p);
+  const int64_t rows = a.n_tok * a.n_q, per = pre::kPlanThreads / (D / 8);
+  const unsigned blocks = (unsigned)std::min<int64_t>((rows + per - 1) / per, 4 * s.sms);
+  pre::k_prepare4<T, D><<<1 + blocks, pre::kPlanThreads, 0, st>>>(c, r, (const T*)q, a, s, p);
   e = cudaGetLastError();
   if (e == cudaSuccess)
-    e = launch_overlapped(kernel, s.cap_units, pre::Cfg<D>::THREADS, smem, st, c, r, (const T*)q, (TO*)out, a, s, p);
+    e = launch_overlapped(kernel, s.cap_units, pre::Cfg<D>::THREADS, smem, st, c, r, (TO*)out, a, s, p);
   if (e == cudaSuccess) e = launch_overlapped(pre::k_prejoin4<TO, D>, dim3(s.sms, 8), 256, 0, st, p, (TO*)out, a, s);
   return e;
 }
@@ -260,7 +266,7 @@ cudaError_t launch_prefill(const Pool& c, const RopeArgs& r, const void* q, void
 sq_status run_prefill(const Pool& c, const RopeArgs& r, const void* q, sq_dtype dtype, void* out, sq_dtype out_dtype,
                       const AttnArgs& a, const pre::Shape& s, uint8_t* ws, cudaStream_t st) {
   pre::Plan p;
-  prefill_layout(s, c.d, ws, &p);
+  prefill_layout(s, c.n_kv, c.d, ws, &p);
   cudaError_t e = cudaSuccess;
 #define SQ_CALL(T, DD)                                                                           \
   if (out_dtype == SQ_F32) e = launch_prefill<T, float, DD>(c, r, q, out, a, s, p, st);          \
@@ -360,7 +366,7 @@ size_t sq_kv4_attn_prefill_workspace(int batch, int n_q_heads, int n_kv_heads, i
       n_tok > 0x7fffffff)
     return 0;
   const pre::Shape s = prefill_shape(batch, n_kv_heads, n_q_heads / n_kv_heads, d, n_tok);
-  return s.cap_units ? prefill_layout(s, d, nullptr, nullptr) : 0;
+  return s.cap_units ? prefill_layout(s, n_kv_heads, d, nullptr, nullptr) : 0;
 }
 
 sq_status sq_kv4_attn_prefill(const sq_kv4_cache* cache, const int32_t* d_cu, const int32_t* d_start, int n_q_heads,

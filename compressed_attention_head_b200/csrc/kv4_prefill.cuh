@@ -46,6 +46,7 @@ template <int D> struct Cfg {
   static constexpr int NKV = D == 256 ? 1 : 2;         // stages of unpacked keys and values
   static constexpr int MAIN = (D / 64) * 16384;        // 128 rows x D fp16, 64 coordinates a slab
   static constexpr int OP = MAIN + 4096;               // and the step that carries the offsets
+  static constexpr int QIMG = OP + M * 4;              // an operand as it lies in memory: rows, and their score factors
   static constexpr int Q = 0;
   static constexpr int K = Q + NS * OP;
   static constexpr int V = K + NKV * OP;
@@ -59,9 +60,9 @@ struct Unit {
   int64_t pos;         // position of the first token
   int row, hs;         // sequence, KV head x pass
   int tok, n;          // first token of the call, tokens
+  int off;             // of the first token in its sequence
   int t0, nt;          // key tiles
   int slot;            // of the partial sums, -1: the whole of it, -2: nothing to do
-  int pad;
 };
 struct Join { int unit, slot, parts, pad; };
 struct Head { int units, joins, slots, pad; };
@@ -69,6 +70,7 @@ struct Head { int units, joins, slots, pad; };
 struct Shape {
   int gt, nsub, tpm, tpu;      // heads of a pass, passes, tokens of a row tile, of a unit
   int cap_units, cap_slots, sms;
+  int64_t q_tiles;
 };
 
 struct Plan {
@@ -76,7 +78,13 @@ struct Plan {
   Unit* units;
   Join* joins;
   float* parts;
+  uint8_t* q;                  // query operands, [n_kv x nsub][row tiles] of Cfg::QIMG bytes
+  int64_t q_tiles;             // row tiles a head
 };
+
+// Row tile of the token at `off` in a sequence whose first token is `tok`: every
+// sequence starts a tile of its own, no two share one, and none is past n_tok / tpm + batch.
+__device__ __forceinline__ int64_t row_tile(int64_t tok, int row, int off, int tpm) { return tok / tpm + row + off / tpm; }
 
 __host__ __device__ inline size_t part_rows(int ns) { return (size_t)ns * M; }
 
@@ -93,8 +101,7 @@ __device__ __forceinline__ void unit_keys(const Pool& c, const RopeArgs& r, cons
 
 constexpr int kPlanThreads = 512;
 
-__global__ void __launch_bounds__(kPlanThreads)
-k_plan4(Pool c, RopeArgs r, AttnArgs a, Shape s, Plan p) {
+__device__ __forceinline__ void make_units(const Pool& c, const RopeArgs& r, const AttnArgs& a, const Shape& s, const Plan& p) {
   __shared__ unsigned long long s_tiles;
   __shared__ int s_longest, s_hist[64], s_at[64], s_slots, s_joins;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -104,7 +111,6 @@ k_plan4(Pool c, RopeArgs r, AttnArgs a, Shape s, Plan p) {
     s_tiles = 0;
     s_longest = s_slots = s_joins = 0;
   }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __syncthreads();
   int pass_cut = 0x7fffffff, longest = 1;
   // three passes over the units: their lengths, the lengths' classes, the list
@@ -128,6 +134,7 @@ k_plan4(Pool c, RopeArgs r, AttnArgs a, Shape s, Plan p) {
         w.pos = start + u * s.tpu;
         w.row = b;
         w.tok = (int)(t_lo + u * s.tpu);
+        w.off = w.tok - __ldg(a.cu + b);
         w.n = (int)min((int64_t)s.tpu, t_hi - w.tok);
         int64_t lo, hi;
         unit_keys(c, r, a, w.pos, w.n, &lo, &hi);
@@ -157,7 +164,6 @@ k_plan4(Pool c, RopeArgs r, AttnArgs a, Shape s, Plan p) {
             }
           }
           w.hs = h;
-          w.pad = 0;
           int t = (int)(lo / KT);
           for (int i = 0; i < parts; ++i, ++at) {
             w.t0 = t;
@@ -196,6 +202,82 @@ k_plan4(Pool c, RopeArgs r, AttnArgs a, Shape s, Plan p) {
   }
   __syncthreads();
   if (tid == 0) p.head->joins = s_joins;
+}
+
+// Block 0 lists the units; the others turn, scale and lay out the queries, D / 8
+// threads a row, as the products take them: fp16, rows of a power of two each, 64
+// coordinates a 16 KB slab of swizzled lines, eight coordinates in the codes' order.
+// Once a call, so that the pieces of a cut unit do not repeat it and a block's
+// prologue is one bulk copy a row tile.
+template <typename T, int D>
+__global__ void __launch_bounds__(kPlanThreads)
+k_prepare4(Pool c, RopeArgs r, const T* __restrict__ q, AttnArgs a, Shape s, Plan p) {
+  using C = Cfg<D>;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (blockIdx.x == 0) {
+    make_units(c, r, a, s, p);
+    return;
+  }
+  constexpr int TPR = D / 8;
+  const int j = threadIdx.x % TPR;
+  const int64_t rows = a.n_tok * a.n_q, step = (int64_t)(gridDim.x - 1) * (kPlanThreads / TPR);
+  for (int64_t x0 = (int64_t)(blockIdx.x - 1) * (kPlanThreads / TPR); x0 < rows; x0 += step) {
+    const int64_t v = x0 + threadIdx.x / TPR;                    // (token, query head)
+    const int64_t tok = v / a.n_q;
+    const int head = (int)(v - tok * a.n_q);
+    int32_t off = 0;
+    const int b = v < rows ? row_of(a.cu, c.batch, tok, &off) : -1;
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = 0.0f;
+    const int64_t pos = b < 0 ? -1 : min((int64_t)__ldg(a.start + b) + off, c.cap() - 1);
+    if (pos >= 0 && !(r.table && pos >= r.n_pos)) {
+      const T* src = q + tok * a.qs_tok + (int64_t)head * a.qs_head;
+      const int pi = partner(8 * j, r);
+      const Vec8<T> own = load8<T>(src + 8 * j), other = load8<T>(src + pi);
+      unpack8<T>(own, x);
+      if (r.table) {
+        float y[8];
+        unpack8<T>(other, y);
+        rotate8<T>(x, y, 8 * j, r, pos);
+      }
+    }
+    float top = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[e]));
+#pragma unroll
+    for (int o = 1; o < TPR; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    // 2^e with top 2^e in [2^6, 2^7): the sum over a head stays below 2^15
+    int e2 = 0;
+    if (top > 0.0f && top < INFINITY) e2 = max(-100, min(100, 6 - ilogbf(top)));
+    const float up = __int_as_float((127 + e2) << 23);
+    float sum = 0.0f;
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __half2 hv = __floats2half2_rn(x[i] * up, x[i + 4] * up);
+      const float2 f = __half22float2(hv);
+      sum += f.x + f.y;
+      w[i] = *(const uint32_t*)&hv;
+    }
+#pragma unroll
+    for (int o = 1; o < TPR; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (b < 0) continue;
+    const int kvh = head / a.group, g = head - kvh * a.group, sub = g / s.gt;
+    const int row = off % s.tpm * s.gt + (g - sub * s.gt);
+    uint8_t* img = p.q + ((int64_t)(kvh * s.nsub + sub) * p.q_tiles + row_tile(tok - off, b, off, s.tpm)) * C::QIMG;
+    *(uint4*)(img + (j >> 3) * 16384 + row * 128 + (((j & 7) ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (j < 2) {
+      // sum(q) in three parts, against the keys' m and 8 s
+      const __half s0 = __float2half_rn(sum);
+      const float d1 = sum - __half2float(s0);
+      const __half s1 = __float2half_rn(d1), s2 = __float2half_rn(d1 - __half2float(s1));
+      const __half2 a0 = __halves2half2(s0, s1), a1 = __halves2half2(s2, s0), a2 = __halves2half2(s1, s2);
+      *(uint4*)(img + C::MAIN + (row >> 3) * 256 + j * 128 + (row & 7) * 16) =
+          j ? make_uint4(0u, 0u, 0u, 0u) : make_uint4(*(const uint32_t*)&a0, *(const uint32_t*)&a1, *(const uint32_t*)&a2, 0u);
+      if (j) *(float*)(img + C::OP + 4 * row) = a.scale * 1.4426950408889634f * __int_as_float((127 - e2) << 23);
+    }
+  }
 }
 
 // ---------------------------------------------------------------- tensor memory, packed floats
@@ -394,17 +476,16 @@ template <int D> __device__ __forceinline__ void row_scale(uint32_t t_o, float f
   sm100::tmem_wait_st();
 }
 
-template <typename T, typename TO, int D>
+template <typename TO, int D>
 __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
-k_prefill4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, AttnArgs a, Shape sh, Plan plan) {
+k_prefill4(Pool c, RopeArgs r, TO* __restrict__ out, AttnArgs a, Shape sh, Plan plan) {
   using C = Cfg<D>;
-  constexpr int NS = C::NS, NU = C::NU, NKV = C::NKV, TPR = D / 8, CH = D / 32 / NU;
+  constexpr int NS = C::NS, NU = C::NU, NKV = C::NKV, CH = D / 32 / NU;
   constexpr int kIssuer = (NS + NU) * 4;        // the warp that issues the products
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t b_q, b_fin, b_s[2], b_p[2], b_o[NS], b_kf[NKV], b_ke[NKV], b_vf[NKV], b_ve[NKV], b_i[kInfo];
   __shared__ uint32_t s_tmem;
   __shared__ Info s_info[kInfo];
-  __shared__ float s_fq[NS][M];
   __shared__ uint32_t s_red[NU][2][4][2];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -417,7 +498,7 @@ k_prefill4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, At
   const int ns = u.n > sh.tpm ? NS : 1, nt = u.nt;
   if (warp == kIssuer) sm100::tmem_alloc(&s_tmem, 512);
   if (tid == 0) {
-    sm100::mbar_init(&b_q, ns * kGroup);
+    sm100::mbar_init(&b_q, 1);
     sm100::mbar_init(&b_fin, 1);
     for (int i = 0; i < 2; ++i) {
       sm100::mbar_init(&b_s[i], 1);
@@ -446,76 +527,6 @@ k_prefill4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, At
     // ------------------------------------------------------------ queries, softmax, outputs
     const int i = warp >> 2, wt = tid & 127;
     if (i < ns) {
-      uint8_t* qop = smem + C::Q + i * C::OP;
-      constexpr int RP = kGroup / TPR, BATCH = 4;
-      const int j = wt % TPR;
-      for (int r0 = 0; r0 < M; r0 += RP * BATCH) {
-        Vec8<T> own[BATCH], part[BATCH];
-        int64_t pos[BATCH];
-        bool has[BATCH];
-        const int pi = partner(8 * j, r);
-#pragma unroll
-        for (int n = 0; n < BATCH; ++n) {
-          const int row = r0 + n * RP + wt / TPR, ti = i * sh.tpm + row / sh.gt, hh = row % sh.gt;
-          pos[n] = min(u.pos + ti, cap - 1);
-          has[n] = row < sh.tpm * sh.gt && ti < u.n && hh < nh && pos[n] >= 0 && !(r.table && pos[n] >= r.n_pos);
-          if (has[n]) {
-            const T* x = q + (int64_t)(u.tok + ti) * a.qs_tok + (int64_t)(h0 + hh) * a.qs_head;
-            own[n] = load8<T>(x + 8 * j);
-            if (r.table && pi != 8 * j) part[n] = load8<T>(x + pi);
-          }
-        }
-#pragma unroll
-        for (int n = 0; n < BATCH; ++n) {
-          const int row = r0 + n * RP + wt / TPR;
-          float x[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = 0.0f;
-          if (has[n]) {
-            unpack8<T>(own[n], x);
-            if (r.table) {
-              float y[8];
-              if (pi != 8 * j) unpack8<T>(part[n], y);
-              rotate8<T>(x, y, 8 * j, r, pos[n]);
-            }
-          }
-          float top = 0.0f;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[e]));
-#pragma unroll
-          for (int o = 1; o < TPR; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          // 2^e with top 2^e in [2^6, 2^7): the sum over a head stays below 2^15
-          int e2 = 0;
-          if (top > 0.0f && top < INFINITY) e2 = max(-100, min(100, 6 - ilogbf(top)));
-          const float up = ldexpf(1.0f, e2);
-          float sum = 0.0f;
-          uint32_t w[4];
-#pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            const __half2 hv = __floats2half2_rn(x[p] * up, x[p + 4] * up);
-            const float2 f = __half22float2(hv);
-            sum += f.x + f.y;
-            w[p] = *(const uint32_t*)&hv;
-          }
-#pragma unroll
-          for (int o = 1; o < TPR; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-          *(uint4*)(qop + (j >> 3) * 16384 + row * 128 + (((j & 7) ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-          if (j == 0) {
-            const __half s0 = __float2half_rn(sum);
-            const float d1 = sum - __half2float(s0);
-            const __half s1 = __float2half_rn(d1), s2 = __float2half_rn(d1 - __half2float(s1));
-            const __half2 a0 = __halves2half2(s0, s1), a1 = __halves2half2(s2, s0), a2 = __halves2half2(s1, s2);
-            uint8_t* ext = qop + C::MAIN + (row >> 3) * 256 + (row & 7) * 16;
-            *(uint4*)ext = make_uint4(*(const uint32_t*)&a0, *(const uint32_t*)&a1, *(const uint32_t*)&a2, 0u);
-            *(uint4*)(ext + 128) = make_uint4(0u, 0u, 0u, 0u);
-            s_fq[i][row] = a.scale * 1.4426950408889634f * ldexpf(1.0f, -e2);
-          }
-        }
-      }
-      sm100::fence_async_smem();
-      sm100::mbar_arrive(&b_q);
-      sm100::named_bar(1 + i, kGroup);
-
       const int ti = i * sh.tpm + wt / sh.gt, hh = wt % sh.gt;
       const bool is_row = wt < sh.tpm * sh.gt && ti < u.n && hh < nh;
       // keys [lo, hi] of the row; rows that are none take any, so that they ask for no masks
@@ -526,7 +537,8 @@ k_prefill4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, At
         lo = a.window > 0 && p - a.window + 1 > 0 ? (int)(p - a.window + 1) : 0;
       }
       const int w_lo = __reduce_max_sync(0xffffffffu, lo), w_hi = __reduce_min_sync(0xffffffffu, hi);
-      const float fq = s_fq[i][wt];
+      const int64_t tile = (int64_t)u.hs * plan.q_tiles + row_tile(u.tok - u.off, u.row, u.off, sh.tpm) + i;
+      const float fq = is_row ? *(const float*)(plan.q + tile * C::QIMG + C::OP + 4 * wt) : 0.0f;
       const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
       const uint32_t t_o = tmem + lanes + 256 + i * D;
       float mref = -INFINITY, vref = 0.0f;
@@ -548,9 +560,9 @@ k_prefill4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, At
         const float* mean = (const float*)(smem + C::MEAN) + ring * KT;
         const float top = fk * (edge ? row_max_edge(t_s, &in, key0, lo, hi) : row_max(t_s));
         const float nv = in.vref;
-        if (__any_sync(0xffffffffu, !(top <= mref + kSlack) || nv != vref)) {
+        if (__any_sync(0xffffffffu, (is_row && top > mref + kSlack) || nv != vref)) {
           float f = 1.0f;
-          if (top > mref) {
+          if (is_row && top > mref) {
             f = dec::ex2(mref - top);            // 0 the first time
             mref = top;
           }
@@ -780,6 +792,12 @@ k_prefill4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, At
     if (warp == kIssuer && lane == 0 && nt > 0) {
       const uint32_t base = sm100::smem_u32(smem);
       constexpr uint32_t id_s = sm100::idesc_f16(M, KT), id_o = sm100::idesc_f16(M, D) | (1u << 16);   // values: n-major
+      asm volatile("fence.proxy.async.global;" ::: "memory");
+      sm100::mbar_expect_tx(&b_q, ns * C::OP);
+      for (int i = 0; i < ns; ++i)
+        sm100::bulk_load(smem + C::Q + i * C::OP,
+                         plan.q + ((int64_t)u.hs * plan.q_tiles + row_tile(u.tok - u.off, u.row, u.off, sh.tpm) + i) * C::QIMG,
+                         C::OP, &b_q);
       bool dead = !sm100::mbar_wait(&b_q, 0, a.flags);
       auto scores = [&](int i, int k) {
         const uint32_t qa = base + C::Q + i * C::OP, ka = base + C::K + (k % NKV) * C::OP;
