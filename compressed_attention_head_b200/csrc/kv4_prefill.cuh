@@ -850,39 +850,22 @@ k_prefill4(Pool c, RopeArgs r, TO* __restrict__ out, AttnArgs a, Shape sh, Plan 
           }
         }
       } else if (wait_k(0)) {
-        // Whichever row tile has its next operand is served: its probabilities, or the end of its last sum.
+        // One row tile's sum and next scores, then the other's: so their softmaxes fall into opposite phases,
+        // and each has the exponential units to itself.
         scores(0, 0);
         scores(1, 0);
         sm100::mma_commit(&b_ke[0]);
-        int at[2] = {0, 0};                       // tiles of a row tile
-        bool summing[2] = {false, false};         // it waits for the end of a sum
-        uint64_t since = 0;
-        for (uint32_t idle = 0; !dead && (at[0] < nt || at[1] < nt); ++idle) {
-#pragma unroll
+        for (int k = 0; k < nt && !dead; ++k) {
           for (int i = 0; i < 2; ++i) {
-            const int k = at[i];
-            if (k >= nt || !sm100::mbar_test(summing[i] ? &b_o[i % NS] : &b_p[i], k & 1)) continue;
-            idle = 0;
-            if (!summing[i]) {
-              if (!wait_v(k)) break;
-              sums(i, k);
-              if (at[i ^ 1] > k || (at[i ^ 1] == k && summing[i ^ 1])) sm100::mma_commit(&b_ve[k % NKV]);     // the second to read them
-              summing[i] = true;
-              if (k + 1 == nt) at[i] = nt;
-            } else {
+            dead = dead || !sm100::mbar_wait(&b_p[i], k & 1, a.flags);
+            if (!wait_v(k)) break;
+            sums(i, k);
+            if (i == 1) sm100::mma_commit(&b_ve[k % NKV]);
+            if (k + 1 < nt) {
+              dead = !sm100::mbar_wait(&b_o[i % NS], k & 1, a.flags);
               if (!wait_k(k + 1)) break;
               scores(i, k + 1);
-              if (at[i ^ 1] > k) sm100::mma_commit(&b_ke[(k + 1) % NKV]);
-              summing[i] = false;
-              at[i] = k + 1;
-            }
-          }
-          if ((idle & 1023u) == 1023u) {
-            const uint64_t now = sm100::global_ns();
-            if (idle == 1023u) since = now;
-            if (now - since > sm100::kTimeoutNs) {
-              raise(a.flags, SQ_FLAG_TIMEOUT);
-              dead = true;
+              if (i == 1) sm100::mma_commit(&b_ke[(k + 1) % NKV]);
             }
           }
         }
