@@ -39,10 +39,10 @@ constexpr float kUp = 11.0f;                  // log2 of the probabilities' scal
 
 template <int D> struct Cfg {
   static constexpr int NS = D == 256 ? 1 : 2;          // row tiles of a block
-  static constexpr int NU = D == 256 ? 2 : 1;          // warp groups that unpack, each a share of the coordinates
+  static constexpr int NU = 2;                         // warp groups that unpack, each half of the coordinates
   static constexpr int THREADS = (NS + NU + 1) * kGroup;
-  // Registers a thread: the softmax's from what the others give up, 512 threads x 128 in all.
-  static constexpr int R_SOFT = 160, R_UNPACK = NU == 2 ? 144 : 128, R_MMA = 64;
+  // Registers a thread: 640 x 96 or 512 x 128 in all, the softmax's from what the others give up.
+  static constexpr int R_SOFT = NS == 2 ? 144 : 160, R_UNPACK = NS == 2 ? 72 : 144, R_MMA = NS == 2 ? 48 : 64;
   static constexpr int NKV = D == 256 ? 1 : 2;         // stages of unpacked keys and values
   static constexpr int MAIN = (D / 64) * 16384;        // 128 rows x D fp16, 64 coordinates a slab
   static constexpr int OP = MAIN + 4096;               // and the step that carries the offsets
@@ -406,33 +406,43 @@ __device__ __forceinline__ float row_max_edge(uint32_t t_s, const Info* in, int 
   return m;
 }
 
-// Two probabilities: their sum, their sum with the offsets, and the pair in fp16.
-__device__ __forceinline__ uint32_t two_probs(f2 t, f2 mean, f2* lsum, f2* msum) {
-  const float p0 = dec::ex2(f2_lo(t)), p1 = dec::ex2(f2_hi(t));
-  const f2 p = f2_of(p0, p1);
-  *lsum = f2_add(*lsum, p);
-  *msum = f2_fma(p, mean, *msum);
-  return dec::pack_h2(p0, p1);
-}
-
-// Scores to probabilities 2^(s fk + nb), which take the place of the scores' first half.
+// Scores to probabilities 2^(s fk + nb), which take the place of the scores' first
+// half; *lsum and *msum grow by their sum and their sum with the offsets. The sums
+// and roundings of 32 keys are written beside the exponentials of the next 32.
 __device__ __forceinline__ void row_probs(uint32_t t_s, float fk, float nb, const float* mean, f2* lsum, f2* msum) {
   const f2 fk2 = f2_of(fk, fk), nb2 = f2_of(nb, nb);
   uint32_t s[2][32];
+  float p[32];
   ld32(t_s, s[0]);
 #pragma unroll
-  for (int ch = 0; ch < 4; ++ch) {
+  for (int ch = 0; ch <= 4; ++ch) {
     uint32_t* x = s[ch & 1];
-    ld_wait(x);
-    if (ch < 3) ld32(t_s + 32 * (ch + 1), s[(ch + 1) & 1]);
     uint32_t pk[16];
+    if (ch < 4) {
+      ld_wait(x);
+      if (ch < 3) ld32(t_s + 32 * (ch + 1), s[(ch + 1) & 1]);
+    }
 #pragma unroll
     for (int e = 0; e < 32; e += 4) {
-      const ulonglong2 mu = *(const ulonglong2*)(mean + 32 * ch + e);
-      pk[e / 2] = two_probs(f2_fma(f2_of(x[e], x[e + 1]), fk2, nb2), mu.x, lsum, msum);
-      pk[e / 2 + 1] = two_probs(f2_fma(f2_of(x[e + 2], x[e + 3]), fk2, nb2), mu.y, lsum, msum);
+      if (ch > 0) {
+        const ulonglong2 mu = *(const ulonglong2*)(mean + 32 * (ch - 1) + e);
+        const f2 pa = f2_of(p[e], p[e + 1]), pb = f2_of(p[e + 2], p[e + 3]);
+        *lsum = f2_add(*lsum, pa);
+        *msum = f2_fma(pa, mu.x, *msum);
+        *lsum = f2_add(*lsum, pb);
+        *msum = f2_fma(pb, mu.y, *msum);
+        pk[e / 2] = dec::pack_h2(p[e], p[e + 1]);
+        pk[e / 2 + 1] = dec::pack_h2(p[e + 2], p[e + 3]);
+      }
+      if (ch < 4) {
+        const f2 ta = f2_fma(f2_of(x[e], x[e + 1]), fk2, nb2), tb = f2_fma(f2_of(x[e + 2], x[e + 3]), fk2, nb2);
+        p[e] = dec::ex2(f2_lo(ta));
+        p[e + 1] = dec::ex2(f2_hi(ta));
+        p[e + 2] = dec::ex2(f2_lo(tb));
+        p[e + 3] = dec::ex2(f2_hi(tb));
+      }
     }
-    st16(t_s + 16 * ch, pk);
+    if (ch > 0) st16(t_s + 16 * (ch - 1), pk);
   }
 }
 struct Sums { f2 l, m; };
@@ -449,8 +459,11 @@ __device__ __forceinline__ Sums row_probs_edge(uint32_t t_s, float fk, float nb,
       const bool k0 = (keep >> e) & 1u, k1 = (keep >> (e + 1)) & 1u;
       const float t0 = fmaf(__uint_as_float(x[e]), fk, nb), t1 = fmaf(__uint_as_float(x[e + 1]), fk, nb);
       const float m0 = mean[32 * ch + e], m1 = mean[32 * ch + e + 1];
-      pk[e / 2] = two_probs(f2_of(k0 ? t0 : -INFINITY, k1 ? t1 : -INFINITY), f2_of(k0 ? m0 : 0.0f, k1 ? m1 : 0.0f), &sum.l,
-                            &sum.m);
+      const float p0 = dec::ex2(k0 ? t0 : -INFINITY), p1 = dec::ex2(k1 ? t1 : -INFINITY);
+      const f2 p = f2_of(p0, p1);
+      sum.l = f2_add(sum.l, p);
+      sum.m = f2_fma(p, f2_of(k0 ? m0 : 0.0f, k1 ? m1 : 0.0f), sum.m);
+      pk[e / 2] = dec::pack_h2(p0, p1);
     }
     st16(t_s + 16 * ch, pk);
   }
@@ -487,7 +500,7 @@ k_prefill4(Pool c, RopeArgs r, TO* __restrict__ out, AttnArgs a, Shape sh, Plan 
   __shared__ uint32_t s_tmem;
   __shared__ Info s_info[kInfo];
   __shared__ uint32_t s_red[NU][2][4][2];
-  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t* smem = smem_raw + ((1024u - (sm100::smem_u32(smem_raw) & 1023u)) & 1023u);   // (kept a shared address)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -643,7 +656,7 @@ k_prefill4(Pool c, RopeArgs r, TO* __restrict__ out, AttnArgs a, Shape sh, Plan 
     }
   } else if (warp < kIssuer) {
     // ------------------------------------------------------------ unpacking: a thread a key, a group its share of the chunks
-    if constexpr (C::R_UNPACK > 128) set_regs_up<C::R_UNPACK>();
+    if constexpr (NS == 1) set_regs_up<C::R_UNPACK>(); else set_regs_down<C::R_UNPACK>();
     const int dt = tid & 127, uw = warp & 3, share = (warp >> 2) - NS, ch0 = share * CH;
     int64_t ulo, uhi;
     unit_keys(c, r, a, u.pos, u.n, &ulo, &uhi);
