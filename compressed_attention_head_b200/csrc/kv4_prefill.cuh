@@ -501,7 +501,7 @@ k_prefill4(Pool c, RopeArgs r, TO* __restrict__ out, AttnArgs a, Shape sh, Plan 
   __shared__ Info s_info[kInfo];
   __shared__ uint32_t s_red[NU][2][4][2];
   uint8_t* smem = smem_raw + ((1024u - (sm100::smem_u32(smem_raw) & 1023u)) & 1023u);   // (kept a shared address)
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -802,89 +802,88 @@ k_prefill4(Pool c, RopeArgs r, TO* __restrict__ out, AttnArgs a, Shape sh, Plan 
   } else {
     // ------------------------------------------------------------ products
     set_regs_down<C::R_MMA>();
-    if (warp == kIssuer && lane == 0 && nt > 0) {
+    if (warp == kIssuer && nt > 0) {
+      // Unrolled, with the addresses of the steps folded into the descriptors: a step is then issued within the
+      // 64 cycles that it takes (128 rows x 128 x 16); in a rolled loop issuing one takes more than 200.
       const uint32_t base = sm100::smem_u32(smem);
       constexpr uint32_t id_s = sm100::idesc_f16(M, KT), id_o = sm100::idesc_f16(M, D) | (1u << 16);   // values: n-major
-      asm volatile("fence.proxy.async.global;" ::: "memory");
-      sm100::mbar_expect_tx(&b_q, ns * C::OP);
-      for (int i = 0; i < ns; ++i)
-        sm100::bulk_load(smem + C::Q + i * C::OP,
-                         plan.q + ((int64_t)u.hs * plan.q_tiles + row_tile(u.tok - u.off, u.row, u.off, sh.tpm) + i) * C::QIMG,
-                         C::OP, &b_q);
-      bool dead = !sm100::mbar_wait(&b_q, 0, a.flags);
-      auto scores = [&](int i, int k) {
-        const uint32_t qa = base + C::Q + i * C::OP, ka = base + C::K + (k % NKV) * C::OP;
-        const uint32_t d = tmem + 128 * (ns == 2 ? i : (k & 1));
-        const uint64_t qd = desc_of(qa, 16, 1024, 2), kd = desc_of(ka, 16, 1024, 2);
-#pragma unroll 4
-        for (int s = 0; s < D / 16; ++s) {
-          const uint64_t off = (uint64_t)((s >> 2) * 1024 + (s & 3) * 2);       // in units of 16 bytes
-          sm100::mma_f16(d, qd + off, kd + off, id_s, s > 0 ? 1u : 0u);
-        }
-        sm100::mma_f16(d, desc_of(qa + C::MAIN, 128, 256, 0), desc_of(ka + C::MAIN, 128, 256, 0), id_s, 1u);
-        sm100::mma_commit(&b_s[ns == 2 ? i : (k & 1)]);
+      bool dead = false;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        dead = __any_sync(0xffffffffu, dead || !sm100::mbar_wait(bar, parity, a.flags));
+        sm100::tc_fence_after();
+        return !dead;
       };
-      auto sums = [&](int i, int k) {
+      auto scores = [&](int i, int k, bool last) {
+        const uint32_t qa = base + C::Q + i * C::OP, ka = base + C::K + (k % NKV) * C::OP;
+        const int sl = ns == 2 ? i : (k & 1);
+        const uint32_t d = tmem + 128 * sl;
+        const uint64_t qd = desc_of(qa, 16, 1024, 2), kd = desc_of(ka, 16, 1024, 2);
+        const uint64_t qe = desc_of(qa + C::MAIN, 128, 256, 0), ke = desc_of(ka + C::MAIN, 128, 256, 0);
+        if (sm100::elect_one()) {
+#pragma unroll
+          for (int s = 0; s < D / 16; ++s) {
+            const uint64_t off = (uint64_t)((s >> 2) * 1024 + (s & 3) * 2);       // in units of 16 bytes
+            sm100::mma_f16(d, qd + off, kd + off, id_s, s > 0 ? 1u : 0u);
+          }
+          sm100::mma_f16(d, qe, ke, id_s, 1u);
+          sm100::mma_commit(&b_s[sl]);
+          if (last) sm100::mma_commit(&b_ke[k % NKV]);
+        }
+        __syncwarp();
+      };
+      auto sums = [&](int i, int k, bool last) {
         const uint32_t va = base + C::V + (k % NKV) * C::MAIN;
         const uint32_t p = tmem + 128 * (ns == 2 ? i : (k & 1)), d = tmem + 256 + i * D;
         const uint64_t vd = desc_of(va, 16384, 1024, 2);
-#pragma unroll 4
-        for (int s = 0; s < KT / 16; ++s) sm100::mma_f16_ts(d, p + 8 * s, vd + 128 * s, id_o, (k | s) ? 1u : 0u);
-        sm100::mma_commit(&b_o[i]);
+        if (sm100::elect_one()) {
+#pragma unroll
+          for (int s = 0; s < KT / 16; ++s) sm100::mma_f16_ts(d, p + 8 * s, vd + 128 * s, id_o, (s > 0 || k > 0) ? 1u : 0u);
+          sm100::mma_commit(&b_o[i]);
+          if (last) sm100::mma_commit(&b_ve[k % NKV]);
+        }
+        __syncwarp();
       };
-      auto wait_k = [&](int k) {
-        dead = dead || !sm100::mbar_wait(&b_kf[k % NKV], (k / NKV) & 1, a.flags);
-        sm100::tc_fence_after();
-        return !dead;
-      };
-      auto wait_v = [&](int k) {
-        dead = dead || !sm100::mbar_wait(&b_vf[k % NKV], (k / NKV) & 1, a.flags);
-        sm100::tc_fence_after();
-        return !dead;
-      };
+      if (sm100::elect_one()) {
+        asm volatile("fence.proxy.async.global;" ::: "memory");
+        sm100::mbar_expect_tx(&b_q, ns * C::OP);
+        for (int i = 0; i < ns; ++i)
+          sm100::bulk_load(smem + C::Q + i * C::OP,
+                           plan.q + ((int64_t)u.hs * plan.q_tiles + row_tile(u.tok - u.off, u.row, u.off, sh.tpm) + i) * C::QIMG,
+                           C::OP, &b_q);
+      }
+      __syncwarp();
+      wait(&b_q, 0);
       // Scores may not take the place of probabilities before the product that reads those has ended: products
       // of different accumulators are not ordered among each other, so the end is waited for.
       if (ns == 1) {
-        for (int k = 0; k < 2 && k < nt; ++k) {
-          if (!wait_k(k)) break;
-          scores(0, k);
-          sm100::mma_commit(&b_ke[k % NKV]);
-        }
+        for (int k = 0; k < 2 && k < nt && wait(&b_kf[k % NKV], (k / NKV) & 1); ++k) scores(0, k, true);
         for (int k = 0; k < nt && !dead; ++k) {
-          dead = !sm100::mbar_wait(&b_p[k & 1], (k >> 1) & 1, a.flags);
-          if (!wait_v(k)) break;
-          sums(0, k);
-          sm100::mma_commit(&b_ve[k % NKV]);
+          if (!wait(&b_p[k & 1], (k >> 1) & 1) || !wait(&b_vf[k % NKV], (k / NKV) & 1)) break;
+          sums(0, k, true);
           if (k + 2 < nt) {
-            dead = !sm100::mbar_wait(&b_o[0], k & 1, a.flags);
-            if (!wait_k(k + 2)) break;
-            scores(0, k + 2);
-            sm100::mma_commit(&b_ke[k % NKV]);
+            if (!wait(&b_o[0], k & 1) || !wait(&b_kf[k % NKV], ((k + 2) / NKV) & 1)) break;
+            scores(0, k + 2, true);
           }
         }
-      } else if (wait_k(0)) {
+      } else if (wait(&b_kf[0], 0)) {
         // One row tile's sum and next scores, then the other's: so their softmaxes fall into opposite phases,
         // and each has the exponential units to itself.
-        scores(0, 0);
-        scores(1, 0);
-        sm100::mma_commit(&b_ke[0]);
+        scores(0, 0, false);
+        scores(1, 0, true);
         for (int k = 0; k < nt && !dead; ++k) {
           for (int i = 0; i < 2; ++i) {
-            dead = dead || !sm100::mbar_wait(&b_p[i], k & 1, a.flags);
-            if (!wait_v(k)) break;
-            sums(i, k);
-            if (i == 1) sm100::mma_commit(&b_ve[k % NKV]);
+            if (!wait(&b_p[i], k & 1) || !wait(&b_vf[k % NKV], (k / NKV) & 1)) break;
+            sums(i % NS, k, i == 1);
             if (k + 1 < nt) {
-              dead = !sm100::mbar_wait(&b_o[i % NS], k & 1, a.flags);
-              if (!wait_k(k + 1)) break;
-              scores(i, k + 1);
-              if (i == 1) sm100::mma_commit(&b_ke[(k + 1) % NKV]);
+              if (!wait(&b_o[i % NS], k & 1) || !wait(&b_kf[(k + 1) % NKV], ((k + 1) / NKV) & 1)) break;
+              scores(i, k + 1, i == 1);
             }
           }
         }
       }
       // nothing of this block is in flight when it gives its tensor memory back
-      sm100::mma_commit(&b_fin);
+      if (sm100::elect_one()) sm100::mma_commit(&b_fin);
+      __syncwarp();
       sm100::mbar_wait(&b_fin, 0, a.flags);
     }
     __syncwarp();
