@@ -39,10 +39,11 @@ constexpr float kUp = 11.0f;                  // log2 of the probabilities' scal
 
 template <int D> struct Cfg {
   static constexpr int NS = D == 256 ? 1 : 2;          // row tiles of a block
-  static constexpr int NU = 2;                         // warp groups that unpack, each half of the coordinates
-  static constexpr int THREADS = (NS + NU + 1) * kGroup;
-  // Registers a thread: 640 x 96 or 512 x 128 in all, the softmax's from what the others give up.
-  static constexpr int R_SOFT = NS == 2 ? 144 : 160, R_UNPACK = NS == 2 ? 72 : 144, R_MMA = NS == 2 ? 48 : 64;
+  // Warp groups: two softmax a row tile (each half of the keys: one warp a scheduler would wait for its own
+  // latencies), two that unpack, one that issues.
+  static constexpr int SOFT = 2 * NS, THREADS = (SOFT + 3) * kGroup;
+  // Registers a thread: 896 x 72 or 640 x 96 in all, the softmax's from what the issuers give up.
+  static constexpr int R_SOFT = NS == 2 ? 88 : 112, R_UNPACK = NS == 2 ? 56 : 104, R_MMA = NS == 2 ? 40 : 48;
   static constexpr int NKV = D == 256 ? 1 : 2;         // stages of unpacked keys and values
   static constexpr int MAIN = (D / 64) * 16384;        // 128 rows x D fp16, 64 coordinates a slab
   static constexpr int OP = MAIN + 4096;               // and the step that carries the offsets
@@ -300,6 +301,19 @@ __device__ __forceinline__ void ld_wait(uint32_t* r) {
                  "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
                  "+r"(r[30]), "+r"(r[31])::"memory");
 }
+__device__ __forceinline__ void ld16(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
+}
+__device__ __forceinline__ void ld_wait16(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               ::"memory");
+}
 __device__ __forceinline__ void st16(uint32_t addr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
@@ -373,64 +387,63 @@ __device__ __forceinline__ uint32_t keys_kept(uint32_t ok, int from, int lo, int
   return ok & (y >= 31 ? 0xffffffffu : (y < 0 ? 0u : 0xffffffffu >> (31 - y)));
 }
 
-// The largest of a row's scores of one tile, as they lie in tensor memory.
+// A thread's share of a tile: a row's scores against 64 keys, 64 columns of tensor
+// memory from t_s on. Their largest:
 __device__ __forceinline__ float row_max(uint32_t t_s) {
-  uint32_t s[2][32];
+  uint32_t x[32], y[32];
+  ld32(t_s, x);
+  ld32(t_s + 32, y);
+  ld_wait(x);
+  ld_wait(y);
   float m0 = -INFINITY, m1 = -INFINITY;
-  ld32(t_s, s[0]);
 #pragma unroll
-  for (int ch = 0; ch < 4; ++ch) {
-    uint32_t* x = s[ch & 1];
-    ld_wait(x);
-    if (ch < 3) ld32(t_s + 32 * (ch + 1), s[(ch + 1) & 1]);
-#pragma unroll
-    for (int e = 0; e < 32; e += 4) {
-      m0 = fmaxf(m0, fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 1])));
-      m1 = fmaxf(m1, fmaxf(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])));
-    }
+  for (int e = 0; e < 32; e += 2) {
+    m0 = fmaxf(m0, fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 1])));
+    m1 = fmaxf(m1, fmaxf(__uint_as_float(y[e]), __uint_as_float(y[e + 1])));
   }
   return fmaxf(m0, m1);
 }
-// The same of the keys that the row attends (few tiles: short code rather than fast).
-__device__ __forceinline__ float row_max_edge(uint32_t t_s, const Info* in, int key0, int lo, int hi) {
+// The same of the keys that the row attends (few tiles: short code rather than fast). ok: two words.
+__device__ __forceinline__ float row_max_edge(uint32_t t_s, const uint32_t* ok, int key0, int lo, int hi) {
   float m = -INFINITY;
 #pragma unroll 1
   for (int ch = 0; ch < 4; ++ch) {
-    uint32_t x[32];
-    ld32(t_s + 32 * ch, x);
-    const uint32_t keep = keys_kept(in->ok[ch], key0 + 32 * ch, lo, hi);
-    ld_wait(x);
+    uint32_t x[16];
+    ld16(t_s + 16 * ch, x);
+    const uint32_t keep = keys_kept(ok[ch >> 1], key0 + 32 * (ch >> 1), lo, hi) >> (16 * (ch & 1));
+    ld_wait16(x);
 #pragma unroll
-    for (int e = 0; e < 32; ++e) m = (keep >> e) & 1u ? fmaxf(m, __uint_as_float(x[e])) : m;
+    for (int e = 0; e < 16; ++e) m = (keep >> e) & 1u ? fmaxf(m, __uint_as_float(x[e])) : m;
   }
   return m;
 }
 
-// Scores to probabilities 2^(s fk + nb), which take the place of the scores' first
-// half; *lsum and *msum grow by their sum and their sum with the offsets. The sums
-// and roundings of 32 keys are written beside the exponentials of the next 32.
-__device__ __forceinline__ void row_probs(uint32_t t_s, float fk, float nb, const float* mean, f2* lsum, f2* msum) {
+struct Sums { f2 l, m; };
+// Scores to probabilities 2^(s fk + nb), which take the place of the first half of
+// them; the sums grow by their sum and their sum with the offsets. The sums and
+// roundings of 16 keys are written beside the exponentials of the next 16.
+__device__ __forceinline__ Sums row_probs(uint32_t t_s, float fk, float nb, const float* mean, Sums sum) {
   const f2 fk2 = f2_of(fk, fk), nb2 = f2_of(nb, nb);
-  uint32_t s[2][32];
-  float p[32];
-  ld32(t_s, s[0]);
+  uint32_t s[2][16];
+  float p[16];
+  ld16(t_s, s[0]);
 #pragma unroll
   for (int ch = 0; ch <= 4; ++ch) {
     uint32_t* x = s[ch & 1];
-    uint32_t pk[16];
+    uint32_t pk[8];
     if (ch < 4) {
-      ld_wait(x);
-      if (ch < 3) ld32(t_s + 32 * (ch + 1), s[(ch + 1) & 1]);
+      ld_wait16(x);
+      if (ch < 3) ld16(t_s + 16 * (ch + 1), s[(ch + 1) & 1]);
     }
 #pragma unroll
-    for (int e = 0; e < 32; e += 4) {
+    for (int e = 0; e < 16; e += 4) {
       if (ch > 0) {
-        const ulonglong2 mu = *(const ulonglong2*)(mean + 32 * (ch - 1) + e);
+        const ulonglong2 mu = *(const ulonglong2*)(mean + 16 * (ch - 1) + e);
         const f2 pa = f2_of(p[e], p[e + 1]), pb = f2_of(p[e + 2], p[e + 3]);
-        *lsum = f2_add(*lsum, pa);
-        *msum = f2_fma(pa, mu.x, *msum);
-        *lsum = f2_add(*lsum, pb);
-        *msum = f2_fma(pb, mu.y, *msum);
+        sum.l = f2_add(sum.l, pa);
+        sum.m = f2_fma(pa, mu.x, sum.m);
+        sum.l = f2_add(sum.l, pb);
+        sum.m = f2_fma(pb, mu.y, sum.m);
         pk[e / 2] = dec::pack_h2(p[e], p[e + 1]);
         pk[e / 2 + 1] = dec::pack_h2(p[e + 2], p[e + 3]);
       }
@@ -442,38 +455,38 @@ __device__ __forceinline__ void row_probs(uint32_t t_s, float fk, float nb, cons
         p[e + 3] = dec::ex2(f2_hi(tb));
       }
     }
-    if (ch > 0) st16(t_s + 16 * (ch - 1), pk);
+    if (ch > 0) sm100::tmem_st8(t_s + 8 * (ch - 1), pk);
   }
+  return sum;
 }
-struct Sums { f2 l, m; };
-__device__ __forceinline__ Sums row_probs_edge(uint32_t t_s, float fk, float nb, const float* mean, Sums sum, const Info* in,
-                                            int key0, int lo, int hi) {
+__device__ __forceinline__ Sums row_probs_edge(uint32_t t_s, float fk, float nb, const float* mean, Sums sum,
+                                               const uint32_t* ok, int key0, int lo, int hi) {
 #pragma unroll 1
   for (int ch = 0; ch < 4; ++ch) {
-    uint32_t x[32], pk[16];
-    ld32(t_s + 32 * ch, x);
-    const uint32_t keep = keys_kept(in->ok[ch], key0 + 32 * ch, lo, hi);
-    ld_wait(x);
+    uint32_t x[16], pk[8];
+    ld16(t_s + 16 * ch, x);
+    const uint32_t keep = keys_kept(ok[ch >> 1], key0 + 32 * (ch >> 1), lo, hi) >> (16 * (ch & 1));
+    ld_wait16(x);
 #pragma unroll
-    for (int e = 0; e < 32; e += 2) {
+    for (int e = 0; e < 16; e += 2) {
       const bool k0 = (keep >> e) & 1u, k1 = (keep >> (e + 1)) & 1u;
       const float t0 = fmaf(__uint_as_float(x[e]), fk, nb), t1 = fmaf(__uint_as_float(x[e + 1]), fk, nb);
-      const float m0 = mean[32 * ch + e], m1 = mean[32 * ch + e + 1];
+      const float m0 = mean[16 * ch + e], m1 = mean[16 * ch + e + 1];
       const float p0 = dec::ex2(k0 ? t0 : -INFINITY), p1 = dec::ex2(k1 ? t1 : -INFINITY);
       const f2 p = f2_of(p0, p1);
       sum.l = f2_add(sum.l, p);
       sum.m = f2_fma(p, f2_of(k0 ? m0 : 0.0f, k1 ? m1 : 0.0f), sum.m);
       pk[e / 2] = dec::pack_h2(p0, p1);
     }
-    st16(t_s + 16 * ch, pk);
+    sm100::tmem_st8(t_s + 8 * ch, pk);
   }
   return sum;
 }
-// Scales a row's sums in tensor memory.
-template <int D> __device__ __forceinline__ void row_scale(uint32_t t_o, float f) {
+// Scales N of a row's sums in tensor memory.
+template <int N> __device__ __forceinline__ void row_scale(uint32_t t_o, float f) {
   const f2 f2v = f2_of(f, f);
 #pragma unroll 1
-  for (int ch = 0; ch < D / 32; ++ch) {
+  for (int ch = 0; ch < N / 32; ++ch) {
     uint32_t x[32];
     ld32(t_o + 32 * ch, x);
     ld_wait(x);
@@ -493,13 +506,15 @@ template <typename TO, int D>
 __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
 k_prefill4(Pool c, RopeArgs r, TO* __restrict__ out, AttnArgs a, Shape sh, Plan plan) {
   using C = Cfg<D>;
-  constexpr int NS = C::NS, NU = C::NU, NKV = C::NKV, CH = D / 32 / NU;
-  constexpr int kIssuer = (NS + NU) * 4;        // the warp that issues the products
+  constexpr int NS = C::NS, NKV = C::NKV;
+  constexpr int kUnpack = C::SOFT * 4, kIssuer = kUnpack + 8;        // first unpacking warp, the one that issues
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t b_q, b_fin, b_s[2], b_p[2], b_o[NS], b_kf[NKV], b_ke[NKV], b_vf[NKV], b_ve[NKV], b_i[kInfo];
   __shared__ uint32_t s_tmem;
   __shared__ Info s_info[kInfo];
-  __shared__ uint32_t s_red[NU][2][4][2];
+  __shared__ uint2 s_red[2][8];
+  __shared__ float s_max[NS][2][2][M];           // a half row's largest score, tiles taking turns
+  __shared__ float2 s_sum[NS][2][M];
   uint8_t* smem = smem_raw + ((1024u - (sm100::smem_u32(smem_raw) & 1023u)) & 1023u);   // (kept a shared address)
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
@@ -515,16 +530,16 @@ k_prefill4(Pool c, RopeArgs r, TO* __restrict__ out, AttnArgs a, Shape sh, Plan 
     sm100::mbar_init(&b_fin, 1);
     for (int i = 0; i < 2; ++i) {
       sm100::mbar_init(&b_s[i], 1);
-      sm100::mbar_init(&b_p[i], kGroup);
+      sm100::mbar_init(&b_p[i], 2 * kGroup);
     }
     for (int i = 0; i < NS; ++i) sm100::mbar_init(&b_o[i], 1);
     for (int i = 0; i < NKV; ++i) {
-      sm100::mbar_init(&b_kf[i], NU * kGroup);
+      sm100::mbar_init(&b_kf[i], 2 * kGroup);
       sm100::mbar_init(&b_ke[i], 1);
-      sm100::mbar_init(&b_vf[i], NU * kGroup);
+      sm100::mbar_init(&b_vf[i], 2 * kGroup);
       sm100::mbar_init(&b_ve[i], 1);
     }
-    for (int i = 0; i < kInfo; ++i) sm100::mbar_init(&b_i[i], kGroup);
+    for (int i = 0; i < kInfo; ++i) sm100::mbar_init(&b_i[i], 2 * kGroup);
     sm100::fence_mbar_init();
   }
   sm100::tc_fence_before();
@@ -535,10 +550,10 @@ k_prefill4(Pool c, RopeArgs r, TO* __restrict__ out, AttnArgs a, Shape sh, Plan 
   const int kvh = u.hs / sh.nsub, h0 = kvh * a.group + (u.hs % sh.nsub) * sh.gt;
   const int nh = min(sh.gt, (kvh + 1) * a.group - h0);
 
-  if (warp < NS * 4) {
+  if (warp < kUnpack) {
     set_regs_up<C::R_SOFT>();
-    // ------------------------------------------------------------ queries, softmax, outputs
-    const int i = warp >> 2, wt = tid & 127;
+    // ------------------------------------------------------------ softmax and outputs: half a row a thread
+    const int i = warp >> 3, half = (warp >> 2) & 1, wt = tid & 127;
     if (i < ns) {
       const int ti = i * sh.tpm + wt / sh.gt, hh = wt % sh.gt;
       const bool is_row = wt < sh.tpm * sh.gt && ti < u.n && hh < nh;
@@ -553,26 +568,30 @@ k_prefill4(Pool c, RopeArgs r, TO* __restrict__ out, AttnArgs a, Shape sh, Plan 
       const int64_t tile = (int64_t)u.hs * plan.q_tiles + row_tile(u.tok - u.off, u.row, u.off, sh.tpm) + i;
       const float fq = is_row ? *(const float*)(plan.q + tile * C::QIMG + C::OP + 4 * wt) : 0.0f;
       const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-      const uint32_t t_o = tmem + lanes + 256 + i * D;
+      const uint32_t t_o = tmem + lanes + 256 + i * D + half * (D / 2);
       float mref = -INFINITY, vref = 0.0f;
       Sums sum{0ull, 0ull};
       bool dead = false;
-      for (int k = 0; k < nt && !dead; ++k) {
+      // A warp whose wait gave up keeps meeting the others at their barriers, and does no more.
+      for (int k = 0; k < nt; ++k) {
         const int sl = ns == 2 ? i : (k & 1);
-        const uint32_t t_s = tmem + lanes + 128 * sl;
+        const uint32_t t_s = tmem + lanes + 128 * sl + 64 * half;
         const int ring = k % kInfo;
-        dead = !sm100::mbar_wait(&b_i[ring], (k / kInfo) & 1, a.flags);
-        if (!dead) dead = !sm100::mbar_wait(&b_s[sl], ns == 2 ? (k & 1) : ((k >> 1) & 1), a.flags);
+        dead = dead || !sm100::mbar_wait(&b_i[ring], (k / kInfo) & 1, a.flags);
+        dead = dead || !sm100::mbar_wait(&b_s[sl], ns == 2 ? (k & 1) : ((k >> 1) & 1), a.flags);
         dead = __any_sync(0xffffffffu, dead);
-        if (dead) break;
         sm100::tc_fence_after();
         const Info& in = s_info[ring];
-        const int key0 = (u.t0 + k) * KT;
-        const bool edge = (in.ok[0] & in.ok[1] & in.ok[2] & in.ok[3]) != 0xffffffffu || key0 < w_lo || key0 + KT - 1 > w_hi;
-        const float fk = fq * in.kf;
-        const float* mean = (const float*)(smem + C::MEAN) + ring * KT;
-        const float top = fk * (edge ? row_max_edge(t_s, &in, key0, lo, hi) : row_max(t_s));
-        const float nv = in.vref;
+        const uint32_t ok[2] = {in.ok[2 * half], in.ok[2 * half + 1]};
+        const int key0 = (u.t0 + k) * KT + 64 * half;
+        const bool edge = (ok[0] & ok[1]) != 0xffffffffu || key0 < w_lo || key0 + 63 > w_hi;
+        const float fk = fq * in.kf, nv = in.vref;
+        const float* mean = (const float*)(smem + C::MEAN) + ring * KT + 64 * half;
+        const float mine = dead ? -INFINITY : edge ? row_max_edge(t_s, ok, key0, lo, hi) : row_max(t_s);
+        s_max[i][k & 1][half][wt] = mine;
+        sm100::named_bar(1 + i, 2 * kGroup);
+        const float top = fk * fmaxf(mine, s_max[i][k & 1][half ^ 1][wt]);
+        if (dead) continue;
         if (__any_sync(0xffffffffu, (is_row && top > mref + kSlack) || nv != vref)) {
           float f = 1.0f;
           if (is_row && top > mref) {
@@ -583,19 +602,15 @@ k_prefill4(Pool c, RopeArgs r, TO* __restrict__ out, AttnArgs a, Shape sh, Plan 
           sum.l = f2_fma(sum.l, ff, 0ull);
           sum.m = f2_fma(sum.m, ff, 0ull);
           if (k > 0) {
-            dead = !sm100::mbar_wait(&b_o[i], (k - 1) & 1, a.flags);
-            dead = __any_sync(0xffffffffu, dead);
-            if (dead) break;
+            dead = __any_sync(0xffffffffu, !sm100::mbar_wait(&b_o[i], (k - 1) & 1, a.flags));
+            if (dead) continue;
             sm100::tc_fence_after();
-            row_scale<D>(t_o, f * (vref / nv));
+            row_scale<D / 2>(t_o, f * (vref / nv));
           }
           vref = nv;
         }
         const float nb = kUp - (mref == -INFINITY ? 0.0f : mref);
-        if (edge)
-          sum = row_probs_edge(t_s, fk, nb, mean, sum, &in, key0, lo, hi);
-        else
-          row_probs(t_s, fk, nb, mean, &sum.l, &sum.m);
+        sum = edge ? row_probs_edge(t_s, fk, nb, mean, sum, ok, key0, lo, hi) : row_probs(t_s, fk, nb, mean, sum);
         sm100::tmem_wait_st();
         sm100::tc_fence_before();
         sm100::mbar_arrive(&b_p[sl]);
@@ -603,17 +618,22 @@ k_prefill4(Pool c, RopeArgs r, TO* __restrict__ out, AttnArgs a, Shape sh, Plan 
       // ---- outputs
       if (nt > 0 && !dead) dead = !sm100::mbar_wait(&b_fin, 0, a.flags);
       dead = __any_sync(0xffffffffu, dead);
+      sm100::tc_fence_after();
+      const float2 own = make_float2(f2_lo(sum.l) + f2_hi(sum.l), f2_lo(sum.m) + f2_hi(sum.m));
+      s_sum[i][half][wt] = own;
+      sm100::named_bar(1 + i, 2 * kGroup);
       if (!dead) {
-        sm100::tc_fence_after();
-        const float l = f2_lo(sum.l) + f2_hi(sum.l), mv = f2_lo(sum.m) + f2_hi(sum.m);
+        const float2 other = s_sum[i][half ^ 1][wt];
+        const float l = own.x + other.x, mv = own.y + other.y;
         const float vf = vref * 0x1p-12f;
         const bool whole = u.slot < 0;
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         const int64_t at = (int64_t)(u.tok + ti) * a.n_q + h0 + hh;
         const int64_t pr = whole ? 0 : (int64_t)u.slot * part_rows(NS) + i * M + wt;
-        float* po = plan.parts + pr * D;
+        float* po = plan.parts + pr * D + half * (D / 2);
+        TO* wo = out + at * D + half * (D / 2);
 #pragma unroll 1
-        for (int ch = 0; ch < D / 32; ++ch) {
+        for (int ch = 0; ch < D / 64; ++ch) {
           uint32_t x[32];
           if (nt > 0) {
             ld32(t_o + 32 * ch, x);
@@ -623,27 +643,27 @@ k_prefill4(Pool c, RopeArgs r, TO* __restrict__ out, AttnArgs a, Shape sh, Plan 
             for (int e = 0; e < 32; ++e) x[e] = 0u;
           }
           if (is_row) {
-          float o[32];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int to = (e & ~7) + ((e & 1) << 2) + ((e & 7) >> 1);   // the codes' order undone
-            o[to] = fmaf(__uint_as_float(x[e]), vf, mv);
-          }
-          if (whole) {
-            TO y[32];
+            for (int g = 0; g < 32; g += 8) {
+              float o[8];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) y[e] = from_f<TO>(l == 0.0f ? 0.0f : o[e] * inv);
+              for (int e = 0; e < 8; ++e)                                   // (the codes' order undone)
+                o[((e & 1) << 2) + (e >> 1)] = fmaf(__uint_as_float(x[g + e]), vf, mv);
+              if (whole) {
+                TO y[8];
 #pragma unroll
-            for (int e = 0; e < 2 * (int)sizeof(TO); ++e)
-              *(uint4*)((uint8_t*)(out + at * D + 32 * ch) + 16 * e) = *(const uint4*)((const uint8_t*)y + 16 * e);
-          } else {
+                for (int e = 0; e < 8; ++e) y[e] = from_f<TO>(l == 0.0f ? 0.0f : o[e] * inv);
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) *(float4*)(po + 32 * ch + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-          }
+                for (int e = 0; e < (int)sizeof(TO) / 2; ++e) ((uint4*)(wo + 32 * ch + g))[e] = ((const uint4*)y)[e];
+              } else {
+#pragma unroll
+                for (int e = 0; e < 8; e += 4) *(float4*)(po + 32 * ch + g + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+              }
+            }
           }
           __syncwarp();
         }
-        if (is_row) {
+        if (is_row && half == 0) {
           if (whole) {
             if (a.lse) a.lse[at] = l == 0.0f ? -INFINITY : (mref + (log2f(l) - kUp)) * 0.69314718055994531f;
           } else {
@@ -655,119 +675,129 @@ k_prefill4(Pool c, RopeArgs r, TO* __restrict__ out, AttnArgs a, Shape sh, Plan 
       }
     }
   } else if (warp < kIssuer) {
-    // ------------------------------------------------------------ unpacking: a thread a key, a group its share of the chunks
+    // ------------------------------------------------------------ unpacking: a warp a block of 16 keys
     if constexpr (NS == 1) set_regs_up<C::R_UNPACK>(); else set_regs_down<C::R_UNPACK>();
-    const int dt = tid & 127, uw = warp & 3, share = (warp >> 2) - NS, ch0 = share * CH;
+    constexpr int NC = D / 64;                       // 16-byte chunks of a block's codes a lane, a side
+    const int uw = warp - kUnpack;
     int64_t ulo, uhi;
     unit_keys(c, r, a, u.pos, u.n, &ulo, &uhi);
     const int64_t page_bytes = ((int64_t)c.n_kv << (c.page_shift - 4)) * blk_bytes(D);
-    const int64_t head_off = ((int64_t)kvh << (c.page_shift - 4)) * blk_bytes(D);
+    const uint8_t* head = c.pages + ((int64_t)kvh << (c.page_shift - 4)) * blk_bytes(D);
+    const int32_t* table = c.table + u.row * c.table_stride;
     const int in_page = (1 << c.page_shift) - 1;
-    const int t16 = dt & 15, sw = swz(t16, D);
     // page numbers two tiles ahead, codes one tile ahead
     auto page_of = [&](int k) {
-      const int64_t t = (int64_t)(u.t0 + k) * KT + dt;
-      if (k >= nt || t < ulo || t > uhi) return -2;
-      return max(-1, __ldg(c.table + u.row * c.table_stride + (t >> c.page_shift)));
+      const int64_t t = (int64_t)(u.t0 + k) * KT + 16 * uw;
+      if (k >= nt || t + 15 < ulo || t > uhi) return -2;
+      return max(-1, __ldg(table + (t >> c.page_shift)));
     };
     // (looked at when its codes are loaded, a tile after it was asked for)
     auto checked = [&](int page) {
       if (page == -1 || page >= c.n_pages) {
-        raise(a.flags, SQ_FLAG_PAGE);
+        if (lane == 0) raise(a.flags, SQ_FLAG_PAGE);
         return -2;
       }
       return page;
     };
     auto block_of = [&](int k, int pg) {
-      const int t = ((u.t0 + k) * KT + dt) & in_page;
-      return c.pages + pg * page_bytes + head_off + (int64_t)(t >> 4) * blk_bytes(D);
+      const int t = ((u.t0 + k) * KT + 16 * uw) & in_page;
+      return head + pg * page_bytes + (t >> 4) * blk_bytes(D);
     };
-    uint4 kc[CH], vc[CH];
-    uint32_t kw = 0, vw = 0;
-    int pg = checked(page_of(0)), pg_v = pg, pg_next;
+    // Lane l holds the pair of key l, or of value l - 16, and chunks l, l + 32, ... of the codes as they lie. Where
+    // they go: row t, coordinates 32 q .. 32 q + 31 as four chunks of a swizzled line. The lanes that write into
+    // slabs of 64 coordinates at once begin with different ones of the four, so that no two meet in a bank.
+    uint32_t to[NC];
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int x = 32 * i + lane, t = x / (D / 32), q = (x % (D / 32)) ^ swz(t, D), row = 16 * uw + t;
+      const int rot = D == 256 ? q >> 1 : D == 128 ? q & 2 : 0;
+      to[i] = (q >> 1) * 16384 + row * 128 + (((((q & 1) << 2) ^ rot ^ row) & 7) << 4);
+    }
+    auto unpack = [&](uint32_t dst, const uint4* codes, uint32_t scales, int from) {
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const uint32_t sc = __shfl_sync(0xffffffffu, scales, from + (32 * i + lane) / (D / 32));
+        const __half2 s2 = __half2half2(__ushort_as_half((unsigned short)sc)), s16 = __half2half2(__ushort_as_half((unsigned short)(sc >> 16)));
+        uint32_t w[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+        const int q = ((32 * i + lane) % (D / 32)) ^ swz((32 * i + lane) / (D / 32), D);
+        if (D >= 128) {                              // words in the order e ^ rot
+          const bool b1 = D == 128 ? (q & 2) != 0 : (q & 4) != 0, b0 = D == 256 && (q & 2) != 0;
+          const uint32_t y0 = b1 ? w[2] : w[0], y1 = b1 ? w[3] : w[1], y2 = b1 ? w[0] : w[2], y3 = b1 ? w[1] : w[3];
+          w[0] = b0 ? y1 : y0;
+          w[1] = b0 ? y0 : y1;
+          w[2] = b0 ? y3 : y2;
+          w[3] = b0 ? y2 : y3;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) *(uint4*)(smem + ((dst + to[i]) ^ (e << 4))) = unpack_codes(w[e], s2, s16);
+      }
+    };
+    uint4 kc[NC], vc[NC];
+#pragma unroll
+    for (int i = 0; i < NC; ++i) kc[i] = vc[i] = make_uint4(0, 0, 0, 0);
+    uint32_t pair = 0;
     auto load_k = [&](int k, int page) {
-      kw = vw = 0;
+      pair = 0;
       if (page >= 0) {
         const uint8_t* blk = block_of(k, page);
-        kw = __ldg((const uint32_t*)(blk + k_pairs(D) + 4 * t16));
-        vw = __ldg((const uint32_t*)(blk + v_pairs(D) + 4 * t16));
+        const int64_t t = (int64_t)(u.t0 + k) * KT + 16 * uw + (lane & 15);
+        if (t >= ulo && t <= uhi) pair = __ldg((const uint32_t*)(blk + k_pairs(D) + 4 * lane));
 #pragma unroll
-        for (int p = 0; p < CH; ++p) kc[p] = __ldg((const uint4*)(blk + t16 * (D / 2) + (((p + ch0) ^ sw) << 4)));
-      } else {
-#pragma unroll
-        for (int p = 0; p < CH; ++p) kc[p] = make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < NC; ++i) kc[i] = __ldg((const uint4*)blk + 32 * i + lane);
       }
     };
     auto load_v = [&](int k, int page) {
       if (page >= 0) {
-        const uint8_t* blk = block_of(k, page) + v_codes(D) + t16 * (D / 2);
+        const uint4* src = (const uint4*)(block_of(k, page) + v_codes(D));
 #pragma unroll
-        for (int p = 0; p < CH; ++p) vc[p] = __ldg((const uint4*)(blk + (((p + ch0) ^ sw) << 4)));
-      } else {
-#pragma unroll
-        for (int p = 0; p < CH; ++p) vc[p] = make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < NC; ++i) vc[i] = __ldg(src + 32 * i + lane);
       }
     };
+    int pg = checked(page_of(0)), pg_v = pg, pg_next;
     load_k(0, pg);
     load_v(0, pg);
     pg_next = page_of(1);
     float sref = 0.0f;
-    __half vs_cur = __float2half(0.0f);
+    uint32_t vs_cur = 0, vs_next = 0;
     bool dead = false;
     // keys of tile k, then values of tile k - 1: each is unpacked while the products of the other run
     for (int k = 0; k <= nt; ++k) {
-      __half vs_next = __float2half(0.0f);
       if (k < nt) {
         const int st = k % NKV;
-        const float ks = __uint_as_float(kw << 16), km = __uint_as_float(kw & 0xffff0000u);
-        const float vs = __uint_as_float(vw << 16), vm = __uint_as_float(vw & 0xffff0000u);
-        // largest offset or step (what is NaN is not greater), as unsigned words
-        const uint32_t km_top = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fabsf(km), fmaxf(8.0f * ks, 0.0f))));
-        const uint32_t vs_top = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(vs, 0.0f)));
-        const uint32_t ok = __ballot_sync(0xffffffffu, pg >= 0);
-        if (lane == 0) {
-          s_red[share][k & 1][uw][0] = km_top;
-          s_red[share][k & 1][uw][1] = vs_top;
-        }
-        sm100::named_bar(3 + share, kGroup);
-        uint32_t kt = 0, vt = 0;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          kt = max(kt, s_red[share][k & 1][w][0]);
-          vt = max(vt, s_red[share][k & 1][w][1]);
-        }
-        const float kref = pow2_up(__uint_as_float(kt));
-        sref = fmaxf(sref, pow2_up(__uint_as_float(vt)));
+        const float s = __uint_as_float(pair << 16), m = __uint_as_float(pair & 0xffff0000u);
+        const int64_t t = (int64_t)(u.t0 + k) * KT + 16 * uw + (lane & 15);
+        const uint32_t ok = __ballot_sync(0xffffffffu, pg >= 0 && t >= ulo && t <= uhi) & 0xffffu;
+        // largest offset and step of the keys, largest step of the values (what is NaN is not greater), as words
+        const uint32_t kv = __float_as_uint(fmaxf(fabsf(m), fmaxf(8.0f * s, 0.0f))), vv = __float_as_uint(fmaxf(s, 0.0f));
+        const uint32_t kt_w = __reduce_max_sync(0xffffffffu, lane < 16 ? kv : 0u);
+        const uint32_t vt_w = __reduce_max_sync(0xffffffffu, lane < 16 ? 0u : vv);
+        if (lane == 0) s_red[k & 1][uw] = make_uint2(kt_w, vt_w);
+        sm100::named_bar(3, 2 * kGroup);
+        const uint2 red = s_red[k & 1][lane & 7];
+        const float kref = pow2_up(__uint_as_float(__reduce_max_sync(0xffffffffu, red.x)));
+        sref = fmaxf(sref, pow2_up(__uint_as_float(__reduce_max_sync(0xffffffffu, red.y))));
         const float kmul = 0x1p13f / kref, vmul = 0x1p12f / sref;
         dead = dead || !sm100::mbar_wait(&b_ke[st], ((k / NKV) & 1) ^ 1, a.flags);
         const int ring = k % kInfo;
-        if (share == 0) {
-          if (dt == 0) {
+        if (lane == 0) {
+          if (uw == 0) {
             s_info[ring].kf = kref * 0x1p-13f;
             s_info[ring].vref = sref;
           }
-          if (lane == 0) s_info[ring].ok[uw] = ok;
-          ((float*)(smem + C::MEAN))[ring * KT + dt] = fmaf(8.0f, vs, vm);
-          sm100::mbar_arrive(&b_i[ring]);
+          ((unsigned short*)s_info[ring].ok)[uw] = (unsigned short)ok;
         }
-        vs_next = __float2half_rn(vs * vmul);
-        const __half ksh = __float2half_rn(ks * kmul), kmh = __float2half_rn(km * kmul), ks8 = __float2half_rn(8.0f * ks * kmul);
-        const __half2 s2 = __half2half2(ksh), s16 = __half2half2(__float2half_rn(ks * kmul * 0.0625f));
-        uint8_t* kop = smem + C::K + st * C::OP;
-#pragma unroll
-        for (int p = 0; p < CH; ++p) {
-          const uint32_t w[4] = {kc[p].x, kc[p].y, kc[p].z, kc[p].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int chunk = 4 * (p + ch0) + e;
-            *(uint4*)(kop + (chunk >> 3) * 16384 + dt * 128 + (((chunk & 7) ^ (dt & 7)) << 4)) = unpack_codes(w[e], s2, s16);
-          }
-        }
-        if (share == NU - 1) {
-        const __half2 e0 = __half2half2(kmh), e1 = __halves2half2(kmh, ks8), e2 = __half2half2(ks8);
-        uint8_t* ext = kop + C::MAIN + (dt >> 3) * 256 + (dt & 7) * 16;
-        *(uint4*)ext = make_uint4(*(const uint32_t*)&e0, *(const uint32_t*)&e1, *(const uint32_t*)&e2, 0u);
-        *(uint4*)(ext + 128) = make_uint4(0u, 0u, 0u, 0u);
+        if (lane >= 16) ((float*)(smem + C::MEAN))[ring * KT + 16 * uw + lane - 16] = fmaf(8.0f, s, m);
+        sm100::mbar_arrive(&b_i[ring]);
+        const float sm = s * (lane < 16 ? kmul : vmul);
+        vs_next = dec::pack_h2(sm, sm * 0.0625f);
+        const uint32_t kop = C::K + st * C::OP;
+        unpack(kop, kc, vs_next, 0);
+        if (lane < 16) {
+          const __half kmh = __float2half_rn(m * kmul), ks8 = __float2half_rn(8.0f * sm);
+          const __half2 e0 = __half2half2(kmh), e1 = __halves2half2(kmh, ks8), e2 = __half2half2(ks8);
+          uint8_t* ext = smem + kop + C::MAIN + (2 * uw + (lane >> 3)) * 256 + (lane & 7) * 16;
+          *(uint4*)ext = make_uint4(*(const uint32_t*)&e0, *(const uint32_t*)&e1, *(const uint32_t*)&e2, 0u);
+          *(uint4*)(ext + 128) = make_uint4(0u, 0u, 0u, 0u);
         }
         sm100::fence_async_smem();
         sm100::mbar_arrive(&b_kf[st]);
@@ -781,17 +811,8 @@ k_prefill4(Pool c, RopeArgs r, TO* __restrict__ out, AttnArgs a, Shape sh, Plan 
       if (k > 0) {
         const int v = k - 1, st = v % NKV;
         dead = dead || !sm100::mbar_wait(&b_ve[st], ((v / NKV) & 1) ^ 1, a.flags);
-        const __half2 s2 = __half2half2(vs_cur), s16 = __half2half2(__float2half_rn(__half2float(vs_cur) * 0.0625f));
-        uint8_t* vop = smem + C::V + st * C::MAIN;
-#pragma unroll
-        for (int p = 0; p < CH; ++p) {
-          const uint32_t w[4] = {vc[p].x, vc[p].y, vc[p].z, vc[p].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int chunk = 4 * (p + ch0) + e;
-            *(uint4*)(vop + (chunk >> 3) * 16384 + dt * 128 + (((chunk & 7) ^ (dt & 7)) << 4)) = unpack_codes(w[e], s2, s16);
-          }
-        }
+        __syncwarp();
+        unpack(C::V + st * C::MAIN, vc, vs_cur, 16);
         sm100::fence_async_smem();
         sm100::mbar_arrive(&b_vf[st]);
         if (k < nt) load_v(k, pg_v);
@@ -837,7 +858,7 @@ k_prefill4(Pool c, RopeArgs r, TO* __restrict__ out, AttnArgs a, Shape sh, Plan 
         const uint64_t vd = desc_of(va, 16384, 1024, 2);
         if (sm100::elect_one()) {
 #pragma unroll
-          for (int s = 0; s < KT / 16; ++s) sm100::mma_f16_ts(d, p + 8 * s, vd + 128 * s, id_o, (s > 0 || k > 0) ? 1u : 0u);
+          for (int s = 0; s < KT / 16; ++s) sm100::mma_f16_ts(d, p + 64 * (s >> 2) + 8 * (s & 3), vd + 128 * s, id_o, (s > 0 || k > 0) ? 1u : 0u);
           sm100::mma_commit(&b_o[i]);
           if (last) sm100::mma_commit(&b_ve[k % NKV]);
         }
