@@ -249,13 +249,14 @@ template <typename T, typename TO, int D>
 cudaError_t launch_prefill(const Pool& c, const RopeArgs& r, const void* q, void* out, const AttnArgs& a, const pre::Shape& s,
                            const pre::Plan& p, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
+  static_assert(sizeof(pre::PlanSmem) <= 48 * 1024, "within what needs no asking for");
   auto kernel = pre::k_prefill4<TO, D>;
   constexpr int smem = pre::Cfg<D>::TOTAL;
   cudaError_t e = allow_smem(kernel, smem, &done);
   if (e != cudaSuccess) return e;
   const int64_t rows = a.n_tok * a.n_q, per = pre::kPlanThreads / (D / 8);
   const unsigned blocks = (unsigned)std::min<int64_t>((rows + per - 1) / per, 4 * s.sms);
-  pre::k_prepare4<T, D><<<1 + blocks, pre::kPlanThreads, 0, st>>>(c, r, (const T*)q, a, s, p);
+  pre::k_prepare4<T, D><<<1 + blocks, pre::kPlanThreads, sizeof(pre::PlanSmem), st>>>(c, r, (const T*)q, a, s, p);
   e = cudaGetLastError();
   if (e == cudaSuccess)
     e = launch_overlapped(kernel, s.cap_units, pre::Cfg<D>::THREADS, smem, st, c, r, (TO*)out, a, s, p);

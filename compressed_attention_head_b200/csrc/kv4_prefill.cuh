@@ -101,108 +101,209 @@ __device__ __forceinline__ void unit_keys(const Pool& c, const RopeArgs& r, cons
 }
 
 constexpr int kPlanThreads = 512;
+constexpr int kListed = 2048;                 // units a head up to which they are sorted and may be cut
 
-__device__ __forceinline__ void make_units(const Pool& c, const RopeArgs& r, const AttnArgs& a, const Shape& s, const Plan& p) {
-  __shared__ unsigned long long s_tiles;
-  __shared__ int s_longest, s_hist[64], s_at[64], s_slots, s_joins;
+// One unit a head: its sequence, its place in it, its tiles.
+struct Listed { int row, j, len; };
+
+struct PlanSmem {
+  int off[kPlanThreads + 1];                  // units before a sequence, of the sequences at hand
+  Listed unit[kListed];
+  int warp[kPlanThreads / 32];
+  int hist[64], parts[33], least[33];
+  unsigned long long tiles;
+  int longest, cut, slots, joins;
+};
+
+// Unit j of sequence row.
+__device__ __forceinline__ Unit unit_of(const Pool& c, const AttnArgs& a, const Shape& s, int row, int j) {
+  const int32_t first = __ldg(a.cu + row);
+  const int64_t t_lo = max(0, first), t_hi = min((int64_t)__ldg(a.cu + row + 1), a.n_tok);
+  Unit w;
+  w.tok = (int)(t_lo + (int64_t)j * s.tpu);
+  w.n = (int)min((int64_t)s.tpu, t_hi - w.tok);
+  w.off = w.tok - first;
+  w.pos = (int64_t)__ldg(a.start + row) + w.off;
+  w.row = row;
+  return w;
+}
+
+// All units of all heads, longest first, cut where that makes the whole end sooner.
+__device__ __forceinline__ void make_units(const Pool& c, const RopeArgs& r, const AttnArgs& a, const Shape& s, const Plan& p,
+                                           PlanSmem& m) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int heads = c.n_kv * s.nsub;
-  if (tid < 64) s_hist[tid] = 0;
-  if (tid == 0) {
-    s_tiles = 0;
-    s_longest = s_slots = s_joins = 0;
+  if (tid < 64) m.hist[tid] = 0;
+  if (tid < 33) {
+    m.parts[tid] = 0;
+    m.least[tid] = 0x7fffffff;
   }
-  __syncthreads();
-  int pass_cut = 0x7fffffff, longest = 1;
-  // three passes over the units: their lengths, the lengths' classes, the list
-  for (int pass = 0; pass < 3; ++pass) {
-    unsigned long long tiles = 0;
-    int most = 0;
-    for (int b = warp; b < c.batch; b += kPlanThreads / 32) {
-      const int64_t t_lo = max(0, __ldg(a.cu + b)), t_hi = min((int64_t)__ldg(a.cu + b + 1), a.n_tok);
-      if (t_hi <= t_lo) continue;
-      const int64_t start = (int64_t)__ldg(a.start + b) + (t_lo - __ldg(a.cu + b));
-      const int64_t n_units = (t_hi - t_lo + s.tpu - 1) / s.tpu;
-      if (pass == 0 && lane == 0 && a.flags) {
-        const int64_t last = start + (t_hi - t_lo) - 1;
+  if (tid == 0) {
+    m.tiles = 0;
+    m.longest = m.slots = m.joins = 0;
+  }
+  int64_t count = 0;                          // units a head
+  unsigned long long tiles = 0;
+  int longest = 0;
+  for (int b0 = 0; b0 < c.batch; b0 += kPlanThreads) {
+    const int b = b0 + tid;
+    int n = 0;
+    if (b < c.batch) {
+      const int32_t first = __ldg(a.cu + b);
+      const int64_t t_lo = max(0, first), t_hi = min((int64_t)__ldg(a.cu + b + 1), a.n_tok);
+      if (t_hi > t_lo) {
+        n = (int)((uint32_t)(t_hi - t_lo + s.tpu - 1) / (uint32_t)s.tpu);
+        const int64_t start = (int64_t)__ldg(a.start + b) + (t_lo - first), last = start + (t_hi - t_lo) - 1;
         uint32_t bits = 0;
         if (last >= c.cap() || start < -1) bits |= SQ_FLAG_SEQLEN;
         if (r.table && min(last, c.cap() - 1) >= r.n_pos) bits |= SQ_FLAG_ROPE;
-        if (bits) atomicOr(a.flags, bits);
+        if (bits && a.flags) atomicOr(a.flags, bits);
       }
-      for (int64_t u = lane; u < n_units; u += 32) {
-        Unit w;
-        w.pos = start + u * s.tpu;
-        w.row = b;
-        w.tok = (int)(t_lo + u * s.tpu);
-        w.off = w.tok - __ldg(a.cu + b);
-        w.n = (int)min((int64_t)s.tpu, t_hi - w.tok);
-        int64_t lo, hi;
-        unit_keys(c, r, a, w.pos, w.n, &lo, &hi);
-        const int len = hi < lo ? 0 : (int)(hi / KT - lo / KT) + 1;
-        if (pass == 0) {
-          tiles += (unsigned long long)len * heads;
-          most = max(most, len);
-          continue;
-        }
-        const int parts = len > pass_cut ? (len + pass_cut - 1) / pass_cut : 1;
-        const int piece = (len + parts - 1) / parts;
-        const int cls = 63 - (int)((int64_t)piece * 63 / longest);
-        if (pass == 1) {
-          atomicAdd(&s_hist[cls], parts * heads);
-          continue;
-        }
-        int at = atomicAdd(&s_at[cls], parts * heads);
+    }
+    // units before each of these sequences
+    int inc = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    __syncthreads();
+    if (lane == 31) m.warp[warp] = inc;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) inc += m.warp[w];
+    m.off[tid + 1] = inc;
+    if (tid == 0) m.off[0] = 0;
+    __syncthreads();
+    const int here = m.off[kPlanThreads];
+    for (int e = tid; e < here; e += kPlanThreads) {
+      int lo_b = 0, hi_b = kPlanThreads;      // the sequence of unit e
+      while (hi_b - lo_b > 1) {
+        const int mid = (lo_b + hi_b) >> 1;
+        if (m.off[mid] <= e) lo_b = mid; else hi_b = mid;
+      }
+      const int j = m.off[lo_b + 1] - 1 - e;  // the last tokens, which attend most, first
+      Unit w = unit_of(c, a, s, b0 + lo_b, j);
+      int64_t lo, hi;
+      unit_keys(c, r, a, w.pos, w.n, &lo, &hi);
+      const int len = hi < lo ? 0 : (int)(hi / KT - lo / KT) + 1;
+      tiles += len;
+      longest = max(longest, len);
+      if (count + e < kListed) {
+        m.unit[count + e] = Listed{b0 + lo_b, j, len};
+      }
+      if (count + here > kListed) {
+        // Too many to sort; so many share the work well enough as they come. (Those listed before are written below.)
+        w.t0 = (int)(lo / KT);
+        w.nt = len;
+        w.slot = -1;
         for (int h = 0; h < heads; ++h) {
-          int slot = -1, join = 0;
-          if (parts > 1) {
-            slot = atomicAdd(&s_slots, parts);
-            if (slot + parts <= s.cap_slots) {
-              join = atomicAdd(&s_joins, 1);
-              p.joins[join] = Join{at, slot, parts, 0};
-            } else {
-              slot = -2;
-            }
-          }
           w.hs = h;
-          int t = (int)(lo / KT);
-          for (int i = 0; i < parts; ++i, ++at) {
-            w.t0 = t;
-            w.nt = len / parts + (i < len % parts ? 1 : 0);
-            w.slot = slot < 0 ? slot : slot + i;
-            t += w.nt;
-            if (at < s.cap_units) p.units[at] = w;
-          }
+          const int64_t at = (count + e) * heads + h;
+          if (at < s.cap_units) p.units[at] = w;
         }
       }
     }
-    if (pass == 0) {
-      atomicAdd(&s_tiles, tiles);
-      atomicMax(&s_longest, most);
-      __syncthreads();
-      // An even share of the work; a unit is cut when it is longer than that by more than a quarter
-      // (below that the cut's own cost, a prologue and partial sums of every row, is more).
-      const int share = max(4, (int)((s_tiles + s.sms - 1) / s.sms));
-      longest = max(1, s_longest);
-      if (longest > share + share / 4) {
-        pass_cut = share;
-        longest = share;
+    count += here;
+  }
+  atomicAdd(&m.tiles, tiles);
+  atomicMax(&m.longest, longest);
+  __syncthreads();
+  const bool sorted = count <= kListed;
+  if (!sorted) {
+    // the listed ones that came with earlier sequences
+    for (int e = tid; e < kListed; e += kPlanThreads) {
+      const Listed l = m.unit[e];
+      Unit w = unit_of(c, a, s, l.row, l.j);
+      int64_t lo, hi;
+      unit_keys(c, r, a, w.pos, w.n, &lo, &hi);
+      w.t0 = (int)(lo / KT);
+      w.nt = l.len;
+      w.slot = -1;
+      for (int h = 0; h < heads; ++h) {
+        w.hs = h;
+        const int64_t at = (int64_t)e * heads + h;
+        if (at < s.cap_units) p.units[at] = w;
       }
-    } else if (pass == 1) {
-      __syncthreads();
-      if (tid == 0) {
-        int at = 0;
-        for (int i = 0; i < 64; ++i) {
-          s_at[i] = at;
-          at += s_hist[i];
-        }
-        p.head->units = min(at, s.cap_units);
-      }
-      __syncthreads();
+    }
+    if (tid == 0) {
+      p.head->units = (int)min(count * heads, (int64_t)s.cap_units);
+      p.head->joins = 0;
+    }
+    return;
+  }
+  // ---- where to cut: an even share of the tiles, or more by up to twice, or nowhere (candidate 32)
+  const int n_units = (int)count;
+  const int share = max(4, (int)((m.tiles * heads + s.sms - 1) / s.sms));
+  longest = max(1, m.longest);
+  auto candidate = [&](int i) { return i == 32 ? longest : min(longest, share + (share * i + 15) / 16); };
+  for (int i = lane; i < 33; i += 32) {
+    const int cut = candidate(i);
+    int parts = 0, least = 0x7fffffff;
+    for (int e = warp; e < n_units; e += kPlanThreads / 32) {
+      const int len = m.unit[e].len, n = len > cut ? (len + cut - 1) / cut : 1;
+      parts += n;
+      least = min(least, len / n);
+    }
+    atomicAdd(&m.parts[i], parts);
+    atomicMin(&m.least[i], least);
+  }
+  __syncthreads();
+  if (warp == 0) {
+    // Pieces run longest first on `sms` places: up to that many, the longest ends last; beyond, the last to begin
+    // ends within its own length of the even share. A piece costs about two tiles besides.
+    auto ends = [&](int i) {
+      const int cut = candidate(i), n = m.parts[i] * heads, waves = (n + s.sms - 1) / s.sms;
+      return (n <= s.sms ? cut : max(cut, share + m.least[i])) + 2 * waves;
+    };
+    const uint32_t best = __reduce_min_sync(0xffffffffu, (uint32_t)ends(lane) << 6 | (uint32_t)lane);
+    const uint32_t uncut = (uint32_t)ends(32) << 6;            // a tie goes to no cut
+    if (lane == 0) m.cut = uncut <= best ? longest : candidate(best & 63u);
+  }
+  __syncthreads();
+  // ---- the list by classes of length
+  const int cut = m.cut;
+  auto cls = [&](int len, int parts) { return 63 - (int)(((len + parts - 1) / parts) * 63.0f / cut); };
+  for (int e = tid; e < n_units; e += kPlanThreads) {
+    const int len = m.unit[e].len, parts = len > cut ? (len + cut - 1) / cut : 1;
+    atomicAdd(&m.hist[cls(len, parts)], parts * heads);
+  }
+  __syncthreads();
+  if (tid == 0) {
+    int at = 0;
+    for (int i = 0; i < 64; ++i) {
+      const int n = m.hist[i];
+      m.hist[i] = at;
+      at += n;
+    }
+    p.head->units = min(at, s.cap_units);
+  }
+  __syncthreads();
+  for (int x = tid; x < n_units * heads; x += kPlanThreads) {
+    const int e = x / heads;
+    const Listed l = m.unit[e];
+    const int parts = l.len > cut ? (l.len + cut - 1) / cut : 1;
+    int at = atomicAdd(&m.hist[cls(l.len, parts)], parts), slot = -1;
+    if (parts > 1) {
+      slot = atomicAdd(&m.slots, parts);
+      // (more than there are places for only when the offsets overlap, which is not allowed)
+      if (slot + parts <= s.cap_slots) p.joins[atomicAdd(&m.joins, 1)] = Join{at, slot, parts, 0};
+      else slot = -2;
+    }
+    Unit w = unit_of(c, a, s, l.row, l.j);
+    int64_t lo, hi;
+    unit_keys(c, r, a, w.pos, w.n, &lo, &hi);
+    w.hs = x - e * heads;
+    int t = (int)(lo / KT);
+    for (int i = 0; i < parts; ++i, ++at) {
+      w.t0 = t;
+      w.nt = l.len / parts + (i < l.len % parts ? 1 : 0);
+      w.slot = slot < 0 ? slot : slot + i;
+      t += w.nt;
+      if (at < s.cap_units) p.units[at] = w;
     }
   }
   __syncthreads();
-  if (tid == 0) p.head->joins = s_joins;
+  if (tid == 0) p.head->joins = m.joins;
 }
 
 // Block 0 lists the units; the others turn, scale and lay out the queries, D / 8
@@ -211,12 +312,13 @@ __device__ __forceinline__ void make_units(const Pool& c, const RopeArgs& r, con
 // Once a call, so that the pieces of a cut unit do not repeat it and a block's
 // prologue is one bulk copy a row tile.
 template <typename T, int D>
-__global__ void __launch_bounds__(kPlanThreads)
+__global__ void __launch_bounds__(kPlanThreads, 3)
 k_prepare4(Pool c, RopeArgs r, const T* __restrict__ q, AttnArgs a, Shape s, Plan p) {
   using C = Cfg<D>;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (blockIdx.x == 0) {
-    make_units(c, r, a, s, p);
+    extern __shared__ __align__(16) uint8_t plan_smem[];
+    make_units(c, r, a, s, p, *(PlanSmem*)plan_smem);
     return;
   }
   constexpr int TPR = D / 8;
