@@ -59,27 +59,32 @@ sq_status stream_args_ok(const sq_kv4_cache* c, const void* k, const void* v, sq
       !aligned(a.flags, 4) || !strides_ok(a.ks_tok, a.ks_head) || !strides_ok(a.vs_tok, a.vs_head))
     return SQ_ERR_ARG;
   if (a.n_tok > 0 && (!k || !v || !aligned(k, 16) || !aligned(v, 16))) return SQ_ERR_ARG;
-  const int64_t vecs = a.n_tok * 2 * c->n_kv_heads;
-  if (vecs / (kStreamThreads / (c->d / 8)) >= 0x7fffffff) return SQ_ERR_ARG;
   return SQ_OK;
+}
+
+// Blocks of a stream: tokens, parts of a token.
+template <int D> dim3 stream_grid(const Pool& c, int64_t n_tok, Share* sh) {
+  *sh = Share::of(2 * c.n_kv, vecs_of_block<D>());
+  return dim3((unsigned)((n_tok + sh->toks - 1) / sh->toks), sh->parts);
 }
 
 template <typename T, int D>
 void launch_append(const Pool& c, const RopeArgs& r, const void* k, const void* v, const StreamArgs& a, cudaStream_t st) {
-  constexpr int VPB = kStreamThreads / (D / 8);
-  const int64_t vecs = a.n_tok * 2 * c.n_kv;
-  const int64_t blocks = (vecs + VPB - 1) / VPB;
-  if (blocks > 4 * 148 * 8)
-    k_append4<T, D, 2><<<(unsigned)((vecs + 2 * VPB - 1) / (2 * VPB)), kStreamThreads, 0, st>>>(c, r, (const T*)k, (const T*)v, a);
+  Share sh;
+  const dim3 grid = stream_grid<D>(c, a.n_tok, &sh);
+  if (!r.table)
+    k_append4<T, D, 0><<<grid, kStreamThreads, 0, st>>>(c, r, (const T*)k, (const T*)v, a, sh);
+  else if (!r.inter && r.rot == D)
+    k_append4<T, D, 1><<<grid, kStreamThreads, 0, st>>>(c, r, (const T*)k, (const T*)v, a, sh);
   else
-    k_append4<T, D, 1><<<(unsigned)blocks, kStreamThreads, 0, st>>>(c, r, (const T*)k, (const T*)v, a);
+    k_append4<T, D, 2><<<grid, kStreamThreads, 0, st>>>(c, r, (const T*)k, (const T*)v, a, sh);
 }
 
 template <typename T, int D>
 void launch_read(const Pool& c, void* k, void* v, const StreamArgs& a, cudaStream_t st) {
-  constexpr int VPB = kStreamThreads / (D / 8);
-  const int64_t vecs = a.n_tok * 2 * c.n_kv;
-  k_read4<T, D><<<(unsigned)((vecs + VPB - 1) / VPB), kStreamThreads, 0, st>>>(c, (T*)k, (T*)v, a);
+  Share sh;
+  const dim3 grid = stream_grid<D>(c, a.n_tok, &sh);
+  k_read4<T, D><<<grid, kStreamThreads, 0, st>>>(c, (T*)k, (T*)v, a, sh);
 }
 
 #define SQ_KV4_D(T, CALL)                \

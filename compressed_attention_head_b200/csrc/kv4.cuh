@@ -82,6 +82,19 @@ template <typename T> __device__ __forceinline__ void unpack8(const Vec8<T>& r, 
   for (int i = 0; i < 8; ++i) x[i] = to_f<T>(e[i]);
 }
 
+// Two values rounded to T.
+template <typename T> __device__ __forceinline__ void round2(float* a, float* b) {}
+template <> __device__ __forceinline__ void round2<__half>(float* a, float* b) {
+  const float2 f = __half22float2(__floats2half2_rn(*a, *b));
+  *a = f.x;
+  *b = f.y;
+}
+template <> __device__ __forceinline__ void round2<__nv_bfloat16>(float* a, float* b) {
+  const float2 f = __bfloat1622float2(__floats2bfloat162_rn(*a, *b));
+  *a = f.x;
+  *b = f.y;
+}
+
 // Coordinates i0 .. i0+7 (x) of a head rotated by its position: y = a cos - b sin
 // of a pair's first element, b cos + a sin of its second, each operation rounded
 // to float once (no contraction: what a row of the cache holds must not depend on
@@ -134,13 +147,41 @@ __device__ __forceinline__ uint32_t bf16_down(float x) {
 }
 __device__ __forceinline__ uint32_t bf16_up(float x) { return (__float_as_uint(x) + 0xffffu) >> 16; }
 
-// The pair of a vector from its smallest and largest coordinate; NaN for a
-// vector that holds a value that is not finite (or whose range is not): the
-// codes are then 0 and every coordinate reads as NaN.
-__device__ __forceinline__ void make_pair(float mn, float mx, bool finite, float* s, float* m, uint32_t* word) {
+// Two floats a register pair: one instruction does an operation on both.
+typedef unsigned long long f2;                 // two floats
+__device__ __forceinline__ f2 f2_of(uint32_t lo, uint32_t hi) { return (f2)lo | ((f2)hi << 32); }
+__device__ __forceinline__ f2 f2_of(float lo, float hi) { return f2_of(__float_as_uint(lo), __float_as_uint(hi)); }
+__device__ __forceinline__ float f2_lo(f2 x) { return __uint_as_float((uint32_t)x); }
+__device__ __forceinline__ float f2_hi(f2 x) { return __uint_as_float((uint32_t)(x >> 32)); }
+__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c) {
+  f2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ f2 f2_add(f2 a, f2 b) {
+  f2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// The pair of a vector from its smallest and largest coordinate (NaN where one of
+// them is); NaN for a vector that holds a value that is not finite (or whose range
+// is not): the codes are then 0 and every coordinate reads as NaN.
+__device__ __forceinline__ void make_pair(float mn, float mx, float* s, float* m, uint32_t* word) {
+  const bool finite = fabsf(mn) < INFINITY && fabsf(mx) < INFINITY;
   uint32_t mb = bf16_down(mn);
-  float mf = __uint_as_float(mb << 16);
-  const float r = __fsub_rn(mx, mf);
+  const float r = __fsub_rn(mx, __uint_as_float(mb << 16));
   uint32_t sb = 0;
   if (r > 0.0f) sb = bf16_up(fmaxf(__fdiv_rn(r, 15.0f), FLT_MIN));
   if (!finite || !(r < INFINITY)) {
@@ -152,19 +193,37 @@ __device__ __forceinline__ void make_pair(float mn, float mx, bool finite, float
   *word = sb | (mb << 16);
 }
 
-// Code of x: (x - m) / s rounded to nearest, ties to even, exactly. The product
-// with inv = 1 / s is within a few rounding errors of the quotient, so its nearest
-// integer is the quotient's or, beside a tie, the next; the sign of the remainder
-// against s / 2, which one fused multiply-add gives, decides.
-__device__ __forceinline__ uint32_t code4(float x, float m, float s, float inv) {
-  const float e = __fsub_rn(x, m);
-  float c = rintf(__fmul_rn(e, inv));
-  const float rest = __fmaf_rn(-c, s, e), half = 0.5f * s;
-  if (fabsf(rest) >= half && s > 0.0f) {
-    const bool odd = ((int)c & 1) != 0;
-    if (fabsf(rest) > half || odd) c += rest > 0.0f ? 1.0f : -1.0f;
+// Eight codes: (x - m) / s rounded to nearest, ties to even, exactly. The product
+// with inv = 1 / s, rounded to an integer by an addition to 1.5 2^23, is within 2^-19
+// of the quotient: its nearest integer is the quotient's or, beside a tie, the next.
+// The remainder against s / 2, which one fused multiply-add gives, tells the two
+// apart; few vectors have such a coordinate. s > 0.
+constexpr float kRound = 12582912.0f;
+__device__ __forceinline__ uint32_t codes8(const float* x, float m, float s, float inv) {
+  const f2 m2 = f2_of(-m, -m), i2 = f2_of(inv, inv), r2 = f2_of(kRound, kRound), n2 = f2_of(-kRound, -kRound), s2 = f2_of(-s, -s);
+  const float half = 0.5f * s;
+  float c[8], rest[8];
+  bool near = false;
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    const f2 e = f2_add(f2_of(x[i], x[i + 1]), m2);
+    const f2 q = f2_add(f2_fma(e, i2, r2), n2);
+    const f2 t = f2_fma(q, s2, e);
+    c[i] = f2_lo(q);
+    c[i + 1] = f2_hi(q);
+    rest[i] = f2_lo(t);
+    rest[i + 1] = f2_hi(t);
+    near |= fabsf(rest[i]) >= half || fabsf(rest[i + 1]) >= half;
   }
-  return (uint32_t)fminf(fmaxf(c, 0.0f), 15.0f);
+  if (near) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (fabsf(rest[i]) > half || (fabsf(rest[i]) == half && ((int)c[i] & 1))) c[i] += rest[i] > 0.0f ? 1.0f : -1.0f;
+  }
+  // four codes are one number of 16 bits, exact in float
+  const float lo = fmaf(fmaf(fmaf(c[3], 16.0f, c[2]), 16.0f, c[1]), 16.0f, c[0]) + kRound;
+  const float hi = fmaf(fmaf(fmaf(c[7], 16.0f, c[6]), 16.0f, c[5]), 16.0f, c[4]) + kRound;
+  return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x5410);
 }
 
 // Sequence of token i among cu[0 .. batch] (cu NULL: one token a sequence), or -1.

@@ -1,11 +1,13 @@
 // Append to, and read back from, the paged 4-bit cache.
 //
-// Both are streams: d / 8 threads hold one vector, eight coordinates each, which
-// is one 16-byte load of a 16-bit input and one 32-bit word of codes; the minimum
-// and maximum go through d / 8 lanes. A key that is rotated by halves is read
-// twice by its warp (its own eight coordinates and the partners'; the second read
-// hits L1). No vector shares a byte with another, so nothing is read to be
-// written back and tokens may come in any order.
+// Both are streams, bound by memory only when their instructions are few: a thread
+// holds sixteen coordinates of a vector, eight of each half of the head (16-byte
+// loads of a 16-bit input, one word of codes each). Rotated by halves over the whole
+// head, the two are each other's partners under the same angles; any other rotation
+// reads its partners from memory again. Minimum and maximum go through d / 16 lanes.
+// The vectors of a block belong to whole tokens, whose places are looked up once,
+// while the loads are on their way. No vector shares a byte with another, so nothing
+// is read to be written back and tokens may come in any order.
 #pragma once
 
 #include "kv4.cuh"
@@ -55,115 +57,175 @@ __device__ __forceinline__ Place place_of(const Pool& c, const StreamArgs& a, in
   return p;
 }
 
-// kVecs vectors a thread group; the block's vectors are consecutive in
-// (token, side, head) order, so a warp reads whole rows of the caller's tensors.
-template <typename T, int D, int kVecs>
-__global__ void __launch_bounds__(kStreamThreads)
-k_append4(Pool c, RopeArgs r, const T* __restrict__ k, const T* __restrict__ v, StreamArgs a) {
-  constexpr int TPV = D / 8, VPB = kStreamThreads / TPV, NV = VPB * kVecs;
-  __shared__ Place places[NV + 1];
-  const int per_tok = 2 * c.n_kv;
-  const int64_t v0 = (int64_t)blockIdx.x * NV;
-  const int64_t t0 = v0 / per_tok;
-  const int n_here = (int)((v0 + NV - 1) / per_tok - t0) + 1;
-  for (int i = threadIdx.x; i < n_here; i += kStreamThreads) places[i] = place_of(c, a, r.table ? r.n_pos : -1, t0 + i);
-  __syncthreads();
-  const int j = threadIdx.x % TPV, i0 = 8 * j;
-  Vec8<T> own[kVecs], part[kVecs];
-  int64_t dst[kVecs];
-  int32_t pos[kVecs];
-  int slot[kVecs];
-  bool key[kVecs];
-  const int pi = partner(i0, r);
-#pragma unroll
-  for (int n = 0; n < kVecs; ++n) {
-    const int64_t vec = v0 + n * VPB + threadIdx.x / TPV;
-    const int ti = (int)(vec / per_tok - t0);
-    const int rem = (int)(vec - (t0 + ti) * per_tok);
-    const Place p = places[ti];
-    dst[n] = -1;
-    key[n] = rem < c.n_kv;
-    if (p.at < 0) continue;
-    const int h = key[n] ? rem : rem - c.n_kv;
-    const T* x = key[n] ? k + (t0 + ti) * a.ks_tok + h * a.ks_head : v + (t0 + ti) * a.vs_tok + h * a.vs_head;
-    own[n] = load8<T>(x + i0);
-    if (key[n] && pi != i0) part[n] = load8<T>(x + pi);
-    dst[n] = (c.head((int)p.at, h) - c.pages) + (int64_t)(p.slot >> 4) * blk_bytes(D);
-    pos[n] = p.pos;
-    slot[n] = p.slot & 15;
+// How a block divides the vectors of its tokens: `toks` tokens of `heads` vectors
+// (keys' heads, then values'), or a part of one token's.
+struct Share {
+  int toks, heads, parts;
+  __host__ __device__ static Share of(int per_tok, int vecs) {
+    Share s;
+    s.parts = (per_tok + vecs - 1) / vecs;
+    s.toks = s.parts > 1 ? 1 : vecs / per_tok;
+    s.heads = s.parts > 1 ? vecs : per_tok;
+    return s;
   }
+};
+constexpr int kVecs = 2;                      // vectors a thread has in flight
+template <int D> __host__ __device__ constexpr int vecs_of_block() { return kStreamThreads / (D / 16) * kVecs; }
+
+// MODE 0: no rotation, 1: halves of the whole head, 2: any.
+template <typename T, int D, int MODE>
+__global__ void __launch_bounds__(kStreamThreads)
+k_append4(Pool c, RopeArgs r, const T* __restrict__ k, const T* __restrict__ v, StreamArgs a, Share sh) {
+  constexpr int TPV = D / 16, VPB = kStreamThreads / TPV, NV = VPB * kVecs;
+  __shared__ Place places[NV];
+  const int64_t t0 = (int64_t)blockIdx.x * sh.toks;
+  const int j = threadIdx.x % TPV, g = threadIdx.x / TPV;
+  Vec8<T> own[kVecs][2], part[MODE == 2 ? kVecs : 1][2];
+  int tok[kVecs], head[kVecs];
+  const int p0 = partner(8 * j, r), p1 = partner(D / 2 + 8 * j, r);
 #pragma unroll
   for (int n = 0; n < kVecs; ++n) {
-    // a vector's threads take this branch together; the shuffles name only them
-    if (dst[n] < 0) continue;
-    float x[8];
-    unpack8<T>(own[n], x);
-    if (key[n] && r.table) {
-      float y[8];
-      if (pi != i0) unpack8<T>(part[n], y);
-      rotate8<T>(x, y, i0, r, pos[n]);
+    const int x = g + n * VPB;
+    tok[n] = x / sh.heads;
+    head[n] = x - tok[n] * sh.heads + (int)blockIdx.y * sh.heads;
+    if (tok[n] >= sh.toks || t0 + tok[n] >= a.n_tok || head[n] >= 2 * c.n_kv) {
+      tok[n] = -1;
+      continue;
     }
-    float mn = x[0], mx = x[0], bad = 0.0f;
+    const bool key = head[n] < c.n_kv;
+    const T* src = key ? k + (t0 + tok[n]) * a.ks_tok + head[n] * a.ks_head : v + (t0 + tok[n]) * a.vs_tok + (head[n] - c.n_kv) * a.vs_head;
+    own[n][0] = load8<T>(src + 8 * j);
+    own[n][1] = load8<T>(src + D / 2 + 8 * j);
+    if (MODE == 2 && key) {
+      part[n][0] = load8<T>(src + p0);
+      part[n][1] = load8<T>(src + p1);
+    }
+  }
+  for (int i = threadIdx.x; i < sh.toks; i += kStreamThreads) places[i] = place_of(c, a, MODE ? r.n_pos : -1, t0 + i);
+  __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      mn = fminf(mn, x[i]);
-      mx = fmaxf(mx, x[i]);
-      bad = fmaf(x[i], 0.0f, bad);      // NaN as soon as one value is not finite
+  for (int n = 0; n < kVecs; ++n) {
+    // a vector's threads take these branches together; the shuffles name only them
+    if (tok[n] < 0) continue;
+    const Place p = places[tok[n]];
+    if (p.at < 0) continue;
+    const bool key = head[n] < c.n_kv;
+    float x[2][8];
+    unpack8<T>(own[n][0], x[0]);
+    unpack8<T>(own[n][1], x[1]);
+    if (MODE == 1 && key) {
+      const float4* row = (const float4*)(r.table + (int64_t)p.pos * D + 8 * j);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const float4 cv = __ldg(row + q), sv = __ldg(row + D / 8 + q);
+        const float cs[4] = {cv.x, cv.y, cv.z, cv.w}, sn[4] = {sv.x, sv.y, sv.z, sv.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float ya = x[0][4 * q + e], yb = x[1][4 * q + e];
+          x[0][4 * q + e] = __fsub_rn(__fmul_rn(ya, cs[e]), __fmul_rn(yb, sn[e]));
+          x[1][4 * q + e] = __fadd_rn(__fmul_rn(yb, cs[e]), __fmul_rn(ya, sn[e]));
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        round2<T>(&x[0][e], &x[0][e + 1]);
+        round2<T>(&x[1][e], &x[1][e + 1]);
+      }
     }
-    bool finite = bad == 0.0f;
-    const unsigned lanes = TPV == 32 ? 0xffffffffu : ((1u << TPV) - 1u) << ((threadIdx.x & 31) / TPV * TPV);
+    if (MODE == 2 && key) {
+      float y[8];
+      unpack8<T>(part[n][0], y);
+      rotate8<T>(x[0], y, 8 * j, r, p.pos);
+      unpack8<T>(part[n][1], y);
+      rotate8<T>(x[1], y, D / 2 + 8 * j, r, p.pos);
+    }
+    float mn = x[0][0], mx = x[0][0];
+#pragma unroll
+    for (int e = 1; e < 16; ++e) {
+      mn = min_nan(mn, x[e >> 3][e & 7]);
+      mx = max_nan(mx, x[e >> 3][e & 7]);
+    }
+    const unsigned lanes = ((1u << TPV) - 1u) << ((threadIdx.x & 31) / TPV * TPV);
 #pragma unroll
     for (int o = 1; o < TPV; o <<= 1) {
-      mn = fminf(mn, __shfl_xor_sync(lanes, mn, o));
-      mx = fmaxf(mx, __shfl_xor_sync(lanes, mx, o));
+      mn = min_nan(mn, __shfl_xor_sync(lanes, mn, o));
+      mx = max_nan(mx, __shfl_xor_sync(lanes, mx, o));
     }
-    finite = __all_sync(lanes, finite);
     float s, m;
-    uint32_t word, w = 0;
-    make_pair(mn, mx, finite, &s, &m, &word);
-    const float inv = s > 0.0f ? __fdiv_rn(1.0f, s) : 0.0f;
+    uint32_t word, w[2] = {0u, 0u};
+    make_pair(mn, mx, &s, &m, &word);
     if (s > 0.0f) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w |= code4(x[i], m, s, inv) << (4 * i);
+      const float inv = __fdiv_rn(1.0f, s);
+      w[0] = codes8(x[0], m, s, inv);
+      w[1] = codes8(x[1], m, s, inv);
     }
-    uint8_t* blk = c.pages + dst[n];
-    const int t = slot[n], side = key[n] ? 0 : 1;
-    *(uint32_t*)(blk + side * v_codes(D) + t * (D / 2) + (((j >> 2) ^ swz(t, D)) << 4) + ((j & 3) << 2)) = w;
+    const int side = key ? 0 : 1, t = p.slot & 15;
+    uint8_t* blk = c.head((int)p.at, head[n] - side * c.n_kv) + (p.slot >> 4) * blk_bytes(D);
+    uint8_t* row = blk + side * v_codes(D) + t * (D / 2) + ((j & 3) << 2);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) *(uint32_t*)(row + ((((j >> 2) + e * (D / 64)) ^ swz(t, D)) << 4)) = w[e];
     if (j == 0) *(uint32_t*)(blk + k_pairs(D) + side * 64 + t * 4) = word;
   }
 }
 
-// x^ = m + s c of the tokens of a call: the product is exact in float (8 + 4
-// bits), the sum is rounded once, then to the output's type.
-template <typename T, int D>
-__global__ void __launch_bounds__(kStreamThreads)
-k_read4(Pool c, T* __restrict__ ko, T* __restrict__ vo, StreamArgs a) {
-  constexpr int TPV = D / 8, VPB = kStreamThreads / TPV;
-  __shared__ Place places[VPB + 1];
-  const int per_tok = 2 * c.n_kv;
-  const int64_t v0 = (int64_t)blockIdx.x * VPB;
-  const int64_t t0 = v0 / per_tok;
-  const int n_here = (int)((v0 + VPB - 1) / per_tok - t0) + 1;
-  for (int i = threadIdx.x; i < n_here; i += kStreamThreads) places[i] = place_of(c, a, -1, t0 + i);
-  __syncthreads();
-  const int j = threadIdx.x % TPV;
-  const int64_t vec = v0 + threadIdx.x / TPV;
-  const int ti = (int)(vec / per_tok - t0);
-  const int rem = (int)(vec - (t0 + ti) * per_tok);
-  const Place p = places[ti];
-  if (p.at < 0) return;
-  const int side = rem < c.n_kv ? 0 : 1, h = rem - side * c.n_kv, t = p.slot & 15;
-  const uint8_t* blk = c.head((int)p.at, h) + (int64_t)(p.slot >> 4) * blk_bytes(D);
-  const uint32_t w = *(const uint32_t*)(blk + side * v_codes(D) + t * (D / 2) + (((j >> 2) ^ swz(t, D)) << 4) + ((j & 3) << 2));
-  const uint32_t pw = *(const uint32_t*)(blk + k_pairs(D) + side * 64 + t * 4);
-  const float s = __uint_as_float(pw << 16), m = __uint_as_float(pw & 0xffff0000u);
+// Eight coordinates of a word: x^ = m + s c, the product exact in float (8 + 4 bits),
+// the sum rounded once, then to the output's type. (A code or'ed into 2^23 is 2^23 + c.)
+template <typename T> __device__ __forceinline__ void values8(uint32_t w, float s, float m, T* out) {
+  const f2 s2 = f2_of(s, s), m2 = f2_of(m, m), b2 = f2_of(-8388608.0f, -8388608.0f);
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    const uint32_t a = (w >> (4 * i)) & 15u | 0x4b000000u, b = (w >> (4 * i + 4)) & 15u | 0x4b000000u;
+    const f2 z = f2_fma(f2_add(f2_of(a, b), b2), s2, m2);
+    y[i] = f2_lo(z);
+    y[i + 1] = f2_hi(z);
+  }
   T e[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) e[i] = from_f<T>(fmaf((float)((w >> (4 * i)) & 15u), s, m));
-  T* out = side ? vo + (t0 + ti) * a.vs_tok + h * a.vs_head : ko + (t0 + ti) * a.ks_tok + h * a.ks_head;
-  const uint4* u = (const uint4*)e;
+  for (int i = 0; i < 8; ++i) e[i] = from_f<T>(y[i]);
 #pragma unroll
-  for (int i = 0; i < (int)sizeof(T) / 2; ++i) ((uint4*)(out + 8 * j))[i] = u[i];
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) ((uint4*)out)[i] = ((const uint4*)e)[i];
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kStreamThreads)
+k_read4(Pool c, T* __restrict__ ko, T* __restrict__ vo, StreamArgs a, Share sh) {
+  constexpr int TPV = D / 16, VPB = kStreamThreads / TPV, NV = VPB * kVecs;
+  __shared__ Place places[NV];
+  const int64_t t0 = (int64_t)blockIdx.x * sh.toks;
+  for (int i = threadIdx.x; i < sh.toks; i += kStreamThreads) places[i] = place_of(c, a, -1, t0 + i);
+  __syncthreads();
+  const int j = threadIdx.x % TPV, g = threadIdx.x / TPV;
+  uint32_t w[kVecs][2], pair[kVecs];
+  int tok[kVecs], head[kVecs];
+#pragma unroll
+  for (int n = 0; n < kVecs; ++n) {
+    const int x = g + n * VPB;
+    tok[n] = x / sh.heads;
+    head[n] = x - tok[n] * sh.heads + (int)blockIdx.y * sh.heads;
+    if (tok[n] >= sh.toks || head[n] >= 2 * c.n_kv) tok[n] = -1;
+    if (tok[n] < 0) continue;
+    const Place p = places[tok[n]];
+    if (p.at < 0) {
+      tok[n] = -1;
+      continue;
+    }
+    const int side = head[n] < c.n_kv ? 0 : 1, t = p.slot & 15;
+    const uint8_t* blk = c.head((int)p.at, head[n] - side * c.n_kv) + (p.slot >> 4) * blk_bytes(D);
+    const uint8_t* row = blk + side * v_codes(D) + t * (D / 2) + ((j & 3) << 2);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) w[n][e] = *(const uint32_t*)(row + ((((j >> 2) + e * (D / 64)) ^ swz(t, D)) << 4));
+    pair[n] = *(const uint32_t*)(blk + k_pairs(D) + side * 64 + t * 4);
+  }
+#pragma unroll
+  for (int n = 0; n < kVecs; ++n) {
+    if (tok[n] < 0) continue;
+    const float s = __uint_as_float(pair[n] << 16), m = __uint_as_float(pair[n] & 0xffff0000u);
+    T* out = (head[n] < c.n_kv ? ko + head[n] * a.ks_head + (t0 + tok[n]) * a.ks_tok
+                               : vo + (head[n] - c.n_kv) * a.vs_head + (t0 + tok[n]) * a.vs_tok) + 8 * j;
+    values8<T>(w[n][0], s, m, out);
+    values8<T>(w[n][1], s, m, out + D / 2);
+  }
 }
 
 }  // namespace kv4

@@ -422,22 +422,6 @@ __device__ __forceinline__ void st16(uint32_t addr, const uint32_t* r) {
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]) : "memory");
 }
-typedef unsigned long long f2;                 // two floats
-__device__ __forceinline__ f2 f2_of(uint32_t lo, uint32_t hi) { return (f2)lo | ((f2)hi << 32); }
-__device__ __forceinline__ f2 f2_of(float lo, float hi) { return f2_of(__float_as_uint(lo), __float_as_uint(hi)); }
-__device__ __forceinline__ float f2_lo(f2 x) { return __uint_as_float((uint32_t)x); }
-__device__ __forceinline__ float f2_hi(f2 x) { return __uint_as_float((uint32_t)(x >> 32)); }
-__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c) {
-  f2 d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ f2 f2_add(f2 a, f2 b) {
-  f2 d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-
 // Registers a thread of this warp group (multiples of 8), which together stay within what the block started with.
 template <int N> __device__ __forceinline__ void set_regs_up() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
