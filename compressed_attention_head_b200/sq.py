@@ -362,8 +362,25 @@ def sq_wait_selftest(limit_us, flags, stream=None):
 
 
 # --------------------------------------------------------------------------- the paged 4-bit cache
+# A decode step of one sequence takes the GPU about ten microseconds, so these bindings
+# spend few on the host: addresses go as plain integers, and the structures of a cache
+# and of a rotation table are made once and again when a field of theirs is set.
+class _Described:
+    """Keeps what describe() made of its fields until one of them is set, or a tensor of them moves."""
+
+    def __setattr__(self, name, value):
+        self.__dict__[name] = value
+        self.__dict__["_made"] = None
+
+    def ref(self):
+        made = self._made
+        if made is None or made[1] != self.where():
+            made = self.__dict__["_made"] = (ctypes.byref(self.struct()), self.where())
+        return made[0]
+
+
 @dataclass
-class PagedKV4:
+class PagedKV4(_Described):
     """Caller-owned pool of pages and the page table of a batch (see sq_kv4_cache in sq.h)."""
 
     pages: torch.Tensor          # uint8 [n_pages, n_kv, page_tokens / 16, 16 d + 128]
@@ -373,6 +390,9 @@ class PagedKV4:
     page_tokens: int
 
     def __post_init__(self):
+        self.check()
+
+    def check(self):
         shape = (self.pages.shape[0], self.n_kv, self.page_tokens // 16, 16 * self.d + 128)
         if self.pages.dtype != torch.uint8 or tuple(self.pages.shape) != shape or not self.pages.is_contiguous():
             raise ValueError(f"pages: a contiguous uint8 tensor of shape {shape} is wanted")
@@ -384,24 +404,35 @@ class PagedKV4:
     def batch(self) -> int:
         return self.table.shape[0]
 
+    def where(self):
+        return self.pages.data_ptr(), self.table.data_ptr(), self.table.shape
+
     def struct(self) -> sq_kv4_cache:
+        self.check()
         return sq_kv4_cache(self.pages.data_ptr(), self.table.data_ptr(), self.pages.shape[0],
                             max(self.table.stride(0), self.table.shape[1]), self.table.shape[0], self.table.shape[1],
                             self.n_kv, self.d, self.page_tokens)
 
 
 @dataclass
-class Rope:
+class Rope(_Described):
     """Rotation table float32 [n_pos, rot_dim]: cosines of rot_dim / 2 angles, then their sines."""
 
     table: torch.Tensor
     interleaved: bool = False
 
     def __post_init__(self):
+        self.check()
+
+    def check(self):
         if self.table.dtype != torch.float32 or self.table.dim() != 2 or not self.table.is_contiguous():
             raise ValueError("rotation table: a contiguous float32 tensor [n_pos, rot_dim] is wanted")
 
+    def where(self):
+        return self.table.data_ptr(), self.table.shape
+
     def struct(self) -> sq_rope:
+        self.check()
         return sq_rope(self.table.data_ptr(), self.table.shape[0], self.table.shape[1], int(self.interleaved))
 
 
@@ -424,64 +455,83 @@ def alloc_kv4(n_pages, n_kv, d, page_tokens, table, device="cuda") -> PagedKV4:
                     table, n_kv, d, page_tokens)
 
 
-def _kv4_here(*tensors):
-    """The tensors of one call live on the current device: a kernel cannot read the others."""
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+def _kv4_call(stream, *tensors):
+    """The stream of a call as an integer. Its tensors live on the current device: a kernel cannot read the others."""
+    dev = tensors[0].get_device()
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.get_device() != dev):
-            raise ValueError(f"every tensor must be on the current device (cuda:{dev}), got one on {t.device}")
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"every tensor must be on the current device, got some on {t.device} and {tensors[0].device}")
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError(f"every tensor must be on the current device, got some on {tensors[0].device}")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _kv4_ints(name, t, n):
-    if t is not None and (t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous()):
+    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous int32 tensor of {n} elements is wanted")
+    return t.data_ptr()
 
 
 def _kv4_heads(name, t, heads, d, rows=None, dtype=None):
-    if (t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d or t.stride(2) != 1 or t.dtype not in DTYPE_CODE
-            or (rows is not None and t.shape[0] != rows) or (dtype is not None and t.dtype != dtype)):
-        raise ValueError(f"{name}: a tensor [{'tokens' if rows is None else rows}, {heads}, {d}] of stride 1 along the "
-                         f"last axis{'' if dtype is None else f' and type {dtype}'} is wanted")
+    """Address, token stride and head stride of a tensor [rows, heads, d] (heads None: any number)."""
+    if t.dim() == 3:
+        n, h, e = t.shape
+        s0, s1, s2 = t.stride()
+        if ((heads is None or h == heads) and e == d and s2 == 1 and t.dtype in DTYPE_CODE
+                and (rows is None or n == rows) and (dtype is None or t.dtype == dtype)):
+            return t.data_ptr(), s0, s1
+    raise ValueError(f"{name}: a tensor [{'tokens' if rows is None else rows}, {'heads' if heads is None else heads}, {d}] "
+                     f"of stride 1 along the last axis{'' if dtype is None else f' and type {dtype}'} is wanted")
 
 
 def _kv4_out(out, lse, q):
-    if tuple(out.shape) != tuple(q.shape) or not out.is_contiguous() or out.dtype not in DTYPE_CODE:
+    """Addresses of the outputs."""
+    shape = q.shape
+    if out.shape != shape or not out.is_contiguous() or out.dtype not in DTYPE_CODE:
         raise ValueError("out: a contiguous tensor of q's shape is wanted")
-    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != tuple(q.shape[:2])
-                            or not lse.is_contiguous()):
+    if lse is None:
+        return out.data_ptr(), None
+    if lse.dtype != torch.float32 or lse.shape != shape[:2] or not lse.is_contiguous():
         raise ValueError("lse: a contiguous float32 tensor [tokens, n_q_heads] is wanted")
+    return out.data_ptr(), lse.data_ptr()
 
 
-def _ref(s):
-    return None if s is None else ctypes.byref(s)
+def _kv4_at(t):
+    return None if t is None else t.data_ptr()
 
 
-def _nbytes(ws):
-    return ws.numel() * ws.element_size() if ws is not None else 0
+def _kv4_bytes(ws):
+    if ws is None:
+        return None, 0
+    if not ws.is_contiguous():
+        raise ValueError("ws: a contiguous tensor is wanted")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def sq_kv4_append(cache, k, v, start, cu=None, rope=None, flags=None, stream=None):
     """Append k, v [tokens, n_kv, d] (any strides but the last axis's) at positions start[b] + i (see sq.h)."""
-    _kv4_here(cache.pages, cache.table, k, v, start, cu, flags, rope.table if rope else None)
-    _kv4_heads("k", k, cache.n_kv, cache.d)
-    _kv4_heads("v", v, cache.n_kv, cache.d, k.shape[0], k.dtype)
-    _kv4_ints("start", start, cache.batch)
-    _kv4_ints("cu", cu, cache.batch + 1)
-    _check(lib().sq_kv4_append(ctypes.byref(cache.struct()), _ptr(k), _ptr(v), DTYPE_CODE[k.dtype], k.stride(0),
-                               k.stride(1), v.stride(0), v.stride(1), k.shape[0], _ptr(cu), _ptr(start),
-                               _ref(rope.struct() if rope else None), _ptr(flags), _stream(stream)), "sq_kv4_append")
+    st = _kv4_call(stream, cache.pages, cache.table, k, v, start, cu, flags, rope.table if rope else None)
+    kp, k0, k1 = _kv4_heads("k", k, cache.n_kv, cache.d)
+    n = k.shape[0]
+    vp, v0, v1 = _kv4_heads("v", v, cache.n_kv, cache.d, n, k.dtype)
+    batch = cache.batch
+    at = _kv4_ints("start", start, batch)
+    cu = None if cu is None else _kv4_ints("cu", cu, batch + 1)
+    _check(lib().sq_kv4_append(cache.ref(), kp, vp, DTYPE_CODE[k.dtype], k0, k1, v0, v1, n, cu, at,
+                               rope.ref() if rope else None, _kv4_at(flags), st), "sq_kv4_append")
 
 
 def sq_kv4_read(cache, start, cu, k_out, v_out, flags=None, stream=None):
     """The tokens at positions start[b] + i, as the cache holds them, into k_out, v_out [tokens, n_kv, d]."""
-    _kv4_here(cache.pages, cache.table, k_out, v_out, start, cu, flags)
-    _kv4_heads("k_out", k_out, cache.n_kv, cache.d)
-    _kv4_heads("v_out", v_out, cache.n_kv, cache.d, k_out.shape[0], k_out.dtype)
-    _kv4_ints("start", start, cache.batch)
-    _kv4_ints("cu", cu, cache.batch + 1)
-    _check(lib().sq_kv4_read(ctypes.byref(cache.struct()), _ptr(k_out), _ptr(v_out), DTYPE_CODE[k_out.dtype],
-                             k_out.stride(0), k_out.stride(1), v_out.stride(0), v_out.stride(1), k_out.shape[0],
-                             _ptr(cu), _ptr(start), _ptr(flags), _stream(stream)), "sq_kv4_read")
+    st = _kv4_call(stream, cache.pages, cache.table, k_out, v_out, start, cu, flags)
+    kp, k0, k1 = _kv4_heads("k_out", k_out, cache.n_kv, cache.d)
+    n = k_out.shape[0]
+    vp, v0, v1 = _kv4_heads("v_out", v_out, cache.n_kv, cache.d, n, k_out.dtype)
+    batch = cache.batch
+    at = _kv4_ints("start", start, batch)
+    cu = None if cu is None else _kv4_ints("cu", cu, batch + 1)
+    _check(lib().sq_kv4_read(cache.ref(), kp, vp, DTYPE_CODE[k_out.dtype], k0, k1, v0, v1, n, cu, at, _kv4_at(flags), st),
+           "sq_kv4_read")
 
 
 def sq_kv4_attn_workspace(batch, n_q_heads, n_kv_heads, d, max_ctx) -> int:
@@ -491,31 +541,30 @@ def sq_kv4_attn_workspace(batch, n_q_heads, n_kv_heads, d, max_ctx) -> int:
 def sq_kv4_attn_decode(cache, seq_lens, q, scale, out, max_ctx, ws, rope=None, window=0, lse=None, flags=None,
                        stream=None):
     """Attention of q [batch, n_q_heads, d] over the first seq_lens[b] tokens of every sequence (see sq.h)."""
-    _kv4_here(cache.pages, cache.table, q, out, seq_lens, lse, ws, flags, rope.table if rope else None)
-    _kv4_heads("q", q, q.shape[1] if q.dim() == 3 else 0, cache.d, cache.batch)
-    _kv4_out(out, lse, q)
-    _kv4_ints("seq_lens", seq_lens, cache.batch)
-    _check(lib().sq_kv4_attn_decode(ctypes.byref(cache.struct()), _ptr(seq_lens), q.shape[1], max_ctx, _ptr(q),
-                                    DTYPE_CODE[q.dtype], q.stride(0), q.stride(1),
-                                    _ref(rope.struct() if rope else None), float(scale), int(window), _ptr(out),
-                                    DTYPE_CODE[out.dtype], _ptr(lse), _ptr(ws), _nbytes(ws), _ptr(flags),
-                                    _stream(stream)), "sq_kv4_attn_decode")
+    st = _kv4_call(stream, cache.pages, cache.table, q, out, seq_lens, lse, ws, flags, rope.table if rope else None)
+    batch = cache.batch
+    qp, q0, q1 = _kv4_heads("q", q, None, cache.d, batch)
+    op, lp = _kv4_out(out, lse, q)
+    wp, wn = _kv4_bytes(ws)
+    _check(lib().sq_kv4_attn_decode(cache.ref(), _kv4_ints("seq_lens", seq_lens, batch), q.shape[1], max_ctx, qp,
+                                    DTYPE_CODE[q.dtype], q0, q1, rope.ref() if rope else None, scale, window, op,
+                                    DTYPE_CODE[out.dtype], lp, wp, wn, _kv4_at(flags), st), "sq_kv4_attn_decode")
 
 
 def sq_kv4_decode_step(cache, k, v, q, pos, scale, out, max_ctx, ws, rope=None, window=0, lse=None, flags=None,
                        stream=None):
     """Append one token a sequence at pos[b], then attend over pos[b] + 1 tokens (see sq.h)."""
-    _kv4_here(cache.pages, cache.table, k, v, q, out, pos, lse, ws, flags, rope.table if rope else None)
-    _kv4_heads("q", q, q.shape[1] if q.dim() == 3 else 0, cache.d, cache.batch)
-    _kv4_heads("k", k, cache.n_kv, cache.d, cache.batch, q.dtype)
-    _kv4_heads("v", v, cache.n_kv, cache.d, cache.batch, q.dtype)
-    _kv4_out(out, lse, q)
-    _kv4_ints("pos", pos, cache.batch)
-    _check(lib().sq_kv4_decode_step(ctypes.byref(cache.struct()), _ptr(k), _ptr(v), _ptr(q), DTYPE_CODE[q.dtype],
-                                    k.stride(0), k.stride(1), v.stride(0), v.stride(1), q.stride(0), q.stride(1),
-                                    _ptr(pos), q.shape[1], max_ctx, _ref(rope.struct() if rope else None),
-                                    float(scale), int(window), _ptr(out), DTYPE_CODE[out.dtype], _ptr(lse), _ptr(ws),
-                                    _nbytes(ws), _ptr(flags), _stream(stream)), "sq_kv4_decode_step")
+    st = _kv4_call(stream, cache.pages, cache.table, k, v, q, out, pos, lse, ws, flags, rope.table if rope else None)
+    batch, n_kv, d, dtype = cache.batch, cache.n_kv, cache.d, q.dtype
+    qp, q0, q1 = _kv4_heads("q", q, None, d, batch)
+    kp, k0, k1 = _kv4_heads("k", k, n_kv, d, batch, dtype)
+    vp, v0, v1 = _kv4_heads("v", v, n_kv, d, batch, dtype)
+    op, lp = _kv4_out(out, lse, q)
+    wp, wn = _kv4_bytes(ws)
+    _check(lib().sq_kv4_decode_step(cache.ref(), kp, vp, qp, DTYPE_CODE[dtype], k0, k1, v0, v1, q0, q1,
+                                    _kv4_ints("pos", pos, batch), q.shape[1], max_ctx, rope.ref() if rope else None,
+                                    scale, window, op, DTYPE_CODE[out.dtype], lp, wp, wn, _kv4_at(flags), st),
+           "sq_kv4_decode_step")
 
 
 def sq_kv4_attn_prefill_workspace(batch, n_q_heads, n_kv_heads, d, n_tok) -> int:
@@ -524,13 +573,12 @@ def sq_kv4_attn_prefill_workspace(batch, n_q_heads, n_kv_heads, d, n_tok) -> int
 
 def sq_kv4_attn_prefill(cache, start, cu, q, scale, out, ws, rope=None, window=0, lse=None, flags=None, stream=None):
     """Causal attention of q [tokens, n_q_heads, d], token cu[b] + i at position start[b] + i (see sq.h)."""
-    _kv4_here(cache.pages, cache.table, q, out, start, cu, lse, ws, flags, rope.table if rope else None)
-    _kv4_heads("q", q, q.shape[1] if q.dim() == 3 else 0, cache.d)
-    _kv4_out(out, lse, q)
-    _kv4_ints("start", start, cache.batch)
-    _kv4_ints("cu", cu, cache.batch + 1)
-    _check(lib().sq_kv4_attn_prefill(ctypes.byref(cache.struct()), _ptr(cu), _ptr(start), q.shape[1], q.shape[0],
-                                     _ptr(q), DTYPE_CODE[q.dtype], q.stride(0), q.stride(1),
-                                     _ref(rope.struct() if rope else None), float(scale), int(window), _ptr(out),
-                                     DTYPE_CODE[out.dtype], _ptr(lse), _ptr(ws), _nbytes(ws), _ptr(flags),
-                                     _stream(stream)), "sq_kv4_attn_prefill")
+    st = _kv4_call(stream, cache.pages, cache.table, q, out, start, cu, lse, ws, flags, rope.table if rope else None)
+    batch = cache.batch
+    qp, q0, q1 = _kv4_heads("q", q, None, cache.d)
+    op, lp = _kv4_out(out, lse, q)
+    wp, wn = _kv4_bytes(ws)
+    _check(lib().sq_kv4_attn_prefill(cache.ref(), _kv4_ints("cu", cu, batch + 1), _kv4_ints("start", start, batch),
+                                     q.shape[1], q.shape[0], qp, DTYPE_CODE[q.dtype], q0, q1, rope.ref() if rope else None,
+                                     scale, window, op, DTYPE_CODE[out.dtype], lp, wp, wn, _kv4_at(flags), st),
+           "sq_kv4_attn_prefill")
