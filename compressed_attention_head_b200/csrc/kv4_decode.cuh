@@ -203,23 +203,19 @@ __device__ Plan make_plan(const Pool& c, const RopeArgs& r, const AttnArgs& a, i
   return p;
 }
 
-// Walks a warp's tiles along the line and fetches their page numbers one tile ahead of their copies.
+// A tile on the line: its pair (sequence, heads) and its place in that.
 template <int D>
 struct Cursor {
   int row, hsub, tile, nt;        // nt: the pair's tiles, rounded up
   int lo, hi;
-  int64_t left;                   // tiles to the block's end, from this one
   __device__ __forceinline__ void enter(const Pool& c, const RopeArgs& r, const AttnArgs& a, int unit) {
     const Span s = span_of(c, r, a, row, nullptr);
     lo = s.lo;
     hi = s.hi;
     nt = (tiles_of<Cfg<D>::TT>(s) + unit - 1) / unit * unit;
   }
-  __device__ __forceinline__ void advance(const Pool& c, const RopeArgs& r, const AttnArgs& a, int unit, int per_row,
-                                          int by) {
-    left -= by;
-    if (left <= 0) return;
-    tile += by;
+  // Into the pairs behind this one, when its tiles are used up.
+  __device__ __forceinline__ void carry(const Pool& c, const RopeArgs& r, const AttnArgs& a, int unit, int per_row) {
     while (tile >= nt) {
       tile -= nt;
       if (++hsub == per_row) {
@@ -231,6 +227,8 @@ struct Cursor {
       }
     }
   }
+  // First position of the tile.
+  __device__ __forceinline__ int first() const { return (lo / Cfg<D>::TT + tile) * Cfg<D>::TT; }
 };
 
 template <typename T, typename TO, int D, bool PAIR>
@@ -272,34 +270,46 @@ k_decode4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, Att
   if (tid == 0) descs[blockIdx.x].parts = 0;
   if (first >= last) return;
 
-  // ---- the warp's copies
+  // ---- the warp's copies: its tiles are warp, warp + W, ... of the block's `count`
+  const int count = (int)(last - first);
   Cursor<D> ahead;
   ahead.row = plan.row;
   ahead.enter(c, r, a, plan.unit);
   ahead.hsub = (int)((first - plan.row_at) / ahead.nt);
   ahead.tile = (int)((first - plan.row_at) % ahead.nt);
   const int row0 = ahead.row, hsub0 = ahead.hsub, tile0 = ahead.tile;
-  ahead.left = last - first;
-  ahead.advance(c, r, a, plan.unit, per_row, warp);
-  int pf_page = 0;
-  int64_t pf_off = 0;
-  bool pf_in = false;
-  // page number of the cursor's tile (lanes below NB: a 16-token block each)
-  auto look = [&]() {
-    pf_in = false;
-    if (ahead.left > 0 && lane < C::NB) {
-      const int t = (ahead.lo / C::TT + ahead.tile) * C::TT + 16 * lane;
-      if (t < ahead.hi && t + 16 > ahead.lo) {
-        pf_in = true;
-        pf_page = __ldg(c.table + ahead.row * c.table_stride + (t >> c.page_shift));
-        pf_off = ((((int64_t)(ahead.hsub / nsub)) << (c.page_shift - 4)) + ((t & ((1 << c.page_shift) - 1)) >> 4)) * blk_bytes(D);
-      }
-    }
-  };
   const int64_t page_bytes = ((int64_t)c.n_kv << (c.page_shift - 4)) * blk_bytes(D);
+  const int in_page = (1 << c.page_shift) - 1;
+  int next = warp, t_next = 0;         // the tile to copy next, and its first position
+  const int32_t* table = nullptr;      // its sequence's pages, and its head's bytes in a page
+  const uint8_t* head = nullptr;
+  auto in_pair = [&]() {
+    if (next >= count) return;
+    ahead.carry(c, r, a, plan.unit, per_row);
+    t_next = ahead.first() + 16 * lane;
+    table = c.table + ahead.row * c.table_stride;
+    head = c.pages + ((int64_t)(ahead.hsub / nsub) << (c.page_shift - 4)) * blk_bytes(D);
+  };
+  ahead.tile += warp;
+  in_pair();
+  // Lanes below NB: a 16-token block each, its page number asked for a tile before its copy.
+  int pf_page = -1;                    // -1: none
+  const uint8_t* pf_from = nullptr;
+  auto look = [&]() {
+    pf_page = -1;
+    if (lane < C::NB && next < count && t_next < ahead.hi && t_next + 16 > ahead.lo) {
+      const int page = __ldg(table + (t_next >> c.page_shift));
+      pf_page = page < 0 ? 0x7fffffff : page;
+      pf_from = head + ((t_next & in_page) >> 4) * blk_bytes(D);
+    }
+    next += W;
+    ahead.tile += W;
+    t_next += W * C::TT;
+    if (ahead.tile >= ahead.nt) in_pair();
+  };
   auto issue = [&](int st) {
-    const bool ok = pf_in && pf_page >= 0 && pf_page < c.n_pages;
-    if (pf_in && !ok) raise(a.flags, SQ_FLAG_PAGE);
+    const bool ok = pf_page >= 0 && pf_page < c.n_pages;
+    if (pf_page >= 0 && !ok) raise(a.flags, SQ_FLAG_PAGE);
     const uint32_t mask = __ballot_sync(0xffffffffu, ok);
     if (lane == 0) {
       oks[warp][st] = mask;
@@ -307,14 +317,13 @@ k_decode4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, Att
     }
     __syncwarp();
     if (ok)
-      sm100::bulk_load(ring + st * C::STAGE + lane * blk_bytes(D), c.pages + pf_page * page_bytes + pf_off,
-                       blk_bytes(D), &bars[warp][st]);
+      sm100::bulk_load(ring + st * C::STAGE + lane * blk_bytes(D), pf_from + pf_page * page_bytes, blk_bytes(D),
+                       &bars[warp][st]);
   };
   look();
 #pragma unroll
   for (int i = 0; i < C::NST - 1; ++i) {
     issue(i);
-    ahead.advance(c, r, a, plan.unit, per_row, W);
     look();
   }
 
@@ -330,14 +339,15 @@ k_decode4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, Att
   at.enter(c, r, a, plan.unit);
   at.hsub = hsub0;
   at.tile = tile0;
-  int64_t seg = first;                           // line position of the segment's first tile in this block
+  int seg = 0;                                   // the segment's first tile of this block
   int stage = 0;
   uint32_t phase = 0;
   bool dead = false;
-  int64_t mine = first + warp;
+  int mine = warp;
 
-  while (seg < last) {
-    const int64_t seg_end = min(last, seg + (at.nt - at.tile));
+  while (seg < count) {
+    const int seg_end = min(count, seg + (at.nt - at.tile));
+    const int pos0 = at.first();                 // the segment's first position
     const int kvh = at.hsub / nsub, h0 = kvh * a.group + (at.hsub % nsub) * HS;
     const int nh = min(HS, (kvh + 1) * a.group - h0);
     // ---- the query operand: D / 8 threads a head
@@ -423,15 +433,13 @@ k_decode4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, Att
       for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
 
     for (; mine < seg_end; mine += W) {
-      const int tile = at.tile + (int)(mine - seg);
       // the next copy goes into the stage that the tile before this one has left
       {
         int st = stage + C::NST - 1;
         st = st >= C::NST ? st - C::NST : st;
         __syncwarp();
-        if (!dead && ahead.left > 0) issue(st);
-        if (ahead.left > 0) {
-          ahead.advance(c, r, a, plan.unit, per_row, W);
+        if (!dead && mine + (C::NST - 1) * W < count) {
+          issue(st);
           look();
         }
       }
@@ -442,7 +450,7 @@ k_decode4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, Att
       const uint8_t* sp = ring + stage * C::STAGE;
       const uint32_t okm = dead ? 0u : oks[warp][stage];
       stage = stage + 1 == C::NST ? 0 : stage + 1;
-      const int t0 = (at.lo / C::TT + tile) * C::TT;
+      const int t0 = pos0 + (mine - seg) * C::TT;
       const bool edge = okm != (1u << C::NB) - 1u || t0 < at.lo || t0 + C::TT > at.hi;
       if (okm == 0) continue;
       // ---- scores
@@ -617,7 +625,7 @@ k_decode4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, Att
       fw[i] = mref[i] == -INFINITY ? (lsum[i] == 0.0f ? 0.0f : 1.0f) : ex2(mref[i] - top);
       fw[i] *= 0x1p13f;                          // 2^24 of the codes over kTop; the reference step follows
     }
-    const bool starts = at.tile == 0, ends = seg + (at.nt - at.tile) <= last;
+    const bool starts = at.tile == 0, ends = seg + (at.nt - at.tile) <= count;
     float* slot = parts + ((int64_t)2 * blockIdx.x + (starts ? 1 : 0)) * part_floats(D);
 #pragma unroll
     for (int jr = 0; jr < NC / 2; ++jr) {
@@ -668,12 +676,12 @@ k_decode4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, Att
       __syncthreads();
     }
     if (starts && !ends && tid == 0) {
-      const int64_t end = seg + at.nt;           // line position behind the pair
+      const int64_t end = first + seg + at.nt;   // line position behind the pair
       descs[blockIdx.x] = Desc{(int)((end - 1) / plan.quota) - (int)blockIdx.x + 1, at.row, at.hsub, 0};
     }
     // ---- the next pair
     seg = seg_end;
-    if (seg < last) {
+    if (seg < count) {
       at.tile = 0;
       if (++at.hsub == per_row) {
         at.hsub = 0;
