@@ -164,6 +164,12 @@ __device__ __forceinline__ f2 f2_add(f2 a, f2 b) {
   return d;
 }
 
+// The power of two at or above x >= 0, within the floats whose reciprocals are normal too.
+__device__ __forceinline__ float pow2_up(float x) {
+  const uint32_t u = (__float_as_uint(x) + 0x7fffffu) & 0x7f800000u;
+  return fminf(fmaxf(__uint_as_float(u), 0x1p-100f), 0x1p127f);
+}
+
 __device__ __forceinline__ float min_nan(float a, float b) {
   float d;
   asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));

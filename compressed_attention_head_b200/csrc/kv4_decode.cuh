@@ -2,9 +2,9 @@
 //
 // Mathematics. With q' = q 2^e (a power of two a head, so that fp16 holds it) and
 // codes c, the score of token t is s_t (q . c_t) + m_t sum(q), and the output is
-// sum_t (p_t s_t) c_t + sum_t p_t m_t: the tensor cores multiply the codes
-// themselves, and the pairs act on scores and probabilities, one token at a time,
-// never on coordinates. A code of 4 bits masked out of its word in place is the
+// sum_t (p_t s_t) (c_t - 8) + sum_t p_t (m_t + 8 s_t): the tensor cores multiply the
+// codes themselves, and the pairs act on scores and probabilities, one token at a
+// time, never on coordinates. A code of 4 bits masked out of its word in place is the
 // fp16 subnormal c 2^-24 (bits 0-3) or 16 c 2^-24 (bits 4-7) in each half of the
 // word: one AND makes two operands, exactly, and the 16 goes into q' or out of the
 // sum. ldmatrix (for the values, its transposed form) lays the words out so that
@@ -13,10 +13,12 @@
 // Softmax: one pass, base 2. Each warp keeps a reference maximum a head, raised
 // when a score passes it by more than 2^4 (one vote a tile), and a reference step
 // (a power of two over all value steps it has met), so that p s, scaled to at most
-// 2^15, keeps fp16's full precision; it enters the product as a high and a low
-// half, 22 bits in all. With up to four query heads a KV head the halves take the
-// two columns a head has in the N = 8 of the product; with up to eight the low
-// halves are a second product into the same accumulators.
+// 2^15, keeps fp16's full precision. The 8 that is taken from the codes is taken
+// times the sum of the rounded p s, which one more product with ones gives: so a
+// rounding (half a step, 2^-11) meets at most 8 of the 15 codes, and the part of a
+// value that all its coordinates share stays in float. Up to four query heads a KV
+// head take every other column of the product, so that each lane has one head to
+// score; up to eight take all.
 //
 // Work. The tiles of all (sequence, KV head) pairs form one line that the resident
 // blocks (two an SM) share evenly, whatever the lengths; inside a block tile i goes
@@ -242,7 +244,7 @@ k_decode4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, Att
   __shared__ __align__(8) uint64_t bars[W][C::NST];
   __shared__ uint32_t oks[W][C::NST];
   __shared__ int64_t red[W];
-  __shared__ float s_q[kMaxHeads][2];           // score factor (of q . c) and m factor, a head
+  __shared__ float s_q[kMaxHeads][2];           // a head's score factor, and sum(q') 2^-24
   __shared__ float s_ml[W][kMaxHeads][4];       // a warp's max, sum, sum of p m, scale of its sums
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, cc = lane & 3;
@@ -352,8 +354,9 @@ k_decode4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, Att
     const int nh = min(HS, (kvh + 1) * a.group - h0);
     // ---- the query operand: D / 8 threads a head
     __syncthreads();
-    for (int base = 0; base < HS * (D / 8); base += 32 * W) {
-      const int i = base + tid, hh = i / (D / 8), j = i % (D / 8);
+    for (int base = 0; base < kMaxHeads * (D / 8); base += 32 * W) {
+      const int i = base + tid, col = i / (D / 8), j = i % (D / 8);
+      const int hh = PAIR ? ((col & 1) ? kMaxHeads : col >> 1) : col;      // (odd columns of pairs are empty)
       float x[8];
       if (hh < nh) {
         const T* src = q + (int64_t)at.row * a.qs_tok + (int64_t)(h0 + hh) * a.qs_head;
@@ -390,43 +393,37 @@ k_decode4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, Att
       }
 #pragma unroll
       for (int o = 1; o < D / 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      if (hh < HS) {
-        *(uint4*)(qop + hh * C::QROW + j * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-        if (j == 0) {
-          const float f = a.scale * 1.4426950408889634f;
-          s_q[hh][0] = f * ldexpf(1.0f, 24 - e2);
-          s_q[hh][1] = f * ldexpf(sum, -e2);
+      if (col < kMaxHeads) {
+        *(uint4*)(qop + col * C::QROW + j * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+        if (j == 0 && hh < HS) {
+          s_q[hh][0] = a.scale * 1.4426950408889634f * ldexpf(1.0f, 24 - e2);
+          s_q[hh][1] = ldexpf(sum, -24);
         }
       }
     }
     __syncthreads();
-    // lane (g, cc): column g of the query operand; in pairs, the odd columns are empty
-    const int qhead = PAIR ? g >> 1 : g;
-    const uint32_t qkeep = PAIR && (g & 1) ? 0u : 0xffffffffu;
-    const uint8_t* qsrc = qop + qhead * C::QROW + cc * 16;
-    uint32_t qf[C::QREG ? NC : 1][4];
+    // lane (g, cc): column g of the query operand
+    const uint8_t* qsrc = qop + g * C::QROW + cc * 16;
+    uint4 qf[C::QREG ? NC : 1];
     if constexpr (C::QREG) {
 #pragma unroll
-      for (int j = 0; j < NC; ++j) {
-        const uint4 u = *(const uint4*)(qsrc + j * 64);
-        qf[j][0] = u.x & qkeep;
-        qf[j][1] = u.y & qkeep;
-        qf[j][2] = u.z & qkeep;
-        qf[j][3] = u.w & qkeep;
-      }
+      for (int j = 0; j < NC; ++j) qf[j] = *(const uint4*)(qsrc + j * 64);
     }
     constexpr int NHL = PAIR ? 1 : 2;            // heads a lane scores: cc, or 2 cc and 2 cc + 1
-    float fq[NHL], fm[NHL], mref[NHL], lsum[NHL], msum[NHL];
+    // nref: what is added to a score, minus the maximum referred to (+inf while there is none)
+    float fq[NHL], fm[NHL], nref[NHL], lsum[NHL], msum[NHL];
 #pragma unroll
     for (int i = 0; i < NHL; ++i) {
       const int hh = PAIR ? cc : 2 * cc + i;
       fq[i] = s_q[hh][0];
       fm[i] = s_q[hh][1];
-      mref[i] = -INFINITY;
+      nref[i] = INFINITY;
       lsum[i] = msum[i] = 0.0f;
     }
     float sref = 0.0f, sinv = 0.0f;              // reference step, and kTop over it
-    float acc[D / 16][4];
+    float acc[D / 16][4], tot[4];                // sums of p s c, and of the rounded p s
+#pragma unroll
+    for (int j = 0; j < 4; ++j) tot[j] = 0.0f;
 #pragma unroll
     for (int i = 0; i < D / 16; ++i)
 #pragma unroll
@@ -454,7 +451,8 @@ k_decode4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, Att
       const bool edge = okm != (1u << C::NB) - 1u || t0 < at.lo || t0 + C::TT > at.hi;
       if (okm == 0) continue;
       // ---- scores
-      float t[C::NB][2][NHL], vs[C::NB][2], vm[C::NB][2];
+      float u[C::NB][2][NHL], t[C::NB][2][NHL], vs[C::NB][2], vm[C::NB][2];
+      bool over = false;
 #pragma unroll
       for (int n = 0; n < C::NB; ++n) {
         float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -464,20 +462,12 @@ k_decode4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, Att
           ldsm4(sb + n * blk_bytes(D) + (koff ^ (j << 4)), w);
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            uint32_t b[4];
-            if constexpr (C::QREG) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) b[e] = qf[j + k][e];
-            } else {
-              const uint4 u = *(const uint4*)(qsrc + (j + k) * 64);
-              b[0] = u.x & qkeep;
-              b[1] = u.y & qkeep;
-              b[2] = u.z & qkeep;
-              b[3] = u.w & qkeep;
-            }
+            uint4 b;
+            if constexpr (C::QREG) b = qf[j + k];
+            else b = *(const uint4*)(qsrc + (j + k) * 64);
             const uint32_t x = w[2 * k], y = w[2 * k + 1], xs = x >> 8, ys = y >> 8;
-            mma(s, x & 0x000f000fu, y & 0x000f000fu, x & 0x00f000f0u, y & 0x00f000f0u, b[0], b[1]);
-            mma(s, xs & 0x000f000fu, ys & 0x000f000fu, xs & 0x00f000f0u, ys & 0x00f000f0u, b[2], b[3]);
+            mma(s, x & 0x000f000fu, y & 0x000f000fu, x & 0x00f000f0u, y & 0x00f000f0u, b.x, b.y);
+            mma(s, xs & 0x000f000fu, ys & 0x000f000fu, xs & 0x00f000f0u, ys & 0x00f000f0u, b.z, b.w);
           }
         }
 #pragma unroll
@@ -486,9 +476,12 @@ k_decode4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, Att
           const uint32_t vw = *(const uint32_t*)(sp + n * blk_bytes(D) + v_pairs(D) + (g + 8 * e) * 4);
           const float ks = __uint_as_float(kw << 16), km = __uint_as_float(kw & 0xffff0000u);
           vs[n][e] = __uint_as_float(vw << 16);
-          vm[n][e] = __uint_as_float(vw & 0xffff0000u);
+          vm[n][e] = fmaf(8.0f, vs[n][e], __uint_as_float(vw & 0xffff0000u));
 #pragma unroll
-          for (int i = 0; i < NHL; ++i) t[n][e][i] = fmaf(ks, s[2 * e + i] * fq[i], km * fm[i]);
+          for (int i = 0; i < NHL; ++i) {
+            u[n][e][i] = fmaf(ks, s[2 * e + i], km * fm[i]);
+            t[n][e][i] = fmaf(u[n][e][i], fq[i], nref[i]);
+          }
         }
       }
       if (edge) {
@@ -500,19 +493,18 @@ k_decode4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, Att
             if (p < at.lo || p >= at.hi || !((okm >> n) & 1u)) {
               vs[n][e] = vm[n][e] = 0.0f;
 #pragma unroll
-              for (int i = 0; i < NHL; ++i) t[n][e][i] = -INFINITY;
+              for (int i = 0; i < NHL; ++i) u[n][e][i] = t[n][e][i] = -INFINITY;
             }
           }
       }
       // ---- the references
-      bool over = false;
 #pragma unroll
       for (int n = 0; n < C::NB; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           over |= vs[n][e] > sref;
 #pragma unroll
-          for (int i = 0; i < NHL; ++i) over |= !(t[n][e][i] <= mref[i] + kSlack);
+          for (int i = 0; i < NHL; ++i) over |= t[n][e][i] > kSlack;
         }
       if (__any_sync(0xffffffffu, over)) {
         float st = 0.0f;
@@ -523,8 +515,7 @@ k_decode4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, Att
         float down = 1.0f;
         if (st > sref) {
           // the power of two at or above the step, kept where its reciprocal stays a float
-          const uint32_t u = (__float_as_uint(st) + 0x7fffffu) & 0x7f800000u;
-          const float ns = fminf(fmaxf(__uint_as_float(u), 0x1p-100f), 0x1p126f);
+          const float ns = fminf(pow2_up(st), 0x1p126f);
           down = sref / ns;
           sref = ns;
           sinv = kTop / ns;
@@ -533,56 +524,50 @@ k_decode4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, Att
         for (int i = 0; i < NHL; ++i) {
           float mx = -INFINITY;
 #pragma unroll
-          for (int n = 0; n < C::NB; ++n) mx = fmaxf(mx, fmaxf(t[n][0][i], t[n][1][i]));
+          for (int n = 0; n < C::NB; ++n) mx = fmaxf(mx, fmaxf(u[n][0][i], u[n][1][i]));
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+          mx *= fq[i];
           float f = 1.0f;
-          if (mx > mref[i]) {
-            f = ex2(mref[i] - mx);             // 0 the first time
-            mref[i] = mx;
+          if (mx > -nref[i]) {
+            f = ex2(-nref[i] - mx);            // 0 the first time
+            nref[i] = -mx;
             lsum[i] *= f;
             msum[i] *= f;
           }
           f *= down;
 #pragma unroll
-          for (int m = 0; m < D / 16; ++m) {
-            if constexpr (PAIR) {
+          for (int j = 0; j < 4; ++j)
+            if (PAIR || (j & 1) == i) tot[j] *= f;
 #pragma unroll
-              for (int j = 0; j < 4; ++j) acc[m][j] *= f;
-            } else {
-              acc[m][i] *= f;
-              acc[m][2 + i] *= f;
-            }
-          }
+          for (int m = 0; m < D / 16; ++m)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (PAIR || (j & 1) == i) acc[m][j] *= f;
+#pragma unroll
+          for (int n = 0; n < C::NB; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) t[n][e][i] = u[n][e][i] == -INFINITY ? -INFINITY : fmaf(u[n][e][i], fq[i], nref[i]);
         }
       }
       // ---- probabilities, and the values' product
 #pragma unroll
       for (int n = 0; n < C::NB; ++n) {
-        uint32_t bh[2], bl[2];
+        uint32_t b[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float ps[2];
+          float ps[2] = {0.0f, 0.0f};
+          const float step = vs[n][e] * sinv;
 #pragma unroll
           for (int i = 0; i < NHL; ++i) {
-            const float base = mref[i] == -INFINITY ? 0.0f : mref[i];
-            const float p = ex2(t[n][e][i] - base);
+            const float p = ex2(t[n][e][i]);
             lsum[i] += p;
             msum[i] = fmaf(p, vm[n][e], msum[i]);
-            ps[i] = p * (vs[n][e] * sinv);
+            ps[i] = p * step;
           }
-          if constexpr (PAIR) {
-            const __half hi = __float2half_rn(ps[0]);
-            const __half lo = __float2half_rn(ps[0] - __half2float(hi));
-            const __half2 hl = __halves2half2(hi, lo);
-            bh[e] = movm(*(const uint32_t*)&hl);
-          } else {
-            const uint32_t hi = pack_h2(ps[0], ps[1]);
-            const float2 f = unpack_h2(hi);
-            bh[e] = movm(hi);
-            bl[e] = movm(pack_h2(ps[0] - f.x, ps[1] - f.y));
-          }
+          b[e] = movm(pack_h2(ps[0], ps[1]));
         }
+        mma(tot, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, b[0], b[1]);
 #pragma unroll
         for (int j = 0; j < NC; j += 2) {
           uint32_t w[4];
@@ -593,8 +578,7 @@ k_decode4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, Att
             const int sh = p < 2 ? 0 : 8;
             const uint32_t a0 = (w[0] >> sh) & mask, a1 = (w[1] >> sh) & mask, a2 = (w[2] >> sh) & mask,
                            a3 = (w[3] >> sh) & mask;
-            mma(acc[2 * j + p], a0, a1, a2, a3, bh[0], bh[1]);
-            if constexpr (!PAIR) mma(acc[2 * j + p], a0, a1, a2, a3, bl[0], bl[1]);
+            mma(acc[2 * j + p], a0, a1, a2, a3, b[0], b[1]);
           }
         }
       }
@@ -610,7 +594,7 @@ k_decode4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, Att
       }
       if (g == 0) {
         float* ml = s_ml[warp][PAIR ? cc : 2 * cc + i];
-        ml[0] = mref[i];
+        ml[0] = -nref[i];
         ml[1] = lsum[i];
         ml[2] = msum[i];
       }
@@ -622,8 +606,8 @@ k_decode4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, Att
       const int hh = PAIR ? cc : 2 * cc + i;
       float top = -INFINITY;
       for (int w = 0; w < W; ++w) top = fmaxf(top, s_ml[w][hh][0]);
-      fw[i] = mref[i] == -INFINITY ? (lsum[i] == 0.0f ? 0.0f : 1.0f) : ex2(mref[i] - top);
-      fw[i] *= 0x1p13f;                          // 2^24 of the codes over kTop; the reference step follows
+      fw[i] = nref[i] == INFINITY ? (lsum[i] == 0.0f ? 0.0f : 1.0f) : ex2(-nref[i] - top);
+      fw[i] *= sref / kTop;
     }
     const bool starts = at.tile == 0, ends = seg + (at.nt - at.tile) <= count;
     float* slot = parts + ((int64_t)2 * blockIdx.x + (starts ? 1 : 0)) * part_floats(D);
@@ -640,8 +624,7 @@ k_decode4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, Att
 #pragma unroll
           for (int p = 0; p < 4; ++p) {
             const float* x = acc[4 * jr + p];
-            const float v = PAIR ? x[2 * half] + x[2 * half + 1] : x[2 * half + i];
-            o[p] = v * fw[i] * sref * ((p & 1) ? 0.0625f : 1.0f);
+            o[p] = fmaf(x[2 * half + i], (p & 1) ? 0x1p20f : 0x1p24f, -8.0f * tot[i]) * fw[i];
           }
           *(float4*)(merge + (warp * HS + hh) * 64 + 32 * half + 4 * g) = o4;
         }

@@ -430,12 +430,6 @@ template <int N> __device__ __forceinline__ void set_regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// The power of two at or above x >= 0, within the floats whose reciprocals are normal too.
-__device__ __forceinline__ float pow2_up(float x) {
-  const uint32_t u = (__float_as_uint(x) + 0x7fffffu) & 0x7f800000u;
-  return fminf(fmaxf(__uint_as_float(u), 0x1p-100f), 0x1p127f);
-}
-
 // Descriptors of an operand in shared memory: keys and queries (coordinates run
 // along k, 64 of a row's in a 128-byte swizzled line), their last step (no swizzle,
 // 16-byte rows of 8 by 8 cores), values (coordinates run along n, tokens along k).
