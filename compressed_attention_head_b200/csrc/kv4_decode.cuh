@@ -61,11 +61,12 @@ template <int D> struct Cfg {
   static constexpr int NST = D == 64 ? 4 : 2;             // tiles in a warp's ring
   static constexpr int QROW = 2 * D + 64;                 // bytes of a head's query operand (64 over: conflict-free)
   static constexpr bool QREG = D <= 128;                  // the query operand stays in registers
+  static constexpr int MC = D == 64 ? 64 : 128;           // coordinates of a round of the sum over the warps
 };
 
 template <int D> struct Smem {
   static constexpr int RING = W * Cfg<D>::NST * Cfg<D>::STAGE;
-  static constexpr int MERGE = W * kMaxHeads * 64 * 4;
+  static constexpr int MERGE = W * kMaxHeads * Cfg<D>::MC * 4;
   static constexpr int Q = kMaxHeads * Cfg<D>::QROW;
   static constexpr int TOTAL = RING + MERGE + Q;
 };
@@ -129,12 +130,14 @@ template <int TT> __device__ __forceinline__ int tiles_of(Span s) {
   return s.hi > 0 ? (s.hi - 1) / TT - s.lo / TT + 1 : 0;
 }
 
-// The line of tiles: `line` tiles in all (each pair's count rounded up to
-// `unit`), `quota` to a block.
+// The line: every pair's tiles (their count rounded up to `unit`) behind `pair`
+// empty places, which stand for what a pair costs besides (its query, the sum over
+// the warps: about as long as sixteen tiles); `line` places in all, `quota` a block.
+constexpr int kPair = 16;
 struct Plan {
   int64_t line;
-  int quota, unit;
-  int row;                 // of the block's first tile
+  int quota, unit, pair;
+  int row;                 // of the block's first place
   int64_t row_at;          // and where that row begins on the line
 };
 
@@ -155,10 +158,10 @@ __device__ Plan make_plan(const Pool& c, const RopeArgs& r, const AttnArgs& a, i
   __shared__ int s_row;
   __shared__ int64_t s_at;
   const int tid = threadIdx.x, lane = tid & 31;
-  int64_t n = 0, padded = 0;
+  int64_t n = 0, padded = 0;                 // places of a line of either kind
   for (int b = tid; b < c.batch; b += 32 * W) {
     const int t = tiles_of<TT>(span_of(c, r, a, b, nullptr));
-    n += t;
+    n += t ? t + kPair : 0;
     padded += (t + W - 1) / W * W;
   }
   n = block_sum(n, red) * per_row;
@@ -169,6 +172,7 @@ __device__ Plan make_plan(const Pool& c, const RopeArgs& r, const AttnArgs& a, i
   p.unit = padded <= (int64_t)gridDim.x * W ? W : 1;
   p.line = p.unit == W ? padded : n;
   p.quota = p.unit == W ? W : (int)((n + gridDim.x - 1) / gridDim.x);
+  p.pair = p.unit == W ? 0 : kPair;
   const int64_t first = (int64_t)blockIdx.x * p.quota;
   if (tid == 0) s_row = -1;
   int64_t carry = 0;
@@ -176,7 +180,7 @@ __device__ Plan make_plan(const Pool& c, const RopeArgs& r, const AttnArgs& a, i
     int64_t mine = 0;
     if (b0 + tid < c.batch) {
       const int t = tiles_of<TT>(span_of(c, r, a, b0 + tid, nullptr));
-      mine = (int64_t)((t + p.unit - 1) / p.unit * p.unit) * per_row;
+      mine = t ? (int64_t)((t + p.unit - 1) / p.unit * p.unit + p.pair) * per_row : 0;
     }
     int64_t inc = mine;
 #pragma unroll
@@ -216,15 +220,17 @@ struct Cursor {
     hi = s.hi;
     nt = (tiles_of<Cfg<D>::TT>(s) + unit - 1) / unit * unit;
   }
-  // Into the pairs behind this one, when its tiles are used up.
-  __device__ __forceinline__ void carry(const Pool& c, const RopeArgs& r, const AttnArgs& a, int unit, int per_row) {
-    while (tile >= nt) {
+  // Into the pairs behind this one, when its tiles are used up; `place` is the tile's, below `count`.
+  __device__ __forceinline__ void carry(const Pool& c, const RopeArgs& r, const AttnArgs& a, const Plan& p, int per_row,
+                                        int count, int* place) {
+    while (tile >= nt && *place < count) {
       tile -= nt;
+      *place += p.pair;
       if (++hsub == per_row) {
         hsub = 0;
         do {
           ++row;
-          enter(c, r, a, unit);
+          enter(c, r, a, p.unit);
         } while (nt == 0);
       }
     }
@@ -245,7 +251,8 @@ k_decode4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, Att
   __shared__ uint32_t oks[W][C::NST];
   __shared__ int64_t red[W];
   __shared__ float s_q[kMaxHeads][2];           // a head's score factor, and sum(q') 2^-24
-  __shared__ float s_ml[W][kMaxHeads][4];       // a warp's max, sum, sum of p m, scale of its sums
+  __shared__ float s_ml[W][kMaxHeads][4];       // a warp's maximum, sum, sum with the offsets
+  __shared__ float s_head[kMaxHeads][4];        // the same of all warps
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, cc = lane & 3;
   uint8_t* ring = smem + warp * C::NST * C::STAGE;
@@ -272,22 +279,29 @@ k_decode4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, Att
   if (tid == 0) descs[blockIdx.x].parts = 0;
   if (first >= last) return;
 
-  // ---- the warp's copies: its tiles are warp, warp + W, ... of the block's `count`
+  // ---- the warp's copies. Places are counted from the block's first one; a pair's tiles go round the warps.
   const int count = (int)(last - first);
   Cursor<D> ahead;
   ahead.row = plan.row;
   ahead.enter(c, r, a, plan.unit);
-  ahead.hsub = (int)((first - plan.row_at) / ahead.nt);
-  ahead.tile = (int)((first - plan.row_at) % ahead.nt);
+  const int64_t in_row = first - plan.row_at;
+  ahead.hsub = (int)(in_row / (ahead.nt + plan.pair));
+  ahead.tile = (int)(in_row % (ahead.nt + plan.pair)) - plan.pair;
+  int seg = 0;                         // the place of the first tile of the pair at hand in this block
+  if (ahead.tile < 0) {
+    seg = -ahead.tile;
+    ahead.tile = 0;
+  }
+  if (seg >= count) return;
   const int row0 = ahead.row, hsub0 = ahead.hsub, tile0 = ahead.tile;
   const int64_t page_bytes = ((int64_t)c.n_kv << (c.page_shift - 4)) * blk_bytes(D);
   const int in_page = (1 << c.page_shift) - 1;
-  int next = warp, t_next = 0;         // the tile to copy next, and its first position
+  int next = seg + warp, t_next = 0;   // the place of the tile to copy next, and its first position
   const int32_t* table = nullptr;      // its sequence's pages, and its head's bytes in a page
   const uint8_t* head = nullptr;
   auto in_pair = [&]() {
+    ahead.carry(c, r, a, plan, per_row, count, &next);
     if (next >= count) return;
-    ahead.carry(c, r, a, plan.unit, per_row);
     t_next = ahead.first() + 16 * lane;
     table = c.table + ahead.row * c.table_stride;
     head = c.pages + ((int64_t)(ahead.hsub / nsub) << (c.page_shift - 4)) * blk_bytes(D);
@@ -295,11 +309,13 @@ k_decode4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, Att
   ahead.tile += warp;
   in_pair();
   // Lanes below NB: a 16-token block each, its page number asked for a tile before its copy.
-  int pf_page = -1;                    // -1: none
+  bool pf_has = false;                 // there is one
+  int pf_page = -1;                    // -1: nothing of it to copy
   const uint8_t* pf_from = nullptr;
   auto look = [&]() {
     pf_page = -1;
-    if (lane < C::NB && next < count && t_next < ahead.hi && t_next + 16 > ahead.lo) {
+    pf_has = next < count;
+    if (lane < C::NB && pf_has && t_next < ahead.hi && t_next + 16 > ahead.lo) {
       const int page = __ldg(table + (t_next >> c.page_shift));
       pf_page = page < 0 ? 0x7fffffff : page;
       pf_from = head + ((t_next & in_page) >> 4) * blk_bytes(D);
@@ -341,11 +357,10 @@ k_decode4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, Att
   at.enter(c, r, a, plan.unit);
   at.hsub = hsub0;
   at.tile = tile0;
-  int seg = 0;                                   // the segment's first tile of this block
   int stage = 0;
   uint32_t phase = 0;
   bool dead = false;
-  int mine = warp;
+  int mine = seg + warp;
 
   while (seg < count) {
     const int seg_end = min(count, seg + (at.nt - at.tile));
@@ -435,7 +450,7 @@ k_decode4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, Att
         int st = stage + C::NST - 1;
         st = st >= C::NST ? st - C::NST : st;
         __syncwarp();
-        if (!dead && mine + (C::NST - 1) * W < count) {
+        if (!dead && pf_has) {
           issue(st);
           look();
         }
@@ -605,65 +620,88 @@ k_decode4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, Att
     for (int i = 0; i < NHL; ++i) {
       const int hh = PAIR ? cc : 2 * cc + i;
       float top = -INFINITY;
+#pragma unroll
       for (int w = 0; w < W; ++w) top = fmaxf(top, s_ml[w][hh][0]);
       fw[i] = nref[i] == INFINITY ? (lsum[i] == 0.0f ? 0.0f : 1.0f) : ex2(-nref[i] - top);
       fw[i] *= sref / kTop;
     }
+    if (tid < 8 * HS) {                          // a head's maximum, sum and shared part: eight lanes a head, a warp's each
+      const float* ml = s_ml[tid & 7][tid >> 3];
+      float top = ml[0];
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float f = ml[0] == -INFINITY ? (ml[1] == 0.0f ? 0.0f : 1.0f) : ex2(ml[0] - top);
+      float l = f * ml[1], m = f * ml[2];
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) {
+        l += __shfl_xor_sync(0xffffffffu, l, o);
+        m += __shfl_xor_sync(0xffffffffu, m, o);
+      }
+      if ((tid & 7) == 0) {
+        s_head[tid >> 3][0] = top;
+        s_head[tid >> 3][1] = l;
+        s_head[tid >> 3][2] = m;
+      }
+    }
     const bool starts = at.tile == 0, ends = seg + (at.nt - at.tile) <= count;
     float* slot = parts + ((int64_t)2 * blockIdx.x + (starts ? 1 : 0)) * part_floats(D);
+    constexpr int MC = Cfg<D>::MC;               // coordinates of a round
 #pragma unroll
-    for (int jr = 0; jr < NC / 2; ++jr) {
-      // 64 coordinates a round: 64 jr + 4 g + p, and 32 further
+    for (int r0 = 0; r0 < D; r0 += MC) {
+      if (r0 > 0) __syncthreads();
 #pragma unroll
-      for (int half = 0; half < 2; ++half)
+      for (int jr = r0 / 64; jr < (r0 + MC) / 64; ++jr)
+        // 64 coordinates: 64 jr + 4 g + p, and 32 further
 #pragma unroll
-        for (int i = 0; i < NHL; ++i) {
-          const int hh = PAIR ? cc : 2 * cc + i;
-          float4 o4;
-          float* o = (float*)&o4;
+        for (int half = 0; half < 2; ++half)
 #pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            const float* x = acc[4 * jr + p];
-            o[p] = fmaf(x[2 * half + i], (p & 1) ? 0x1p20f : 0x1p24f, -8.0f * tot[i]) * fw[i];
-          }
-          *(float4*)(merge + (warp * HS + hh) * 64 + 32 * half + 4 * g) = o4;
-        }
-      __syncthreads();
-      for (int i = tid; i < HS * 64; i += 32 * W) {
-        const int hh = i >> 6, x = i & 63;
-        if (hh < nh) {
-          float top = -INFINITY, l = 0.0f, o = 0.0f;
+          for (int i = 0; i < NHL; ++i) {
+            const int hh = PAIR ? cc : 2 * cc + i;
+            float4 o4;
+            float* o = (float*)&o4;
 #pragma unroll
-          for (int w = 0; w < W; ++w) top = fmaxf(top, s_ml[w][hh][0]);
-#pragma unroll
-          for (int w = 0; w < W; ++w) {
-            const float* ml = s_ml[w][hh];
-            const float f = ml[0] == -INFINITY ? (ml[1] == 0.0f ? 0.0f : 1.0f) : ex2(ml[0] - top);
-            l = fmaf(f, ml[1], l);
-            o += fmaf(f, ml[2], merge[(w * HS + hh) * 64 + x]);
-          }
-          const int dim = 64 * jr + x;
-          if (starts && ends) {
-            const int64_t at_out = (int64_t)at.row * a.n_q + h0 + hh;
-            out[at_out * D + dim] = from_f<TO>(l == 0.0f ? 0.0f : o / l);
-            if (a.lse && dim == 0) a.lse[at_out] = l == 0.0f ? -INFINITY : (top + log2f(l)) * 0.69314718055994531f;
-          } else {
-            slot[hh * D + dim] = o;
-            if (dim == 0) {
-              slot[kMaxHeads * D + 2 * hh] = top;
-              slot[kMaxHeads * D + 2 * hh + 1] = l;
+            for (int p = 0; p < 4; ++p) {
+              const float* x = acc[4 * jr + p];
+              o[p] = fmaf(x[2 * half + i], (p & 1) ? 0x1p20f : 0x1p24f, -8.0f * tot[i]) * fw[i];
             }
+            *(float4*)(merge + (warp * HS + hh) * MC + 64 * jr - r0 + 32 * half + 4 * g) = o4;
+          }
+      __syncthreads();
+      for (int i = tid; i < nh * (MC / 4); i += 32 * W) {
+        const int hh = i / (MC / 4), x = (i % (MC / 4)) * 4, dim = r0 + x;
+        const float l = s_head[hh][1], m = s_head[hh][2];
+        float4 o = make_float4(m, m, m, m);
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          const float4 y = *(const float4*)(merge + (w * HS + hh) * MC + x);
+          o.x += y.x;
+          o.y += y.y;
+          o.z += y.z;
+          o.w += y.w;
+        }
+        if (starts && ends) {
+          const int64_t at_out = (int64_t)at.row * a.n_q + h0 + hh;
+          const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+          TO y[4] = {from_f<TO>(o.x * inv), from_f<TO>(o.y * inv), from_f<TO>(o.z * inv), from_f<TO>(o.w * inv)};
+          if (sizeof(TO) == 2) *(uint2*)(out + at_out * D + dim) = *(const uint2*)y;
+          else *(uint4*)(out + at_out * D + dim) = *(const uint4*)y;
+          if (a.lse && dim == 0) a.lse[at_out] = l == 0.0f ? -INFINITY : (s_head[hh][0] + log2f(l)) * 0.69314718055994531f;
+        } else {
+          *(float4*)(slot + hh * D + dim) = o;
+          if (dim == 0) {
+            slot[kMaxHeads * D + 2 * hh] = s_head[hh][0];
+            slot[kMaxHeads * D + 2 * hh + 1] = l;
           }
         }
       }
-      __syncthreads();
     }
     if (starts && !ends && tid == 0) {
-      const int64_t end = first + seg + at.nt;   // line position behind the pair
+      const int64_t end = first + seg + at.nt;   // the place behind the pair
       descs[blockIdx.x] = Desc{(int)((end - 1) / plan.quota) - (int)blockIdx.x + 1, at.row, at.hsub, 0};
     }
     // ---- the next pair
-    seg = seg_end;
+    seg = seg_end + plan.pair;
+    mine += plan.pair;
     if (seg < count) {
       at.tile = 0;
       if (++at.hsub == per_row) {
