@@ -254,14 +254,20 @@ template <typename T, typename TO, int D>
 cudaError_t launch_prefill(const Pool& c, const RopeArgs& r, const void* q, void* out, const AttnArgs& a, const pre::Shape& s,
                            const pre::Plan& p, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
-  static_assert(sizeof(pre::PlanSmem) <= 48 * 1024, "within what needs no asking for");
   auto kernel = pre::k_prefill4<TO, D>;
   constexpr int smem = pre::Cfg<D>::TOTAL;
   cudaError_t e = allow_smem(kernel, smem, &done);
   if (e != cudaSuccess) return e;
-  const int64_t rows = a.n_tok * a.n_q, per = pre::kPlanThreads / (D / 8);
-  const unsigned blocks = (unsigned)std::min<int64_t>((rows + per - 1) / per, 4 * s.sms);
-  pre::k_prepare4<T, D><<<1 + blocks, pre::kPlanThreads, sizeof(pre::PlanSmem), st>>>(c, r, (const T*)q, a, s, p);
+  const int64_t items = a.n_tok * ((a.n_q + pre::kQHeads - 1) / pre::kQHeads), per = pre::kPlanThreads / (D / 16);
+  const unsigned blocks = 1 + (unsigned)std::min<int64_t>((items + per - 1) / per, 8 * s.sms);
+  constexpr int plan = sizeof(pre::PlanSmem);
+  static_assert(plan <= 48 * 1024, "within what needs no asking for");
+  if (!r.table)
+    pre::k_prepare4<T, D, 0><<<blocks, pre::kPlanThreads, plan, st>>>(c, r, (const T*)q, a, s, p);
+  else if (!r.inter && r.rot == D)
+    pre::k_prepare4<T, D, 1><<<blocks, pre::kPlanThreads, plan, st>>>(c, r, (const T*)q, a, s, p);
+  else
+    pre::k_prepare4<T, D, 2><<<blocks, pre::kPlanThreads, plan, st>>>(c, r, (const T*)q, a, s, p);
   e = cudaGetLastError();
   if (e == cudaSuccess)
     e = launch_overlapped(kernel, s.cap_units, pre::Cfg<D>::THREADS, smem, st, c, r, (TO*)out, a, s, p);

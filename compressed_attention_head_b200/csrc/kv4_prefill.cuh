@@ -306,13 +306,15 @@ __device__ __forceinline__ void make_units(const Pool& c, const RopeArgs& r, con
   if (tid == 0) p.head->joins = m.joins;
 }
 
-// Block 0 lists the units; the others turn, scale and lay out the queries, D / 8
-// threads a row, as the products take them: fp16, rows of a power of two each, 64
-// coordinates a 16 KB slab of swizzled lines, eight coordinates in the codes' order.
-// Once a call, so that the pieces of a cut unit do not repeat it and a block's
-// prologue is one bulk copy a row tile.
-template <typename T, int D>
-__global__ void __launch_bounds__(kPlanThreads, 3)
+// Block 0 lists the units; the others turn, scale and lay out the queries, D / 16
+// threads a row (eight coordinates of each half, as the append takes them) and four
+// heads of a token at once, under the same angles: fp16, rows of a power of two
+// each, 64 coordinates a 16 KB slab of swizzled lines, eight coordinates in the
+// codes' order. Once a call, so that the pieces of a cut unit do not repeat it and a
+// block's prologue is one bulk copy a row tile. MODE as in k_append4.
+constexpr int kQHeads = 4;
+template <typename T, int D, int MODE>
+__global__ void __launch_bounds__(kPlanThreads, 2)
 k_prepare4(Pool c, RopeArgs r, const T* __restrict__ q, AttnArgs a, Shape s, Plan p) {
   using C = Cfg<D>;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -321,64 +323,110 @@ k_prepare4(Pool c, RopeArgs r, const T* __restrict__ q, AttnArgs a, Shape s, Pla
     make_units(c, r, a, s, p, *(PlanSmem*)plan_smem);
     return;
   }
-  constexpr int TPR = D / 8;
-  const int j = threadIdx.x % TPR;
-  const int64_t rows = a.n_tok * a.n_q, step = (int64_t)(gridDim.x - 1) * (kPlanThreads / TPR);
-  for (int64_t x0 = (int64_t)(blockIdx.x - 1) * (kPlanThreads / TPR); x0 < rows; x0 += step) {
-    const int64_t v = x0 + threadIdx.x / TPR;                    // (token, query head)
-    const int64_t tok = v / a.n_q;
-    const int head = (int)(v - tok * a.n_q);
+  constexpr int TPR = D / 16;
+  const int j = threadIdx.x % TPR, parts = (a.n_q + kQHeads - 1) / kQHeads;
+  const int64_t items = a.n_tok * parts, step = (int64_t)(gridDim.x - 1) * (kPlanThreads / TPR);
+  const int p0 = partner(8 * j, r), p1 = partner(D / 2 + 8 * j, r);
+  for (int64_t x0 = (int64_t)(blockIdx.x - 1) * (kPlanThreads / TPR); x0 < items; x0 += step) {
+    const int64_t v = x0 + threadIdx.x / TPR;
+    const int64_t tok = v < items ? (items < 0x7fffffff ? (int64_t)((uint32_t)v / (uint32_t)parts) : v / parts) : 0;
+    const int h0 = (int)(v - tok * parts) * kQHeads;
     int32_t off = 0;
-    const int b = v < rows ? row_of(a.cu, c.batch, tok, &off) : -1;
-    float x[8];
+    const int b = v < items ? row_of(a.cu, c.batch, tok, &off) : -1;
+    if (__all_sync(0xffffffffu, b < 0)) continue;
+    Vec8<T> own[kQHeads][2], part[MODE == 2 ? kQHeads : 1][2];
+    const int nh = b < 0 ? 0 : min(kQHeads, a.n_q - h0);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = 0.0f;
+    for (int n = 0; n < kQHeads; ++n)
+      if (n < nh) {
+        const T* src = q + tok * a.qs_tok + (int64_t)(h0 + n) * a.qs_head;
+        own[n][0] = load8<T>(src + 8 * j);
+        own[n][1] = load8<T>(src + D / 2 + 8 * j);
+        if (MODE == 2) {
+          part[n][0] = load8<T>(src + p0);
+          part[n][1] = load8<T>(src + p1);
+        }
+      }
     const int64_t pos = b < 0 ? -1 : min((int64_t)__ldg(a.start + b) + off, c.cap() - 1);
-    if (pos >= 0 && !(r.table && pos >= r.n_pos)) {
-      const T* src = q + tok * a.qs_tok + (int64_t)head * a.qs_head;
-      const int pi = partner(8 * j, r);
-      const Vec8<T> own = load8<T>(src + 8 * j), other = load8<T>(src + pi);
-      unpack8<T>(own, x);
-      if (r.table) {
-        float y[8];
-        unpack8<T>(other, y);
-        rotate8<T>(x, y, 8 * j, r, pos);
+    const bool live = pos >= 0 && !(MODE && pos >= r.n_pos);
+    float cs[8], sn[8];
+    if (MODE == 1 && live) {
+      const float4* row = (const float4*)(r.table + pos * D + 8 * j);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        *(float4*)(cs + 4 * e) = __ldg(row + e);
+        *(float4*)(sn + 4 * e) = __ldg(row + D / 8 + e);
       }
     }
-    float top = 0.0f;
+    const int64_t tile = b < 0 ? 0 : row_tile(tok - off, b, off, s.tpm);
+    const int row0 = off % s.tpm * s.gt;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[e]));
+    for (int n = 0; n < kQHeads; ++n) {
+      float x[2][8];
 #pragma unroll
-    for (int o = 1; o < TPR; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    // 2^e with top 2^e in [2^6, 2^7): the sum over a head stays below 2^15
-    int e2 = 0;
-    if (top > 0.0f && top < INFINITY) e2 = max(-100, min(100, 6 - ilogbf(top)));
-    const float up = __int_as_float((127 + e2) << 23);
-    float sum = 0.0f;
-    uint32_t w[4];
+      for (int e = 0; e < 16; ++e) x[e >> 3][e & 7] = 0.0f;
+      if (n < nh && live) {
+        unpack8<T>(own[n][0], x[0]);
+        unpack8<T>(own[n][1], x[1]);
+        if (MODE == 1) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __half2 hv = __floats2half2_rn(x[i] * up, x[i + 4] * up);
-      const float2 f = __half22float2(hv);
-      sum += f.x + f.y;
-      w[i] = *(const uint32_t*)&hv;
-    }
+          for (int e = 0; e < 8; ++e) {
+            const float ya = x[0][e], yb = x[1][e];
+            x[0][e] = __fsub_rn(__fmul_rn(ya, cs[e]), __fmul_rn(yb, sn[e]));
+            x[1][e] = __fadd_rn(__fmul_rn(yb, cs[e]), __fmul_rn(ya, sn[e]));
+          }
 #pragma unroll
-    for (int o = 1; o < TPR; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (b < 0) continue;
-    const int kvh = head / a.group, g = head - kvh * a.group, sub = g / s.gt;
-    const int row = off % s.tpm * s.gt + (g - sub * s.gt);
-    uint8_t* img = p.q + ((int64_t)(kvh * s.nsub + sub) * p.q_tiles + row_tile(tok - off, b, off, s.tpm)) * C::QIMG;
-    *(uint4*)(img + (j >> 3) * 16384 + row * 128 + (((j & 7) ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-    if (j < 2) {
-      // sum(q) in three parts, against the keys' m and 8 s
-      const __half s0 = __float2half_rn(sum);
-      const float d1 = sum - __half2float(s0);
-      const __half s1 = __float2half_rn(d1), s2 = __float2half_rn(d1 - __half2float(s1));
-      const __half2 a0 = __halves2half2(s0, s1), a1 = __halves2half2(s2, s0), a2 = __halves2half2(s1, s2);
-      *(uint4*)(img + C::MAIN + (row >> 3) * 256 + j * 128 + (row & 7) * 16) =
-          j ? make_uint4(0u, 0u, 0u, 0u) : make_uint4(*(const uint32_t*)&a0, *(const uint32_t*)&a1, *(const uint32_t*)&a2, 0u);
-      if (j) *(float*)(img + C::OP + 4 * row) = a.scale * 1.4426950408889634f * __int_as_float((127 - e2) << 23);
+          for (int e = 0; e < 8; e += 2) {
+            round2<T>(&x[0][e], &x[0][e + 1]);
+            round2<T>(&x[1][e], &x[1][e + 1]);
+          }
+        }
+        if (MODE == 2) {
+          float y[8];
+          unpack8<T>(part[n][0], y);
+          rotate8<T>(x[0], y, 8 * j, r, pos);
+          unpack8<T>(part[n][1], y);
+          rotate8<T>(x[1], y, D / 2 + 8 * j, r, pos);
+        }
+      }
+      float top = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(x[e >> 3][e & 7]));
+#pragma unroll
+      for (int o = 1; o < TPR; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      // 2^e with top 2^e in [2^6, 2^7): the sum over a head stays below 2^15
+      int e2 = 0;
+      if (top > 0.0f && top < INFINITY) e2 = max(-100, min(100, 6 + 127 - (int)(__float_as_uint(top) >> 23)));
+      const float up = __int_as_float((127 + e2) << 23);
+      float sum = 0.0f;
+      uint32_t w[2][4];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const __half2 hv = __floats2half2_rn(x[i >> 2][i & 3] * up, x[i >> 2][(i & 3) + 4] * up);
+        const float2 f = __half22float2(hv);
+        sum += f.x + f.y;
+        w[i >> 2][i & 3] = *(const uint32_t*)&hv;
+      }
+#pragma unroll
+      for (int o = 1; o < TPR; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (n >= nh) continue;
+      const int head = h0 + n, kvh = head / a.group, g = head - kvh * a.group, sub = g / s.gt, row = row0 + g - sub * s.gt;
+      uint8_t* img = p.q + ((int64_t)(kvh * s.nsub + sub) * p.q_tiles + tile) * C::QIMG;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int ch = j + e * TPR;
+        *(uint4*)(img + (ch >> 3) * 16384 + row * 128 + (((ch & 7) ^ (row & 7)) << 4)) = make_uint4(w[e][0], w[e][1], w[e][2], w[e][3]);
+      }
+      if (j < 2) {
+        // sum(q) in three parts, against the keys' m and 8 s
+        const __half s0 = __float2half_rn(sum);
+        const float d1 = sum - __half2float(s0);
+        const __half s1 = __float2half_rn(d1), s2 = __float2half_rn(d1 - __half2float(s1));
+        const __half2 a0 = __halves2half2(s0, s1), a1 = __halves2half2(s2, s0), a2 = __halves2half2(s1, s2);
+        *(uint4*)(img + C::MAIN + (row >> 3) * 256 + j * 128 + (row & 7) * 16) =
+            j ? make_uint4(0u, 0u, 0u, 0u) : make_uint4(*(const uint32_t*)&a0, *(const uint32_t*)&a1, *(const uint32_t*)&a2, 0u);
+        if (j) *(float*)(img + C::OP + 4 * row) = a.scale * 1.4426950408889634f * __int_as_float((127 - e2) << 23);
+      }
     }
   }
 }
