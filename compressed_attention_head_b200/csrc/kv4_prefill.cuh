@@ -312,7 +312,7 @@ __device__ __forceinline__ void make_units(const Pool& c, const RopeArgs& r, con
 // each, 64 coordinates a 16 KB slab of swizzled lines, eight coordinates in the
 // codes' order. Once a call, so that the pieces of a cut unit do not repeat it and a
 // block's prologue is one bulk copy a row tile. MODE as in k_append4.
-constexpr int kQHeads = 4;
+constexpr int kQHeads = 2;
 template <typename T, int D, int MODE>
 __global__ void __launch_bounds__(kPlanThreads, 2)
 k_prepare4(Pool c, RopeArgs r, const T* __restrict__ q, AttnArgs a, Shape s, Plan p) {
