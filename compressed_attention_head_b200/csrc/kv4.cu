@@ -170,12 +170,14 @@ cudaError_t launch_overlapped(void (*kernel)(KA...), dim3 grid, dim3 block, size
 int head_passes(int group) { return group <= 4 ? 1 : (group + 7) / 8; }
 
 // Blocks: two an SM, fewer where the bound on the lengths leaves less than a block's eight tiles each.
-int decode_blocks(int batch, int n_kv, int group, int d, int64_t max_ctx) {
+// *whole: no pair has more than a block's tiles and every pair has a block, so none is cut.
+int decode_blocks(int batch, int n_kv, int group, int d, int64_t max_ctx, bool* whole) {
   const int tt = d == 256 ? 16 : 32;
   const int64_t tiles = (max_ctx + tt - 1) / tt + 1;
   const int64_t units = (tiles + dec::W - 1) / dec::W;
   const double all = (double)batch * n_kv * head_passes(group) * (double)units;
   const int most = 2 * sms();
+  if (whole) *whole = units == 1 && all <= most;
   return all < most ? (int)all : most;
 }
 
@@ -190,7 +192,8 @@ cudaError_t launch_decode(const Pool& c, const RopeArgs& r, const void* q, void*
   auto kernel = dec::k_decode4<T, TO, D, PAIR>;
   cudaError_t e = allow_smem(kernel, dec::Smem<D>::TOTAL, &done);
   if (e != cudaSuccess) return e;
-  const int blocks = decode_blocks(c.batch, c.n_kv, a.group, D, std::min<int64_t>(a.max_ctx, (int64_t)c.per_row << c.page_shift));
+  bool whole = false;
+  const int blocks = decode_blocks(c.batch, c.n_kv, a.group, D, std::min<int64_t>(a.max_ctx, (int64_t)c.per_row << c.page_shift), &whole);
   const int nsub = head_passes(a.group);
   float* parts = (float*)ws;
   dec::Desc* descs = (dec::Desc*)(parts + (size_t)2 * blocks * dec::part_floats(D));
@@ -199,7 +202,7 @@ cudaError_t launch_decode(const Pool& c, const RopeArgs& r, const void* q, void*
   else
     kernel<<<blocks, 32 * dec::W, dec::Smem<D>::TOTAL, st>>>(c, r, (const T*)q, (TO*)out, a, nsub, parts, descs);
   if (e == cudaSuccess) e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || whole) return e;
   const int hs = PAIR ? 4 : 8;
   return launch_overlapped(dec::k_join4<TO, D>, dim3(blocks, std::min(hs, a.group)), 256, 0, st, parts, descs, (TO*)out, a, nsub, hs);
 }
@@ -331,7 +334,7 @@ sq_status sq_kv4_read(const sq_kv4_cache* cache, void* k_out, void* v_out, sq_dt
 size_t sq_kv4_attn_workspace(int batch, int n_q_heads, int n_kv_heads, int d, int64_t max_ctx) {
   if (batch < 1 || n_q_heads < 1 || n_kv_heads < 1 || n_q_heads % n_kv_heads != 0 || !head_dim_ok(d) || max_ctx < 1)
     return 0;
-  return decode_ws(decode_blocks(batch, n_kv_heads, n_q_heads / n_kv_heads, d, max_ctx), d);
+  return decode_ws(decode_blocks(batch, n_kv_heads, n_q_heads / n_kv_heads, d, max_ctx, nullptr), d);
 }
 
 sq_status sq_kv4_attn_decode(const sq_kv4_cache* cache, const int32_t* d_seq_lens, int n_q_heads, int64_t max_ctx,
