@@ -243,13 +243,13 @@ pre::Shape prefill_shape(int batch, int n_kv, int group, int d, int64_t n_tok) {
 constexpr size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 size_t prefill_layout(const pre::Shape& s, int n_kv, int d, uint8_t* ws, pre::Plan* p) {
-  const size_t units = 256, joins = units + up256((size_t)s.cap_units * sizeof(pre::Unit));
-  const size_t parts = joins + up256((size_t)s.sms * sizeof(pre::Join));
+  const size_t units = 256, done = units + up256((size_t)s.cap_units * sizeof(pre::Unit));
+  const size_t parts = done + up256((size_t)s.cap_slots * sizeof(int));
   const size_t rows = (size_t)s.cap_slots * pre::part_rows(d == 256 ? 1 : 2);
   const size_t q = parts + up256(rows * (d + 2) * sizeof(float));
   const size_t image = d == 64 ? pre::Cfg<64>::QIMG : d == 128 ? pre::Cfg<128>::QIMG : pre::Cfg<256>::QIMG;
   if (p)
-    *p = pre::Plan{(pre::Head*)ws, (pre::Unit*)(ws + units), (pre::Join*)(ws + joins), (float*)(ws + parts), ws + q, s.q_tiles};
+    *p = pre::Plan{(pre::Head*)ws, (pre::Unit*)(ws + units), (int*)(ws + done), (float*)(ws + parts), ws + q, s.q_tiles};
   return q + (size_t)n_kv * s.nsub * s.q_tiles * image;
 }
 
@@ -274,7 +274,6 @@ cudaError_t launch_prefill(const Pool& c, const RopeArgs& r, const void* q, void
   e = cudaGetLastError();
   if (e == cudaSuccess)
     e = launch_overlapped(kernel, s.cap_units, pre::Cfg<D>::THREADS, smem, st, c, r, (TO*)out, a, s, p);
-  if (e == cudaSuccess) e = launch_overlapped(pre::k_prejoin4<TO, D>, dim3(s.sms, 8), 256, 0, st, p, (TO*)out, a, s);
   return e;
 }
 

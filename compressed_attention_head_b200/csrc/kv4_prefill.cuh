@@ -20,8 +20,8 @@
 //
 // The maximum a row refers to is raised, and its sums scaled, only when a score
 // passes it by 2^4. Pieces: a small kernel first lists the units, longest first, and
-// cuts those that would outlast an even share of all the work; the cut ones leave
-// partial sums that a last kernel joins in order.
+// cuts those that would outlast an even share of all the work; the pieces of a cut one
+// leave partial sums, and the piece that ends last joins them in their order.
 #pragma once
 
 #include "kv4_decode.cuh"
@@ -63,10 +63,10 @@ struct Unit {
   int tok, n;          // first token of the call, tokens
   int off;             // of the first token in its sequence
   int t0, nt;          // key tiles
-  int slot;            // of the partial sums, -1: the whole of it, -2: nothing to do
+  int slot;            // of the first piece's partial sums, -1: the whole of it, -2: nothing to do
+  int part, parts;     // which piece of how many
 };
-struct Join { int unit, slot, parts, pad; };
-struct Head { int units, joins, slots, pad; };
+struct Head { int units, pad[3]; };
 
 struct Shape {
   int gt, nsub, tpm, tpu;      // heads of a pass, passes, tokens of a row tile, of a unit
@@ -77,7 +77,7 @@ struct Shape {
 struct Plan {
   Head* head;
   Unit* units;
-  Join* joins;
+  int* done;                   // pieces of a cut unit that are written, at its first slot
   float* parts;
   uint8_t* q;                  // query operands, [n_kv x nsub][row tiles] of Cfg::QIMG bytes
   int64_t q_tiles;             // row tiles a head
@@ -112,7 +112,7 @@ struct PlanSmem {
   int warp[kPlanThreads / 32];
   int hist[64], parts[33], least[33];
   unsigned long long tiles;
-  int longest, cut, slots, joins;
+  int longest, cut, slots;
 };
 
 // Unit j of sequence row.
@@ -140,7 +140,7 @@ __device__ __forceinline__ void make_units(const Pool& c, const RopeArgs& r, con
   }
   if (tid == 0) {
     m.tiles = 0;
-    m.longest = m.slots = m.joins = 0;
+    m.longest = m.slots = 0;
   }
   int64_t count = 0;                          // units a head
   unsigned long long tiles = 0;
@@ -227,7 +227,6 @@ __device__ __forceinline__ void make_units(const Pool& c, const RopeArgs& r, con
     }
     if (tid == 0) {
       p.head->units = (int)min(count * heads, (int64_t)s.cap_units);
-      p.head->joins = 0;
     }
     return;
   }
@@ -286,24 +285,24 @@ __device__ __forceinline__ void make_units(const Pool& c, const RopeArgs& r, con
     if (parts > 1) {
       slot = atomicAdd(&m.slots, parts);
       // (more than there are places for only when the offsets overlap, which is not allowed)
-      if (slot + parts <= s.cap_slots) p.joins[atomicAdd(&m.joins, 1)] = Join{at, slot, parts, 0};
+      if (slot + parts <= s.cap_slots) p.done[slot] = 0;
       else slot = -2;
     }
     Unit w = unit_of(c, a, s, l.row, l.j);
     int64_t lo, hi;
     unit_keys(c, r, a, w.pos, w.n, &lo, &hi);
     w.hs = x - e * heads;
+    w.slot = slot;
+    w.parts = parts;
     int t = (int)(lo / KT);
     for (int i = 0; i < parts; ++i, ++at) {
       w.t0 = t;
       w.nt = l.len / parts + (i < l.len % parts ? 1 : 0);
-      w.slot = slot < 0 ? slot : slot + i;
+      w.part = i;
       t += w.nt;
       if (at < s.cap_units) p.units[at] = w;
     }
   }
-  __syncthreads();
-  if (tid == 0) p.head->joins = m.joins;
 }
 
 // Block 0 lists the units; the others turn, scale and lay out the queries, D / 16
@@ -630,6 +629,68 @@ template <int N> __device__ __forceinline__ void row_scale(uint32_t t_o, float f
   sm100::tmem_wait_st();
 }
 
+// Joins the pieces of a cut unit in their order, a warp a row, by the block that wrote the last of them.
+template <typename TO, int D>
+__device__ __forceinline__ void join_unit(const Plan& plan, const Unit& u, TO* __restrict__ out, const AttnArgs& a, const Shape& sh,
+                                          int h0, int nh, int rows, int warp, int warps) {
+  constexpr int NS = Cfg<D>::NS;
+  constexpr int R = 4;                        // rows at once: their reads are on the way together
+  const int lane = threadIdx.x & 31;
+  const float2* ml = (const float2*)(plan.parts + (size_t)sh.cap_slots * part_rows(NS) * D);
+  for (int row0 = warp; row0 < rows; row0 += R * warps) {
+    int64_t at[R], first[R];
+    float top[R], l[R], o[R][D / 32];
+#pragma unroll
+    for (int n = 0; n < R; ++n) {
+      const int row = row0 + n * warps, i = row / M, wt = row % M, ti = i * sh.tpm + wt / sh.gt, hh = wt % sh.gt;
+      at[n] = row < rows && wt < sh.tpm * sh.gt && ti < u.n && hh < nh ? (int64_t)(u.tok + ti) * a.n_q + h0 + hh : -1;
+      first[n] = (int64_t)u.slot * part_rows(NS) + (at[n] < 0 ? 0 : row);
+      top[n] = -INFINITY;
+      l[n] = 0.0f;
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) o[n][e] = 0.0f;
+    }
+    // lane p has piece p's maximum and sum
+    for (int p = lane; p < u.parts; p += 32)
+#pragma unroll
+      for (int n = 0; n < R; ++n) top[n] = fmaxf(top[n], __ldcg(ml + first[n] + p * (int64_t)part_rows(NS)).x);
+#pragma unroll
+    for (int n = 0; n < R; ++n)
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1) top[n] = fmaxf(top[n], __shfl_xor_sync(0xffffffffu, top[n], x));
+    for (int p0 = 0; p0 < u.parts; p0 += 32) {
+      float f[R];
+#pragma unroll
+      for (int n = 0; n < R; ++n) {
+        const float2 x = p0 + lane < u.parts ? __ldcg(ml + first[n] + (p0 + lane) * (int64_t)part_rows(NS)) : make_float2(-INFINITY, 0.0f);
+        f[n] = x.x == -INFINITY ? (x.y == 0.0f ? 0.0f : 1.0f) : dec::ex2(x.x - top[n]);
+        float y = f[n] * x.y;
+#pragma unroll
+        for (int z = 16; z > 0; z >>= 1) y += __shfl_xor_sync(0xffffffffu, y, z);
+        l[n] += y;
+      }
+      const int here = min(32, u.parts - p0);
+#pragma unroll 2
+      for (int p = 0; p < here; ++p)
+#pragma unroll
+        for (int n = 0; n < R; ++n) {
+          const float fp = __shfl_sync(0xffffffffu, f[n], p);
+          const float* src = plan.parts + (first[n] + (p0 + p) * (int64_t)part_rows(NS)) * D + lane;
+#pragma unroll
+          for (int e = 0; e < D / 32; ++e) o[n][e] = fmaf(fp, __ldcg(src + 32 * e), o[n][e]);
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < R; ++n) {
+      if (at[n] < 0) continue;
+      const float inv = l[n] == 0.0f ? 0.0f : 1.0f / l[n];
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) out[at[n] * D + 32 * e + lane] = from_f<TO>(l[n] == 0.0f ? 0.0f : o[n][e] * inv);
+      if (a.lse && lane == 0) a.lse[at[n]] = l[n] == 0.0f ? -INFINITY : (top[n] + (log2f(l[n]) - kUp)) * 0.69314718055994531f;
+    }
+  }
+}
+
 template <typename TO, int D>
 __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
 k_prefill4(Pool c, RopeArgs r, TO* __restrict__ out, AttnArgs a, Shape sh, Plan plan) {
@@ -639,6 +700,7 @@ k_prefill4(Pool c, RopeArgs r, TO* __restrict__ out, AttnArgs a, Shape sh, Plan 
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t b_q, b_fin, b_s[2], b_p[2], b_o[NS], b_kf[NKV], b_ke[NKV], b_vf[NKV], b_ve[NKV], b_i[kInfo];
   __shared__ uint32_t s_tmem;
+  __shared__ int s_last;
   __shared__ Info s_info[kInfo];
   __shared__ uint2 s_red[2][8];
   __shared__ float s_max[NS][2][2][M];           // a half row's largest score, tiles taking turns
@@ -757,7 +819,7 @@ k_prefill4(Pool c, RopeArgs r, TO* __restrict__ out, AttnArgs a, Shape sh, Plan 
         const bool whole = u.slot < 0;
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         const int64_t at = (int64_t)(u.tok + ti) * a.n_q + h0 + hh;
-        const int64_t pr = whole ? 0 : (int64_t)u.slot * part_rows(NS) + i * M + wt;
+        const int64_t pr = whole ? 0 : (int64_t)(u.slot + u.part) * part_rows(NS) + i * M + wt;
         float* po = plan.parts + pr * D + half * (D / 2);
         TO* wo = out + at * D + half * (D / 2);
 #pragma unroll 1
@@ -799,6 +861,17 @@ k_prefill4(Pool c, RopeArgs r, TO* __restrict__ out, AttnArgs a, Shape sh, Plan 
             ml[0] = mref;
             ml[1] = l;
           }
+        }
+      }
+      // ---- the piece that is written last joins them all
+      if (u.slot >= 0) {
+        __threadfence();
+        sm100::named_bar(4, 2 * ns * kGroup);
+        if (tid == 0) s_last = atomicAdd(plan.done + u.slot, 1) == u.parts - 1;
+        sm100::named_bar(4, 2 * ns * kGroup);
+        if (s_last) {
+          __threadfence();
+          join_unit<TO, D>(plan, u, out, a, sh, h0, nh, ns * M, warp, 8 * ns);
         }
       }
     }
@@ -1043,42 +1116,6 @@ k_prefill4(Pool c, RopeArgs r, TO* __restrict__ out, AttnArgs a, Shape sh, Plan 
     sm100::tc_fence_after();
     sm100::tmem_relinquish();
     sm100::tmem_dealloc(tmem, 512);
-  }
-}
-
-// Joins the pieces of a cut unit, a warp a row.
-template <typename TO, int D>
-__global__ void __launch_bounds__(256)
-k_prejoin4(Plan plan, TO* __restrict__ out, AttnArgs a, Shape sh) {
-  constexpr int NS = Cfg<D>::NS;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if ((int)blockIdx.x >= plan.head->joins) return;
-  const Join j = plan.joins[blockIdx.x];
-  const Unit u = plan.units[j.unit];
-  const int kvh = u.hs / sh.nsub, h0 = kvh * a.group + (u.hs % sh.nsub) * sh.gt;
-  const int nh = min(sh.gt, (kvh + 1) * a.group - h0);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const float* ml = plan.parts + (size_t)sh.cap_slots * part_rows(NS) * D;
-  for (int row = blockIdx.y * 8 + warp; row < NS * M; row += gridDim.y * 8) {
-    const int i = row / M, wt = row % M, ti = i * sh.tpm + wt / sh.gt, hh = wt % sh.gt;
-    if (wt >= sh.tpm * sh.gt || ti >= u.n || hh >= nh) continue;
-    float top = -INFINITY;
-    for (int p = 0; p < j.parts; ++p) top = fmaxf(top, ml[((int64_t)(j.slot + p) * part_rows(NS) + row) * 2]);
-    const float base = top == -INFINITY ? 0.0f : top;
-    float l = 0.0f, o[D / 32];
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e) o[e] = 0.0f;
-    for (int p = 0; p < j.parts; ++p) {
-      const int64_t pr = (int64_t)(j.slot + p) * part_rows(NS) + row;
-      const float f = ml[pr * 2] == -INFINITY ? (ml[pr * 2 + 1] == 0.0f ? 0.0f : 1.0f) : dec::ex2(ml[pr * 2] - base);
-      l = fmaf(f, ml[pr * 2 + 1], l);
-#pragma unroll
-      for (int e = 0; e < D / 32; ++e) o[e] = fmaf(f, plan.parts[pr * D + 32 * e + lane], o[e]);
-    }
-    const int64_t at = (int64_t)(u.tok + ti) * a.n_q + h0 + hh;
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e) out[at * D + 32 * e + lane] = from_f<TO>(l == 0.0f ? 0.0f : o[e] / l);
-    if (a.lse && lane == 0) a.lse[at] = l == 0.0f ? -INFINITY : (top + (log2f(l) - kUp)) * 0.69314718055994531f;
   }
 }
 
