@@ -182,14 +182,14 @@ int decode_blocks(int batch, int n_kv, int group, int d, int64_t max_ctx, bool* 
 }
 
 size_t decode_ws(int blocks, int d) {
-  return (size_t)2 * blocks * dec::part_floats(d) * 4 + (size_t)blocks * sizeof(dec::Desc);
+  return (size_t)2 * blocks * dec::part_floats(d) * 4 + (size_t)blocks * (sizeof(dec::Desc) + sizeof(int));
 }
 
-template <typename T, typename TO, int D, bool PAIR>
+template <typename T, typename TO, int D, bool PAIR, bool JOIN>
 cudaError_t launch_decode(const Pool& c, const RopeArgs& r, const void* q, void* out, const AttnArgs& a, void* ws,
-                          bool overlap, cudaStream_t st) {
+                          bool step, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
-  auto kernel = dec::k_decode4<T, TO, D, PAIR>;
+  auto kernel = dec::k_decode4<T, TO, D, PAIR, JOIN>;
   cudaError_t e = allow_smem(kernel, dec::Smem<D>::TOTAL, &done);
   if (e != cudaSuccess) return e;
   bool whole = false;
@@ -197,30 +197,34 @@ cudaError_t launch_decode(const Pool& c, const RopeArgs& r, const void* q, void*
   const int nsub = head_passes(a.group);
   float* parts = (float*)ws;
   dec::Desc* descs = (dec::Desc*)(parts + (size_t)2 * blocks * dec::part_floats(D));
-  if (overlap)
+  if (step)                                     // behind its append
     e = launch_overlapped(kernel, blocks, 32 * dec::W, dec::Smem<D>::TOTAL, st, c, r, (const T*)q, (TO*)out, a, nsub, parts, descs);
   else
     kernel<<<blocks, 32 * dec::W, dec::Smem<D>::TOTAL, st>>>(c, r, (const T*)q, (TO*)out, a, nsub, parts, descs);
   if (e == cudaSuccess) e = cudaGetLastError();
-  if (e != cudaSuccess || whole) return e;
+  if (e != cudaSuccess || whole || JOIN) return e;
   const int hs = PAIR ? 4 : 8;
   return launch_overlapped(dec::k_join4<TO, D>, dim3(blocks, std::min(hs, a.group)), 256, 0, st, parts, descs, (TO*)out, a, nsub, hs);
 }
 
 sq_status run_decode(const Pool& c, const RopeArgs& r, const void* q, sq_dtype dtype, void* out, sq_dtype out_dtype,
-                     const AttnArgs& a, void* ws, bool overlap, cudaStream_t st) {
+                     const AttnArgs& a, void* ws, bool step, cudaStream_t st) {
   cudaError_t e = cudaSuccess;
-#define SQ_CALL2(T, TO, DD) \
-  e = a.group <= 4 ? launch_decode<T, TO, DD, true>(c, r, q, out, a, ws, overlap, st) \
-                   : launch_decode<T, TO, DD, false>(c, r, q, out, a, ws, overlap, st)
-#define SQ_CALL(T, DD)                                   \
-  if (out_dtype == SQ_F32) SQ_CALL2(T, float, DD);       \
-  else if (out_dtype == SQ_F16) SQ_CALL2(T, __half, DD); \
-  else SQ_CALL2(T, __nv_bfloat16, DD)
+#define SQ_CALL3(T, TO, DD, PAIR)                                                         \
+  e = a.done ? launch_decode<T, TO, DD, PAIR, true>(c, r, q, out, a, ws, step, st)        \
+             : launch_decode<T, TO, DD, PAIR, false>(c, r, q, out, a, ws, step, st)
+#define SQ_CALL2(T, TO, DD)                   \
+  if (a.group <= 4) SQ_CALL3(T, TO, DD, true); \
+  else SQ_CALL3(T, TO, DD, false)
+#define SQ_CALL(T, DD)                                       \
+  if (out_dtype == SQ_F32) { SQ_CALL2(T, float, DD); }       \
+  else if (out_dtype == SQ_F16) { SQ_CALL2(T, __half, DD); } \
+  else { SQ_CALL2(T, __nv_bfloat16, DD); }
   if (dtype == SQ_F16) { SQ_KV4_D(__half, SQ_CALL) }
   else { SQ_KV4_D(__nv_bfloat16, SQ_CALL) }
 #undef SQ_CALL
 #undef SQ_CALL2
+#undef SQ_CALL3
   return cuda_ok(e);
 }
 
@@ -312,7 +316,7 @@ sq_status sq_kv4_append(const sq_kv4_cache* cache, const void* k, const void* v,
                         int64_t k_stride_head, int64_t v_stride_tok, int64_t v_stride_head, int64_t n_tok,
                         const int32_t* d_cu, const int32_t* d_start, const sq_rope* rope, uint32_t* d_flags,
                         sq_stream stream) {
-  const StreamArgs a{d_cu, d_start, n_tok, k_stride_tok, k_stride_head, v_stride_tok, v_stride_head, d_flags};
+  const StreamArgs a{d_cu, d_start, n_tok, k_stride_tok, k_stride_head, v_stride_tok, v_stride_head, d_flags, nullptr, 0};
   sq_status s = stream_args_ok(cache, k, v, dtype, a);
   if (s != SQ_OK) return s;
   if (!rope_ok(rope, cache->d)) return SQ_ERR_ARG;
@@ -323,7 +327,7 @@ sq_status sq_kv4_append(const sq_kv4_cache* cache, const void* k, const void* v,
 sq_status sq_kv4_read(const sq_kv4_cache* cache, void* k_out, void* v_out, sq_dtype dtype, int64_t k_stride_tok,
                       int64_t k_stride_head, int64_t v_stride_tok, int64_t v_stride_head, int64_t n_tok,
                       const int32_t* d_cu, const int32_t* d_start, uint32_t* d_flags, sq_stream stream) {
-  const StreamArgs a{d_cu, d_start, n_tok, k_stride_tok, k_stride_head, v_stride_tok, v_stride_head, d_flags};
+  const StreamArgs a{d_cu, d_start, n_tok, k_stride_tok, k_stride_head, v_stride_tok, v_stride_head, d_flags, nullptr, 0};
   sq_status s = stream_args_ok(cache, k_out, v_out, dtype, a);
   if (s != SQ_OK) return s;
   if (n_tok == 0) return SQ_OK;
@@ -347,7 +351,7 @@ sq_status sq_kv4_attn_decode(const sq_kv4_cache* cache, const int32_t* d_seq_len
   if (ws_bytes < sq_kv4_attn_workspace(cache->batch, n_q_heads, cache->n_kv_heads, cache->d, max_ctx))
     return SQ_ERR_WORKSPACE;
   const AttnArgs a{nullptr, d_seq_lens, -1, cache->batch, max_ctx, q_stride_row, q_stride_head, n_q_heads,
-                   n_q_heads / cache->n_kv_heads, window, scale_of(scale, cache->d), lse_out, d_flags};
+                   n_q_heads / cache->n_kv_heads, window, scale_of(scale, cache->d), lse_out, d_flags, nullptr};
   return run_decode(pool_of(cache), rope_of(rope), q, dtype, out, out_dtype, a, ws, false, (cudaStream_t)stream);
 }
 
@@ -360,7 +364,7 @@ sq_status sq_kv4_decode_step(const sq_kv4_cache* cache, const void* k, const voi
   sq_status s = attn_args_ok(cache, n_q_heads, q, dtype, q_stride_row, q_stride_head, rope, window, out, out_dtype,
                              lse_out, ws, d_flags);
   if (s != SQ_OK) return s;
-  const StreamArgs ap{nullptr, d_pos, cache->batch, k_stride_tok, k_stride_head, v_stride_tok, v_stride_head, d_flags};
+  StreamArgs ap{nullptr, d_pos, cache->batch, k_stride_tok, k_stride_head, v_stride_tok, v_stride_head, d_flags, nullptr, 0};
   s = stream_args_ok(cache, k, v, dtype, ap);
   if (s != SQ_OK) return s;
   if (max_ctx < 1) return SQ_ERR_ARG;
@@ -368,10 +372,21 @@ sq_status sq_kv4_decode_step(const sq_kv4_cache* cache, const void* k, const voi
     return SQ_ERR_WORKSPACE;
   const Pool c = pool_of(cache);
   const RopeArgs r = rope_of(rope);
+  const int group = n_q_heads / cache->n_kv_heads;
+  const int blocks = decode_blocks(c.batch, c.n_kv, group, c.d, max_ctx, nullptr);
+  // Where the step leaves most of the GPU idle, a launch is what it can save (one sequence, 2 KV heads, 501 tokens:
+  // 25.3 us a call and its read back with a kernel that joins, 23.6 without); a full one ends sooner with the
+  // kernel (four sequences, 8 KV heads, 8192 tokens: 30.7 against 32.1 us).
+  int* done = nullptr;
+  if (blocks < 2 * sms()) {
+    done = (int*)((uint8_t*)ws + decode_ws(blocks, c.d)) - blocks;
+    ap.zero = done;
+    ap.n_zero = blocks;
+  }
   s = run_append(c, r, k, v, dtype, ap, (cudaStream_t)stream);
   if (s != SQ_OK) return s;
   const AttnArgs a{nullptr, d_pos, 0, cache->batch, max_ctx, q_stride_row, q_stride_head, n_q_heads,
-                   n_q_heads / cache->n_kv_heads, window, scale_of(scale, cache->d), lse_out, d_flags};
+                   group, window, scale_of(scale, cache->d), lse_out, d_flags, done};
   return run_decode(c, r, q, dtype, out, out_dtype, a, ws, true, (cudaStream_t)stream);
 }
 
@@ -397,7 +412,7 @@ sq_status sq_kv4_attn_prefill(const sq_kv4_cache* cache, const int32_t* d_cu, co
   if (ws_bytes < sq_kv4_attn_prefill_workspace(cache->batch, n_q_heads, cache->n_kv_heads, cache->d, n_tok))
     return SQ_ERR_WORKSPACE;
   const AttnArgs a{d_cu, d_start, 0, n_tok, 0x7fffffff, q_stride_tok, q_stride_head, n_q_heads,
-                   n_q_heads / cache->n_kv_heads, window, scale_of(scale, cache->d), lse_out, d_flags};
+                   n_q_heads / cache->n_kv_heads, window, scale_of(scale, cache->d), lse_out, d_flags, nullptr};
   const pre::Shape sh = prefill_shape(cache->batch, cache->n_kv_heads, a.group, cache->d, n_tok);
   if (!sh.cap_units) return SQ_ERR_ARG;
   return run_prefill(pool_of(cache), rope_of(rope), q, dtype, out, out_dtype, a, sh, (uint8_t*)ws, (cudaStream_t)stream);

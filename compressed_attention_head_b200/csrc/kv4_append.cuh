@@ -23,6 +23,8 @@ struct StreamArgs {
   int64_t n_tok;
   int64_t ks_tok, ks_head, vs_tok, vs_head;   // strides of the caller's keys and values, in elements
   uint32_t* flags;
+  int* zero;                                  // counters that the kernel behind an append wants at 0, or NULL
+  int n_zero;
 };
 
 // Where a token's vectors go: the byte of head 0's block in its page (or -1) and its slot and position.
@@ -102,6 +104,8 @@ k_append4(Pool c, RopeArgs r, const T* __restrict__ k, const T* __restrict__ v, 
     }
   }
   for (int i = threadIdx.x; i < sh.toks; i += kStreamThreads) places[i] = place_of(c, a, MODE ? r.n_pos : -1, t0 + i);
+  if (a.zero && blockIdx.x == 0 && blockIdx.y == 0)
+    for (int i = threadIdx.x; i < a.n_zero; i += kStreamThreads) a.zero[i] = 0;
   __syncthreads();
 #pragma unroll
   for (int n = 0; n < kVecs; ++n) {

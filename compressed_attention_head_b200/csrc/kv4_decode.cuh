@@ -24,8 +24,10 @@
 // blocks (two an SM) share evenly, whatever the lengths; inside a block tile i goes
 // to warp i mod 8. A warp brings its tiles by bulk copies into a ring of its own and
 // meets the other warps only where a pair ends, to add up. Pairs cut by a block's
-// end leave partial sums that a second, overlapped launch joins, in order: results
-// do not depend on timing.
+// end leave partial sums, which are joined in order, so that results do not depend on
+// timing: by a second, overlapped launch, or, in a decode step of few blocks, where a
+// launch costs more than it does, by the block that writes the last of them (the append
+// before has cleared the counters for that).
 #pragma once
 
 #include "kv4_append.cuh"
@@ -45,6 +47,7 @@ struct AttnArgs {
   float scale;
   float* lse;
   uint32_t* flags;
+  int* done;              // decode: pieces of a pair that are written, at the block it begins in, all 0
 };
 
 namespace dec {
@@ -239,7 +242,42 @@ struct Cursor {
   __device__ __forceinline__ int first() const { return (lo / Cfg<D>::TT + tile) * Cfg<D>::TT; }
 };
 
-template <typename T, typename TO, int D, bool PAIR>
+// The sum of pieces p0, p0 + step, ... of the pair that block `begin` began, for its hh-th head; a warp's lanes have
+// the coordinates 32 i + lane.
+template <int D>
+__device__ __forceinline__ void join_parts(const float* parts, int begin, int hh, int p0, int step, int n, float* top_out,
+                                           float* l_out, float* o) {
+  const int lane = threadIdx.x & 31;
+  auto slot = [&](int p) { return parts + ((int64_t)2 * (begin + p) + (p == 0 ? 1 : 0)) * part_floats(D); };
+  auto ml = [&](int p) { return p < n ? __ldcg((const float2*)(slot(p) + kMaxHeads * D + 2 * hh)) : make_float2(-INFINITY, 0.0f); };
+  float top = -INFINITY, l = 0.0f;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) o[i] = 0.0f;
+  // a lane a piece: its maximum and sum
+  for (int p = p0 + step * lane; p < n; p += 32 * step) top = fmaxf(top, ml(p).x);
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+  for (int q = p0; q < n; q += 32 * step) {
+    const float2 m = ml(q + step * lane);
+    const float f = m.x == -INFINITY ? (m.y == 0.0f ? 0.0f : 1.0f) : ex2(m.x - top);
+    l += f * m.y;
+    const int here = min(32, (n - q + step - 1) / step);
+#pragma unroll 4
+    for (int p = 0; p < here; ++p) {
+      const float fp = __shfl_sync(0xffffffffu, f, p);
+      const float* src = slot(q + step * p) + hh * D + lane;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) o[i] = fmaf(fp, __ldcg(src + 32 * i), o[i]);
+    }
+  }
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+  *top_out = top;
+  *l_out = l;
+}
+
+// JOIN: the block that writes a pair's last piece joins them (AttnArgs::done); else a kernel behind this one does.
+template <typename T, typename TO, int D, bool PAIR, bool JOIN>
 __global__ void __launch_bounds__(32 * W, 2)
 k_decode4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, AttnArgs a, int nsub, float* parts,
           Desc* descs) {
@@ -253,6 +291,7 @@ k_decode4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, Att
   __shared__ float s_q[kMaxHeads][2];           // a head's score factor, and sum(q') 2^-24
   __shared__ float s_ml[W][kMaxHeads][4];       // a warp's maximum, sum, sum with the offsets
   __shared__ float s_head[kMaxHeads][4];        // the same of all warps
+  __shared__ int s_last;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, cc = lane & 3;
   uint8_t* ring = smem + warp * C::NST * C::STAGE;
@@ -276,7 +315,7 @@ k_decode4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, Att
   }
   const int64_t first = (int64_t)blockIdx.x * plan.quota;
   const int64_t last = min(first + plan.quota, plan.line);
-  if (tid == 0) descs[blockIdx.x].parts = 0;
+  if (!JOIN && tid == 0) descs[blockIdx.x].parts = 0;
   if (first >= last) return;
 
   // ---- the warp's copies. Places are counted from the block's first one; a pair's tiles go round the warps.
@@ -695,9 +734,28 @@ k_decode4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, Att
         }
       }
     }
-    if (starts && !ends && tid == 0) {
-      const int64_t end = first + seg + at.nt;   // the place behind the pair
-      descs[blockIdx.x] = Desc{(int)((end - 1) / plan.quota) - (int)blockIdx.x + 1, at.row, at.hsub, 0};
+    if (!starts || !ends) {
+      const int64_t begin = first + seg - at.tile;     // the pair's first place
+      const int b0 = (int)(begin / plan.quota), pieces = (int)((begin + at.nt - 1) / plan.quota) - b0 + 1;
+      if constexpr (!JOIN) {
+        if (starts && tid == 0) descs[blockIdx.x] = Desc{pieces, at.row, at.hsub, 0};
+      } else {
+        // the block that writes the last piece joins them all, a warp a head
+        __threadfence();
+        __syncthreads();
+        if (tid == 0) s_last = atomicAdd(a.done + b0, 1) == pieces - 1;
+        __syncthreads();
+        if (s_last && warp < nh) {
+          __threadfence();
+          float top, l, o[D / 32];
+          join_parts<D>(parts, b0, warp, 0, 1, pieces, &top, &l, o);
+          const int64_t at_out = (int64_t)at.row * a.n_q + h0 + warp;
+          const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) out[at_out * D + 32 * i + lane] = from_f<TO>(l == 0.0f ? 0.0f : o[i] * inv);
+          if (a.lse && lane == 0) a.lse[at_out] = l == 0.0f ? -INFINITY : (top + log2f(l)) * 0.69314718055994531f;
+        }
+      }
     }
     // ---- the next pair
     seg = seg_end + plan.pair;
@@ -715,8 +773,8 @@ k_decode4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, Att
   }
 }
 
-// Joins the partial sums of a pair that several blocks of k_decode4 share: block
-// (i, h) those of the pair that block i began, for its h-th head; a warp a partial.
+// Joins the partial sums of pairs that several blocks of k_decode4 share: block (i, h)
+// those of the pair that block i began, for its h-th head.
 template <typename TO, int D>
 __global__ void __launch_bounds__(256)
 k_join4(const float* __restrict__ parts, const Desc* __restrict__ descs, TO* __restrict__ out, AttnArgs a, int nsub,
@@ -729,23 +787,8 @@ k_join4(const float* __restrict__ parts, const Desc* __restrict__ descs, TO* __r
   __shared__ float s_m[8], s_l[8];
   __shared__ float s_o[8][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float top = -INFINITY, l = 0.0f, o[D / 32];
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) o[i] = 0.0f;
-  for (int p = warp; p < ds.parts; p += 8) {
-    const float* s = parts + ((int64_t)2 * (blockIdx.x + p) + (p == 0 ? 1 : 0)) * part_floats(D);
-    const float m = s[kMaxHeads * D + 2 * hh], pl = s[kMaxHeads * D + 2 * hh + 1];
-    float x[D / 32];
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) x[i] = s[hh * D + 32 * i + lane];
-    const float nt = fmaxf(top, m), base = nt == -INFINITY ? 0.0f : nt;
-    const float fa = top == -INFINITY ? (l == 0.0f ? 0.0f : 1.0f) : ex2(top - base);
-    const float fb = m == -INFINITY ? (pl == 0.0f ? 0.0f : 1.0f) : ex2(m - base);
-    l = l * fa + pl * fb;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) o[i] = o[i] * fa + x[i] * fb;
-    top = nt;
-  }
+  float top, l, o[D / 32];
+  join_parts<D>(parts, blockIdx.x, hh, warp, 8, ds.parts, &top, &l, o);
   if (lane == 0) {
     s_m[warp] = top;
     s_l[warp] = l;
