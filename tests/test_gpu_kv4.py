@@ -526,3 +526,210 @@ def test_graphs_that_share_a_workspace_and_other_streams():
     ref = torch.empty(3, n_q, d, device="cuda")
     sq.sq_kv4_attn_decode(cache, lens[0], q[0], 0.0, ref, 1200, ws)
     assert torch.equal(outs[0], ref)
+
+
+# ------------------------------------------------------------------ where the kernels' own divisions could go wrong
+@pytest.mark.parametrize("d,n_kv,page,rot,inter", [(256, 20, 16, 256, False), (128, 3, 32, 48, False), (64, 35, 16, 64, True)])
+def test_append_of_many_and_of_odd_head_counts(d, n_kv, page, rot, inter):
+    """More vectors a token than a block holds, and numbers of them that do not divide it."""
+    g = torch.Generator().manual_seed(d + n_kv)
+    k, v = (torch.randn(19, n_kv, d, generator=g).to(BF16) for _ in range(2))
+    start, cu = [3, 11], [0, 12, 19]
+    table, total = make_table([1, 2], 1)
+    pool = torch.zeros(total, n_kv, page // 16, 16 * d + 128, dtype=torch.uint8)
+    want = pool.numpy().copy()
+    rope = kv4.rope_table(32, rot)
+    append_oracle(want, table, page, k, v, start, cu, rope, inter, BF16)
+    cache = sq.PagedKV4(pool.cuda(), torch.from_numpy(table).cuda(), n_kv, d, page)
+    st, cud = torch.tensor(start, dtype=torch.int32).cuda(), torch.tensor(cu, dtype=torch.int32).cuda()
+    sq.sq_kv4_append(cache, k.cuda(), v.cuda(), st, cud, rope=sq.Rope(torch.from_numpy(rope).cuda(), inter))
+    assert np.array_equal(cache.pages.cpu().numpy(), want)
+    ko, vo = torch.empty_like(k, device="cuda"), torch.empty_like(v, device="cuda")
+    sq.sq_kv4_read(cache, st, cud, ko, vo)
+    for b, i, h in ((0, 0, 0), (0, 11, n_kv - 1), (1, 6, n_kv // 2)):
+        p = start[b] + i
+        for side, got in ((0, ko), (1, vo)):
+            c, sb, mb = kv4.load(want, table[b, p // page], h, p % page, side)
+            x = torch.from_numpy(kv4.values(c, np.uint32(sb), np.uint32(mb))).float().to(BF16)
+            assert torch.equal(got[cu[b] + i, h].cpu(), x)
+
+
+def test_codes_beside_ties_are_those_of_the_exact_quotient():
+    """Coordinates half a step from two codes, and one float beside that, over many steps."""
+    d, page = 256, 16
+    g = torch.Generator().manual_seed(0)
+    rows = []
+    for e in range(-40, 40, 5):
+        s = float(torch.tensor((1 + torch.rand(1, generator=g).item()) * 2.0 ** e).to(BF16))
+        x = np.arange(d, dtype=np.float64) % 15 * s + s / 2
+        x = x.astype(np.float32)
+        x[1::3] = np.nextafter(x[1::3], np.float32(np.inf))
+        x[2::3] = np.nextafter(x[2::3], np.float32(-np.inf))
+        x[0], x[1] = 0.0, np.float32(15 * s)
+        rows.append(torch.from_numpy(x))
+    x = torch.stack(rows)[:, None]
+    table, total = make_table([1], 0)
+    cache = sq.alloc_kv4(total, 1, d, page, torch.from_numpy(table).cuda())
+    want = cache.pages.cpu().numpy().copy()
+    append_oracle(want, table, page, x, -x, [0], [0, len(rows)], None, False, F32)
+    sq.sq_kv4_append(cache, x.cuda(), (-x).cuda(), torch.zeros(1, dtype=torch.int32).cuda(),
+                     torch.tensor([0, len(rows)], dtype=torch.int32).cuda())
+    assert np.array_equal(cache.pages.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("d,group", [(64, 130), (128, 150), (256, 33)])
+def test_groups_larger_than_a_row_tile(d, group):
+    decode_case(d, group, 1, F16, F32, 16, [70, 0, 5], rot=32, seed=3)
+    prefill_case(d, group, 1, F16, F32, 16, [40, 0], [6, 3], rot=32, seed=3)
+
+
+@pytest.mark.parametrize("d", [64, 256])
+def test_steps_and_offsets_of_unlike_sizes(d):
+    """Pairs of one pool over forty powers of two: what is exact for each must not depend on its neighbours."""
+    Q_TYPE[0] = F16
+    page, n = 16, 200
+    table, total = make_table([-(-n // page)], 5)
+    pool = random_pool(total, 1, page, d, 5)
+    pairs = pool[..., 16 * d:].contiguous().view(BF16).view(total, 1, 1, 2, 16, 2)
+    e = torch.randint(-20, 21, (total, 1, 1, 2, 16, 1), generator=torch.Generator().manual_seed(2)).cuda()
+    e[:, :, :, 0] -= 18                                   # keys' scores stay moderate
+    pairs = (pairs.float() * torch.exp2(e.float())).to(BF16)
+    pool[..., 16 * d:] = pairs.contiguous().view(torch.uint8).view(total, 1, 1, 128)
+    cache = sq.PagedKV4(pool, torch.from_numpy(table).cuda(), 1, d, page)
+    q = torch.randn(9, 3, d, generator=torch.Generator().manual_seed(1)).to(F16).cuda()
+    out, lse = torch.empty(9, 3, d, device="cuda"), torch.empty(9, 3, device="cuda")
+    ws = torch.empty(sq.sq_kv4_attn_prefill_workspace(1, 3, 1, d, 9), dtype=torch.uint8, device="cuda")
+    sq.sq_kv4_attn_prefill(cache, torch.tensor([n - 9], dtype=torch.int32).cuda(), torch.tensor([0, 9], dtype=torch.int32).cuda(),
+                           q, 0.0, out, ws, lse=lse)
+    check_attention(out, lse, q, [(0, n - 9 + i) for i in range(9)], pool, table, page, 3, 1, d, F32)
+    out, lse = torch.empty(1, 3, d, device="cuda"), torch.empty(1, 3, device="cuda")
+    ws = torch.empty(sq.sq_kv4_attn_workspace(1, 3, 1, d, n), dtype=torch.uint8, device="cuda")
+    sq.sq_kv4_attn_decode(cache, torch.tensor([n], dtype=torch.int32).cuda(), q[:1], 0.0, out, n, ws, lse=lse)
+    check_attention(out, lse, q[:1], [(0, n - 1)], pool, table, page, 3, 1, d, F32)
+
+
+def test_prefill_of_thousands_of_sequences():
+    """More units than are sorted: single tokens, two of every three sequences idle; the same as decode attention."""
+    d, page, n_kv, batch = 64, 16, 1, 6500
+    rng = np.random.default_rng(0)
+    lens = rng.integers(1, 40, batch)
+    new = np.where(np.arange(batch) % 3 == 0, 1, 0)
+    table, total = make_table([3] * 64, 0)
+    table = table[rng.integers(0, 64, batch)]                        # shared pages
+    cache = sq.PagedKV4(random_pool(total, n_kv, page, d, 0), torch.from_numpy(table).cuda(), n_kv, d, page)
+    cu = torch.from_numpy(np.concatenate([[0], np.cumsum(new)]).astype(np.int32)).cuda()
+    start = torch.from_numpy(lens.astype(np.int32)).cuda()
+    n_tok = int(new.sum())
+    q = torch.randn(n_tok, 2, d, generator=torch.Generator(device="cuda").manual_seed(0), device="cuda").to(F16)
+    out, lse = torch.empty(n_tok, 2, d, device="cuda"), torch.empty(n_tok, 2, device="cuda")
+    ws = torch.full((sq.sq_kv4_attn_prefill_workspace(batch, 2, n_kv, d, n_tok),), 255, dtype=torch.uint8, device="cuda")
+    sq.sq_kv4_attn_prefill(cache, start, cu, q, 0.0, out, ws, lse=lse)
+    rows = torch.from_numpy(np.flatnonzero(new)).cuda()
+    one = sq.PagedKV4(cache.pages, cache.table[rows].contiguous(), n_kv, d, page)
+    want, wl = torch.empty(n_tok, 2, d, device="cuda"), torch.empty(n_tok, 2, device="cuda")
+    ws = torch.empty(sq.sq_kv4_attn_workspace(n_tok, 2, n_kv, d, 41), dtype=torch.uint8, device="cuda")
+    sq.sq_kv4_attn_decode(one, (start[rows] + 1).contiguous(), q, 0.0, want, 41, ws, lse=wl)
+    # both weights rounded (2 x 2^-11) against steps below 0.97 and codes at most 8 from their middle
+    assert (out - want).abs().max() <= 2 * 2.0 ** -11 * 0.97 * 8 and (lse - wl).abs().max() <= 2.0 ** -16
+
+
+@pytest.mark.parametrize("d,group,start,new,window", [
+    (64, 2, [500], [150], 0), (128, 6, [6000, 4100], [30, 7], 0), (256, 2, [3000, 36, 700], [300, 60, 90], 1024),
+    (128, 4, [0], [700], 0), (64, 1, [9000], [1], 0), (256, 8, [5000], [3], 0)])
+def test_chunks_repeat_bit_for_bit(d, group, start, new, window):
+    """Cut units, single row tiles and pairs of them, whatever the blocks' order: twelve runs are equal, and equal in a graph
+    that shares their workspace with another."""
+    page, n_kv = 16, 2
+    table, total = make_table([-(-(s + n) // page) for s, n in zip(start, new)], 1)
+    cache = sq.PagedKV4(random_pool(total, n_kv, page, d, 1), torch.from_numpy(table).cuda(), n_kv, d, page)
+    st = torch.tensor(start, dtype=torch.int32).cuda()
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32).cuda()
+    n_tok, n_q = sum(new), group * n_kv
+    q = [torch.randn(n_tok, n_q, d, generator=torch.Generator(device="cuda").manual_seed(i), device="cuda").to(F16) for i in (0, 1)]
+    ws = torch.full((sq.sq_kv4_attn_prefill_workspace(len(new), n_q, n_kv, d, n_tok),), 255, dtype=torch.uint8, device="cuda")
+    first = []
+    for i in (0, 1):
+        for r in range(12):
+            out, lse = torch.full((n_tok, n_q, d), 9.0, device="cuda"), torch.full((n_tok, n_q), 9.0, device="cuda")
+            sq.sq_kv4_attn_prefill(cache, st, cu, q[i], 0.0, out, ws, window=window, lse=lse)
+            if r == 0:
+                first.append((out, lse))
+            assert torch.equal(out, first[i][0]) and torch.equal(lse, first[i][1])
+    graphs = []
+    outs = [torch.zeros_like(first[0][0]) for _ in (0, 1)]
+    for i in (0, 1):
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            sq.sq_kv4_attn_prefill(cache, st, cu, q[i], 0.0, outs[i], ws, window=window)
+        graphs.append(gr)
+    for _ in range(3):
+        for gr in graphs:
+            gr.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, f[0]) for o, f in zip(outs, first))
+
+
+@pytest.mark.parametrize("batch,pos", [(1, [501]), (2, [1700, 60]), (5, [9000, 1, 4000, 77, 2500])])
+def test_steps_in_a_graph_continue_a_sequence(batch, pos):
+    """A captured step replayed over positions that advance on the device: the outputs of separate calls, of few blocks (which
+    join by themselves) and of many."""
+    d, page, n_kv, n_q, steps = 128, 16, 2, 12, 4
+    table, total = make_table([-(-(p + steps) // page) for p in pos], 4)
+    pool = random_pool(total, n_kv, page, d, 4)
+    rope = sq.Rope(sq.rope_table(max(pos) + steps, d))
+    g = torch.Generator(device="cuda").manual_seed(3)
+    qkv = torch.randn(steps, batch, n_q + 2 * n_kv, d, generator=g, device="cuda").to(BF16)
+    cut = lambda t: (t[:, n_q:n_q + n_kv], t[:, n_q + n_kv:], t[:, :n_q])  # noqa: E731
+    a = sq.PagedKV4(pool.clone(), torch.from_numpy(table).cuda(), n_kv, d, page)
+    b = sq.PagedKV4(pool.clone(), torch.from_numpy(table).cuda(), n_kv, d, page)
+    ctx = max(pos) + steps
+    ws = torch.full((sq.sq_kv4_attn_workspace(batch, n_q, n_kv, d, ctx),), 255, dtype=torch.uint8, device="cuda")
+    at = torch.tensor(pos, dtype=torch.int32).cuda()
+    x, out = qkv[0].clone(), torch.zeros(batch, n_q, d, device="cuda")
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        sq.sq_kv4_decode_step(a, *cut(x), at, 0.0, out, ctx, ws, rope=rope)
+        at.add_(1)
+    at.copy_(torch.tensor(pos, dtype=torch.int32))
+    a.pages.copy_(pool)
+    for i in range(steps):
+        x.copy_(qkv[i])
+        gr.replay()
+        want = torch.zeros_like(out)
+        now = torch.tensor(pos, dtype=torch.int32).cuda() + i
+        k, v, q = cut(qkv[i])
+        sq.sq_kv4_append(b, k, v, now, rope=rope)
+        ws2 = torch.empty_like(ws)
+        sq.sq_kv4_attn_decode(b, now + 1, q, 0.0, want, ctx, ws2, rope=rope)
+        assert torch.equal(a.pages, b.pages)
+        # the join of a step and of a separate call sum in the same order, but scale with other roundings: a few of 2^-24
+        assert (out - want).abs().max() <= 16 * 2.0 ** -24 * 16
+
+
+def test_calls_of_two_streams_at_once():
+    """Two chunks and two decodes on two streams, each with a workspace of its own, leave each other's outputs alone."""
+    d, page, n_kv, n_q = 128, 16, 2, 8
+    table, total = make_table([200, 200], 6)
+    cache = sq.PagedKV4(random_pool(total, n_kv, page, d, 6), torch.from_numpy(table).cuda(), n_kv, d, page)
+    st, cu = torch.tensor([3000, 2500], dtype=torch.int32).cuda(), torch.tensor([0, 100, 180], dtype=torch.int32).cuda()
+    lens = torch.tensor([3200, 3100], dtype=torch.int32).cuda()
+    q = torch.randn(180, n_q, d, generator=torch.Generator(device="cuda").manual_seed(0), device="cuda").to(F16)
+
+    def run(out, one, wp, wd, stream=None):
+        sq.sq_kv4_attn_prefill(cache, st, cu, q, 0.0, out, wp, stream=stream)
+        sq.sq_kv4_attn_decode(cache, lens, q[:2], 0.0, one, 3200, wd, stream=stream)
+
+    new = lambda: (torch.empty(180, n_q, d, device="cuda"), torch.empty(2, n_q, d, device="cuda"),  # noqa: E731
+                   torch.empty(sq.sq_kv4_attn_prefill_workspace(2, n_q, n_kv, d, 180), dtype=torch.uint8, device="cuda"),
+                   torch.empty(sq.sq_kv4_attn_workspace(2, n_q, n_kv, d, 3200), dtype=torch.uint8, device="cuda"))
+    ref = new()
+    run(*ref)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    sets = [new(), new()]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for s, x in zip(streams, sets):
+            run(*x, stream=s)
+    torch.cuda.synchronize()
+    for x in sets:
+        assert torch.equal(x[0], ref[0]) and torch.equal(x[1], ref[1])
