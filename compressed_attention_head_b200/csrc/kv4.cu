@@ -64,7 +64,7 @@ sq_status stream_args_ok(const sq_kv4_cache* c, const void* k, const void* v, sq
 
 // Blocks of a stream: tokens, parts of a token.
 template <int D> dim3 stream_grid(const Pool& c, int64_t n_tok, Share* sh) {
-  *sh = Share::of(2 * c.n_kv, vecs_of_block<D>());
+  *sh = Share::of(2 * c.n_kv, vecs_of_block<D>(), vecs_of_block<D>() / kVecs);
   return dim3((unsigned)((n_tok + sh->toks - 1) / sh->toks), sh->parts);
 }
 

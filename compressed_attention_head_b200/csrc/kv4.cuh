@@ -181,6 +181,17 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return d;
 }
 
+__device__ __forceinline__ float min_nan(float a, float b, float c) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // The pair of a vector from its smallest and largest coordinate (NaN where one of
 // them is); NaN for a vector that holds a value that is not finite (or whose range
 // is not): the codes are then 0 and every coordinate reads as NaN.
@@ -189,7 +200,12 @@ __device__ __forceinline__ void make_pair(float mn, float mx, float* s, float* m
   uint32_t mb = bf16_down(mn);
   const float r = __fsub_rn(mx, __uint_as_float(mb << 16));
   uint32_t sb = 0;
-  if (r > 0.0f) sb = bf16_up(fmaxf(__fdiv_rn(r, 15.0f), FLT_MIN));
+  if (r > 0.0f) {
+    // r / 15 as a division rounds it: Markstein's correction of the product with the rounded 1 / 15, which is exact
+    // for this divisor (all 2^23 significands at thirteen exponents compared on the host; below FLT_MIN it is not used)
+    const float y = 1.0f / 15.0f, q = __fmul_rn(r, y);
+    sb = bf16_up(fmaxf(__fmaf_rn(__fmaf_rn(-15.0f, q, r), y, q), FLT_MIN));
+  }
   if (!finite || !(r < INFINITY)) {
     mb = 0x7fc0u;
     sb = 0;
@@ -200,10 +216,15 @@ __device__ __forceinline__ void make_pair(float mn, float mx, float* s, float* m
 }
 
 // Eight codes: (x - m) / s rounded to nearest, ties to even, exactly. The product
-// with inv = 1 / s, rounded to an integer by an addition to 1.5 2^23, is within 2^-19
+// with inv, 1 / s within 2^-23, rounded to an integer by an addition to 1.5 2^23, is within 2^-19
 // of the quotient: its nearest integer is the quotient's or, beside a tie, the next.
 // The remainder against s / 2, which one fused multiply-add gives, tells the two
 // apart; few vectors have such a coordinate. s > 0.
+__device__ __forceinline__ float reciprocal(float s) {
+  float y;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(s));
+  return y;
+}
 constexpr float kRound = 12582912.0f;
 __device__ __forceinline__ uint32_t codes8(const float* x, float m, float s, float inv) {
   const f2 m2 = f2_of(-m, -m), i2 = f2_of(inv, inv), r2 = f2_of(kRound, kRound), n2 = f2_of(-kRound, -kRound), s2 = f2_of(-s, -s);

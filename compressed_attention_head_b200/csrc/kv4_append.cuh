@@ -27,10 +27,10 @@ struct StreamArgs {
   int n_zero;
 };
 
-// Where a token's vectors go: the byte of head 0's block in its page (or -1) and its slot and position.
+// Where a token's vectors go: head 0's block (an offset into the pool, or -1), its row in that, its position.
 struct Place {
   int64_t at;
-  int slot;
+  int row;
   int32_t pos;
 };
 
@@ -53,8 +53,8 @@ __device__ __forceinline__ Place place_of(const Pool& c, const StreamArgs& a, in
     raise(a.flags, SQ_FLAG_PAGE);
     return p;
   }
-  p.slot = (int)(pos & ((1 << c.page_shift) - 1));
-  p.at = (int64_t)page;
+  p.row = (int)(pos & 15);
+  p.at = c.head(page, 0) - c.pages + ((int)(pos & ((1 << c.page_shift) - 1)) >> 4) * blk_bytes(c.d);
   p.pos = (int32_t)pos;
   return p;
 }
@@ -63,11 +63,14 @@ __device__ __forceinline__ Place place_of(const Pool& c, const StreamArgs& a, in
 // (keys' heads, then values'), or a part of one token's.
 struct Share {
   int toks, heads, parts;
-  __host__ __device__ static Share of(int per_tok, int vecs) {
+  int next_tok, next_head;     // a thread's next vector is this many tokens and heads on (less `heads` where that is too many)
+  __host__ __device__ static Share of(int per_tok, int vecs, int step) {
     Share s;
     s.parts = (per_tok + vecs - 1) / vecs;
     s.toks = s.parts > 1 ? 1 : vecs / per_tok;
     s.heads = s.parts > 1 ? vecs : per_tok;
+    s.next_tok = step / s.heads;
+    s.next_head = step % s.heads;
     return s;
   }
 };
@@ -85,17 +88,25 @@ k_append4(Pool c, RopeArgs r, const T* __restrict__ k, const T* __restrict__ v, 
   Vec8<T> own[kVecs][2], part[MODE == 2 ? kVecs : 1][2];
   int tok[kVecs], head[kVecs];
   const int p0 = partner(8 * j, r), p1 = partner(D / 2 + 8 * j, r);
+  const T *k0 = k + t0 * a.ks_tok, *v0 = v + t0 * a.vs_tok;
+  const int toks = (int)min((int64_t)sh.toks, a.n_tok - t0), first = (int)blockIdx.y * sh.heads;
+  int x_tok = g / sh.heads, x_head = g - x_tok * sh.heads;
 #pragma unroll
   for (int n = 0; n < kVecs; ++n) {
-    const int x = g + n * VPB;
-    tok[n] = x / sh.heads;
-    head[n] = x - tok[n] * sh.heads + (int)blockIdx.y * sh.heads;
-    if (tok[n] >= sh.toks || t0 + tok[n] >= a.n_tok || head[n] >= 2 * c.n_kv) {
+    tok[n] = x_tok;
+    head[n] = x_head + first;
+    x_tok += sh.next_tok;
+    x_head += sh.next_head;
+    if (x_head >= sh.heads) {
+      x_head -= sh.heads;
+      ++x_tok;
+    }
+    if (tok[n] >= toks || head[n] >= 2 * c.n_kv) {
       tok[n] = -1;
       continue;
     }
     const bool key = head[n] < c.n_kv;
-    const T* src = key ? k + (t0 + tok[n]) * a.ks_tok + head[n] * a.ks_head : v + (t0 + tok[n]) * a.vs_tok + (head[n] - c.n_kv) * a.vs_head;
+    const T* src = key ? k0 + tok[n] * a.ks_tok + head[n] * a.ks_head : v0 + tok[n] * a.vs_tok + (head[n] - c.n_kv) * a.vs_head;
     own[n][0] = load8<T>(src + 8 * j);
     own[n][1] = load8<T>(src + D / 2 + 8 * j);
     if (MODE == 2 && key) {
@@ -107,6 +118,7 @@ k_append4(Pool c, RopeArgs r, const T* __restrict__ k, const T* __restrict__ v, 
   if (a.zero && blockIdx.x == 0 && blockIdx.y == 0)
     for (int i = threadIdx.x; i < a.n_zero; i += kStreamThreads) a.zero[i] = 0;
   __syncthreads();
+  const int head_bytes = blk_bytes(D) << (c.page_shift - 4);
 #pragma unroll
   for (int n = 0; n < kVecs; ++n) {
     // a vector's threads take these branches together; the shuffles name only them
@@ -145,10 +157,12 @@ k_append4(Pool c, RopeArgs r, const T* __restrict__ k, const T* __restrict__ v, 
     }
     float mn = x[0][0], mx = x[0][0];
 #pragma unroll
-    for (int e = 1; e < 16; ++e) {
-      mn = min_nan(mn, x[e >> 3][e & 7]);
-      mx = max_nan(mx, x[e >> 3][e & 7]);
+    for (int e = 1; e < 15; e += 2) {
+      mn = min_nan(mn, x[e >> 3][e & 7], x[(e + 1) >> 3][(e + 1) & 7]);
+      mx = max_nan(mx, x[e >> 3][e & 7], x[(e + 1) >> 3][(e + 1) & 7]);
     }
+    mn = min_nan(mn, x[1][7]);
+    mx = max_nan(mx, x[1][7]);
     const unsigned lanes = ((1u << TPV) - 1u) << ((threadIdx.x & 31) / TPV * TPV);
 #pragma unroll
     for (int o = 1; o < TPV; o <<= 1) {
@@ -159,12 +173,12 @@ k_append4(Pool c, RopeArgs r, const T* __restrict__ k, const T* __restrict__ v, 
     uint32_t word, w[2] = {0u, 0u};
     make_pair(mn, mx, &s, &m, &word);
     if (s > 0.0f) {
-      const float inv = __fdiv_rn(1.0f, s);
+      const float inv = reciprocal(s);
       w[0] = codes8(x[0], m, s, inv);
       w[1] = codes8(x[1], m, s, inv);
     }
-    const int side = key ? 0 : 1, t = p.slot & 15;
-    uint8_t* blk = c.head((int)p.at, head[n] - side * c.n_kv) + (p.slot >> 4) * blk_bytes(D);
+    const int side = key ? 0 : 1, t = p.row;
+    uint8_t* blk = c.pages + p.at + (int64_t)(head[n] - side * c.n_kv) * head_bytes;
     uint8_t* row = blk + side * v_codes(D) + t * (D / 2) + ((j & 3) << 2);
 #pragma unroll
     for (int e = 0; e < 2; ++e) *(uint32_t*)(row + ((((j >> 2) + e * (D / 64)) ^ swz(t, D)) << 4)) = w[e];
@@ -200,13 +214,21 @@ k_read4(Pool c, T* __restrict__ ko, T* __restrict__ vo, StreamArgs a, Share sh) 
   for (int i = threadIdx.x; i < sh.toks; i += kStreamThreads) places[i] = place_of(c, a, -1, t0 + i);
   __syncthreads();
   const int j = threadIdx.x % TPV, g = threadIdx.x / TPV;
+  T *k0 = ko + t0 * a.ks_tok, *v0 = vo + t0 * a.vs_tok;
   uint32_t w[kVecs][2], pair[kVecs];
   int tok[kVecs], head[kVecs];
+  const int head_bytes = blk_bytes(D) << (c.page_shift - 4), first = (int)blockIdx.y * sh.heads;
+  int x_tok = g / sh.heads, x_head = g - x_tok * sh.heads;
 #pragma unroll
   for (int n = 0; n < kVecs; ++n) {
-    const int x = g + n * VPB;
-    tok[n] = x / sh.heads;
-    head[n] = x - tok[n] * sh.heads + (int)blockIdx.y * sh.heads;
+    tok[n] = x_tok;
+    head[n] = x_head + first;
+    x_tok += sh.next_tok;
+    x_head += sh.next_head;
+    if (x_head >= sh.heads) {
+      x_head -= sh.heads;
+      ++x_tok;
+    }
     if (tok[n] >= sh.toks || head[n] >= 2 * c.n_kv) tok[n] = -1;
     if (tok[n] < 0) continue;
     const Place p = places[tok[n]];
@@ -214,8 +236,8 @@ k_read4(Pool c, T* __restrict__ ko, T* __restrict__ vo, StreamArgs a, Share sh) 
       tok[n] = -1;
       continue;
     }
-    const int side = head[n] < c.n_kv ? 0 : 1, t = p.slot & 15;
-    const uint8_t* blk = c.head((int)p.at, head[n] - side * c.n_kv) + (p.slot >> 4) * blk_bytes(D);
+    const int side = head[n] < c.n_kv ? 0 : 1, t = p.row;
+    const uint8_t* blk = c.pages + p.at + (int64_t)(head[n] - side * c.n_kv) * head_bytes;
     const uint8_t* row = blk + side * v_codes(D) + t * (D / 2) + ((j & 3) << 2);
 #pragma unroll
     for (int e = 0; e < 2; ++e) w[n][e] = *(const uint32_t*)(row + ((((j >> 2) + e * (D / 64)) ^ swz(t, D)) << 4));
@@ -225,8 +247,8 @@ k_read4(Pool c, T* __restrict__ ko, T* __restrict__ vo, StreamArgs a, Share sh) 
   for (int n = 0; n < kVecs; ++n) {
     if (tok[n] < 0) continue;
     const float s = __uint_as_float(pair[n] << 16), m = __uint_as_float(pair[n] & 0xffff0000u);
-    T* out = (head[n] < c.n_kv ? ko + head[n] * a.ks_head + (t0 + tok[n]) * a.ks_tok
-                               : vo + (head[n] - c.n_kv) * a.vs_head + (t0 + tok[n]) * a.vs_tok) + 8 * j;
+    T* out = (head[n] < c.n_kv ? k0 + head[n] * a.ks_head + tok[n] * a.ks_tok
+                               : v0 + (head[n] - c.n_kv) * a.vs_head + tok[n] * a.vs_tok) + 8 * j;
     values8<T>(w[n][0], s, m, out);
     values8<T>(w[n][1], s, m, out + D / 2);
   }
