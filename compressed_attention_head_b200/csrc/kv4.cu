@@ -11,6 +11,9 @@
 #include "kv4_prefill.cuh"
 
 namespace sq {
+
+sq_status cuda_ok(cudaError_t e);      // SQ_OK, or SQ_ERR_CUDA with the error's name kept for sq_last_error (api.cu)
+
 namespace kv4 {
 namespace {
 

@@ -469,6 +469,14 @@ __device__ __forceinline__ void st16(uint32_t addr, const uint32_t* r) {
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]) : "memory");
 }
+// True in one lane of a converged warp. A warp that issues its products under this,
+// and stays converged otherwise, keeps the operands' descriptors in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // Registers a thread of this warp group (multiples of 8), which together stay within what the block started with.
 template <int N> __device__ __forceinline__ void set_regs_up() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -1041,7 +1049,7 @@ k_prefill4(Pool c, RopeArgs r, TO* __restrict__ out, AttnArgs a, Shape sh, Plan 
         const uint32_t d = tmem + 128 * sl;
         const uint64_t qd = desc_of(qa, 16, 1024, 2), kd = desc_of(ka, 16, 1024, 2);
         const uint64_t qe = desc_of(qa + C::MAIN, 128, 256, 0), ke = desc_of(ka + C::MAIN, 128, 256, 0);
-        if (sm100::elect_one()) {
+        if (elect_one()) {
 #pragma unroll
           for (int s = 0; s < D / 16; ++s) {
             const uint64_t off = (uint64_t)((s >> 2) * 1024 + (s & 3) * 2);       // in units of 16 bytes
@@ -1057,7 +1065,7 @@ k_prefill4(Pool c, RopeArgs r, TO* __restrict__ out, AttnArgs a, Shape sh, Plan 
         const uint32_t va = base + C::V + (k % NKV) * C::MAIN;
         const uint32_t p = tmem + 128 * (ns == 2 ? i : (k & 1)), d = tmem + 256 + i * D;
         const uint64_t vd = desc_of(va, 16384, 1024, 2);
-        if (sm100::elect_one()) {
+        if (elect_one()) {
 #pragma unroll
           for (int s = 0; s < KT / 16; ++s) sm100::mma_f16_ts(d, p + 64 * (s >> 2) + 8 * (s & 3), vd + 128 * s, id_o, (s > 0 || k > 0) ? 1u : 0u);
           sm100::mma_commit(&b_o[i]);
@@ -1065,7 +1073,7 @@ k_prefill4(Pool c, RopeArgs r, TO* __restrict__ out, AttnArgs a, Shape sh, Plan 
         }
         __syncwarp();
       };
-      if (sm100::elect_one()) {
+      if (elect_one()) {
         asm volatile("fence.proxy.async.global;" ::: "memory");
         sm100::mbar_expect_tx(&b_q, ns * C::OP);
         for (int i = 0; i < ns; ++i)
@@ -1104,7 +1112,7 @@ k_prefill4(Pool c, RopeArgs r, TO* __restrict__ out, AttnArgs a, Shape sh, Plan 
         }
       }
       // nothing of this block is in flight when it gives its tensor memory back
-      if (sm100::elect_one()) sm100::mma_commit(&b_fin);
+      if (elect_one()) sm100::mma_commit(&b_fin);
       __syncwarp();
       sm100::mbar_wait(&b_fin, 0, a.flags);
     }

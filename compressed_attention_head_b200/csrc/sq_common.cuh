@@ -35,9 +35,6 @@ __host__ __device__ inline size_t rec_word0(size_t row, int64_t cap, int W, int6
   return row * (size_t)cap * (size_t)W + (size_t)(t >> 5) * (size_t)W * 32u + (size_t)(t & 31);
 }
 
-// SQ_OK, or SQ_ERR_CUDA with the error's name kept for sq_last_error (api.cu).
-sq_status cuda_ok(cudaError_t e);
-
 // Device arrays of one packed cache, as the kernels take them.
 struct CacheArgs {
   uint32_t* codes;
