@@ -243,7 +243,7 @@ pre::Shape prefill_shape(int batch, int n_kv, int group, int d, int64_t n_tok) {
   s.cap_slots = 2 * s.sms;
   const int64_t units = (int64_t)n_kv * s.nsub * ((n_tok + s.tpu - 1) / s.tpu + batch) + s.cap_slots;
   s.cap_units = units > 0x7fffffff ? 0 : (int)units;
-  s.q_tiles = n_tok / s.tpm + batch + 1;      // one more: offsets that begin below 0 round up
+  s.q_tiles = n_tok / s.tpm + batch;
   return s;
 }
 

@@ -253,7 +253,7 @@ __device__ __forceinline__ uint32_t codes8(const float* x, float m, float s, flo
   return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x5410);
 }
 
-// Sequence of token i among cu[0 .. batch] (cu NULL: one token a sequence), or -1.
+// Sequence of token i among cu[0 .. batch] (cu NULL: one token a sequence), or -1 (also where its offset is below 0).
 __device__ __forceinline__ int row_of(const int32_t* cu, int batch, int64_t i, int32_t* off) {
   if (!cu) {
     *off = 0;
@@ -265,7 +265,7 @@ __device__ __forceinline__ int row_of(const int32_t* cu, int batch, int64_t i, i
     if ((int64_t)__ldg(cu + mid) <= i) lo = mid; else hi = mid;
   }
   const int32_t a = __ldg(cu + lo), b = __ldg(cu + lo + 1);
-  if (i < a || i >= b) return -1;
+  if (a < 0 || i < a || i >= b) return -1;
   *off = (int32_t)(i - a);
   return lo;
 }

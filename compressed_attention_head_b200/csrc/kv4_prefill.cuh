@@ -84,7 +84,7 @@ struct Plan {
 };
 
 // Row tile of the token at `off` in a sequence whose first token is `tok`: every
-// sequence starts a tile of its own, no two share one, and none is past n_tok / tpm + batch.
+// sequence starts a tile of its own, no two share one, and all are below n_tok / tpm + batch.
 __device__ __forceinline__ int64_t row_tile(int64_t tok, int row, int off, int tpm) { return tok / tpm + row + off / tpm; }
 
 __host__ __device__ inline size_t part_rows(int ns) { return (size_t)ns * M; }
@@ -117,12 +117,11 @@ struct PlanSmem {
 
 // Unit j of sequence row.
 __device__ __forceinline__ Unit unit_of(const Pool& c, const AttnArgs& a, const Shape& s, int row, int j) {
-  const int32_t first = __ldg(a.cu + row);
-  const int64_t t_lo = max(0, first), t_hi = min((int64_t)__ldg(a.cu + row + 1), a.n_tok);
+  const int64_t t_lo = __ldg(a.cu + row), t_hi = min((int64_t)__ldg(a.cu + row + 1), a.n_tok);
   Unit w;
   w.tok = (int)(t_lo + (int64_t)j * s.tpu);
   w.n = (int)min((int64_t)s.tpu, t_hi - w.tok);
-  w.off = w.tok - first;
+  w.off = w.tok - (int)t_lo;
   w.pos = (int64_t)__ldg(a.start + row) + w.off;
   w.row = row;
   return w;
@@ -149,11 +148,10 @@ __device__ __forceinline__ void make_units(const Pool& c, const RopeArgs& r, con
     const int b = b0 + tid;
     int n = 0;
     if (b < c.batch) {
-      const int32_t first = __ldg(a.cu + b);
-      const int64_t t_lo = max(0, first), t_hi = min((int64_t)__ldg(a.cu + b + 1), a.n_tok);
-      if (t_hi > t_lo) {
+      const int64_t t_lo = __ldg(a.cu + b), t_hi = min((int64_t)__ldg(a.cu + b + 1), a.n_tok);
+      if (t_lo >= 0 && t_hi > t_lo) {
         n = (int)((uint32_t)(t_hi - t_lo + s.tpu - 1) / (uint32_t)s.tpu);
-        const int64_t start = (int64_t)__ldg(a.start + b) + (t_lo - first), last = start + (t_hi - t_lo) - 1;
+        const int64_t start = __ldg(a.start + b), last = start + (t_hi - t_lo) - 1;
         uint32_t bits = 0;
         if (last >= c.cap() || start < -1) bits |= SQ_FLAG_SEQLEN;
         if (r.table && min(last, c.cap() - 1) >= r.n_pos) bits |= SQ_FLAG_ROPE;

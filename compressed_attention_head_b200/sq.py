@@ -496,8 +496,12 @@ def _kv4_out(out, lse, q):
     return out.data_ptr(), lse.data_ptr()
 
 
-def _kv4_at(t):
-    return None if t is None else t.data_ptr()
+def _kv4_at(flags):
+    if flags is None:
+        return None
+    if flags.element_size() != 4 or flags.numel() < 1:
+        raise ValueError("flags: a 32-bit word is wanted")
+    return flags.data_ptr()
 
 
 def _kv4_bytes(ws):

@@ -569,8 +569,8 @@ size_t sq_kv4_page_bytes(int n_kv_heads, int d, int page_tokens);
  *               k_stride_tok + h * k_stride_head + i (views into a fused
  *               projection need no copy). 16-byte aligned, strides multiples of 8.
  *  n_tok        token rows of k and v.
- *  d_cu         device int32[batch + 1], rising: tokens d_cu[b] .. d_cu[b + 1] - 1
- *               belong to sequence b; rows from d_cu[batch] on (a padded batch) are
+ *  d_cu         device int32[batch + 1], rising from 0 or more: tokens d_cu[b] ..
+ *               d_cu[b + 1] - 1 belong to sequence b; rows from d_cu[batch] on (a padded batch) are
  *               left alone. NULL: token b belongs to sequence b.
  *  d_start      device int32[batch]: position of each sequence's first new token.
  *  rope         NULL: no rotation. The values are never rotated.
@@ -632,7 +632,11 @@ sq_status sq_kv4_decode_step(const sq_kv4_cache* cache, const void* k, const voi
                              sq_dtype out_dtype, float* lse_out, void* ws, size_t ws_bytes, uint32_t* d_flags,
                              sq_stream stream);
 
-/* Workspace bytes of sq_kv4_attn_prefill (0 if unsupported). */
+/*
+ * Workspace bytes of sq_kv4_attn_prefill (0 if unsupported): the queries laid out once
+ * more (rows of 128 a KV head and sequence) and the partial sums of cut pieces (about
+ * 40 MB).
+ */
 size_t sq_kv4_attn_prefill_workspace(int batch, int n_q_heads, int n_kv_heads, int d, int64_t n_tok);
 
 /*

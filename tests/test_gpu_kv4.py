@@ -733,3 +733,24 @@ def test_calls_of_two_streams_at_once():
     torch.cuda.synchronize()
     for x in sets:
         assert torch.equal(x[0], ref[0]) and torch.equal(x[1], ref[1])
+
+
+def test_offsets_below_zero_name_no_tokens():
+    """A sequence whose first offset is below 0, however far: its rows stay as they were, the others' are right."""
+    Q_TYPE[0] = F16
+    d, page, n_kv, n_q = 128, 16, 1, 4
+    cache, table = small_cache(d=d, n_kv=n_kv, page=page, batch=3)
+    q = torch.randn(8, n_q, d, generator=torch.Generator().manual_seed(0)).to(F16).cuda()
+    ws = torch.full((sq.sq_kv4_attn_prefill_workspace(3, n_q, n_kv, d, 8),), 255, dtype=torch.uint8, device="cuda")
+    start = torch.tensor([5, 9, 20], dtype=torch.int32, device="cuda")
+    for first in (-1, -200, -2 ** 31):
+        cu = torch.tensor([first, 2, 5, 8], dtype=torch.int32, device="cuda")
+        out = torch.full((8, n_q, d), 3.0, device="cuda")
+        sq.sq_kv4_attn_prefill(cache, start, cu, q, 0.0, out, ws)
+        pos = [(-1, 0)] * 2 + [(1, 9 + i) for i in range(3)] + [(2, 20 + i) for i in range(3)]
+        check_attention(out, None, q, pos, cache.pages, table, page, n_q, n_kv, d, F32)
+        assert (out[:2] == 3).all()
+        before = cache.pages.clone()
+        k = torch.randn(2, n_kv, d, device="cuda", dtype=F16)
+        sq.sq_kv4_append(cache, k, k, start, torch.tensor([first, 2, 2, 2], dtype=torch.int32, device="cuda"))
+        assert torch.equal(cache.pages, before)
