@@ -28,6 +28,12 @@
 // timing: by a second, overlapped launch, or, in a decode step of few blocks, where a
 // launch costs more than it does, by the block that writes the last of them (the append
 // before has cleared the counters for that).
+//
+// Measured (one B200): 64 x 4096 x 8 KV heads at head_dim 256, two query heads each:
+// 129 us, 4.3 TB/s; 16 x 32768 x 2 at 128, six heads each: 45 us, 3.2 TB/s. 16 warps an
+// SM (128 registers) use 56 % of the instruction slots and 56 % of the ALU that takes the
+// codes apart, in turns: neither more warps of fewer registers nor two chains of products
+// a tile were faster.
 #pragma once
 
 #include "kv4_append.cuh"

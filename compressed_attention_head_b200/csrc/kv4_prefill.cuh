@@ -12,8 +12,8 @@
 //
 // Split. A block takes one KV head, 128 / group tokens with their query heads as the
 // rows of one accumulator (two of them up to head_dim 128) and 128 keys at a time.
-// Four warps a row tile hold the softmax, a thread a row; four unpack keys and
-// values; one thread issues the products. Scores and probabilities share tensor
+// Eight warps a row tile hold the softmax, half a row a thread; eight unpack keys and
+// values, 16 keys each; one issues the products. Scores and probabilities share tensor
 // memory, probabilities are the A operand from there. With two row tiles one's
 // softmax runs beside the other's products; with one (short chunks, head_dim 256)
 // the scores of the next keys are formed meanwhile.
@@ -22,6 +22,17 @@
 // passes it by 2^4. Pieces: a small kernel first lists the units, longest first, and
 // cuts those that would outlast an even share of all the work; the pieces of a cut one
 // leave partial sums, and the piece that ends last joins them in their order.
+//
+// Measured (one B200): a causal prompt of 2048 tokens, 32 query heads, 8 KV heads,
+// head_dim 128: 76 us, 450 TFLOP/s; 512 tokens of two sequences behind 12001 and 16385
+// others, 12 heads on 2: 172 us, 530 TFLOP/s. 128 keys against two row tiles take about
+// 5000 cycles where the products alone are 2176 and the exponentials 2048: a row tile's
+// softmax (2500), the end of its sum and its next scores (2000) follow one another, and
+// the other tile's fall beside them. The unpacked keys and values, the products' reads
+// of them and the offsets' use 3200 of those cycles of shared memory. Two issuing warps
+// that do not take turns were slower (190 us for the chunks: both softmaxes at once).
+// Not to wait for the end of a sum before the next scores take its operand's place
+// would save about a tenth; nothing orders the two products, so it is waited for.
 #pragma once
 
 #include "kv4_decode.cuh"
