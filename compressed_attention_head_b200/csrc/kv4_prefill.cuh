@@ -276,14 +276,17 @@ __device__ __forceinline__ void make_units(const Pool& c, const RopeArgs& r, con
     atomicAdd(&m.hist[cls(len, parts)], parts * heads);
   }
   __syncthreads();
-  if (tid == 0) {
-    int at = 0;
-    for (int i = 0; i < 64; ++i) {
-      const int n = m.hist[i];
-      m.hist[i] = at;
-      at += n;
+  if (warp == 0) {                            // pieces before each class
+    const int a0 = m.hist[2 * lane], a1 = m.hist[2 * lane + 1];
+    int inc = a0 + a1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
     }
-    p.head->units = min(at, s.cap_units);
+    m.hist[2 * lane] = inc - a0 - a1;
+    m.hist[2 * lane + 1] = inc - a1;
+    if (lane == 31) p.head->units = min(inc, s.cap_units);
   }
   __syncthreads();
   for (int x = tid; x < n_units * heads; x += kPlanThreads) {
@@ -727,9 +730,9 @@ k_prefill4(Pool c, RopeArgs r, TO* __restrict__ out, AttnArgs a, Shape sh, Plan 
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if ((int)blockIdx.x >= plan.head->units) return;
-  const Unit u = plan.units[blockIdx.x];
-  if (u.slot == -2) return;
+  const int units = plan.head->units;
+  const Unit u = plan.units[blockIdx.x];       // (asked for together with their number: there is a place for each block)
+  if ((int)blockIdx.x >= units || u.slot == -2) return;
   const int ns = u.n > sh.tpm ? NS : 1, nt = u.nt;
   if (warp == kIssuer) sm100::tmem_alloc(&s_tmem, 512);
   if (tid == 0) {
