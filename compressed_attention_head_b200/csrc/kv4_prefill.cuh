@@ -48,6 +48,10 @@ constexpr int kInfo = 4;                      // tiles whose factors are kept
 constexpr float kSlack = 4.0f;                // log2 of what a probability may exceed 1 by
 constexpr float kUp = 11.0f;                  // log2 of the probabilities' scale: 2^15 at most with the slack
 
+// Thirty-two rows of 32 elements in shared memory, an odd number of 16-byte words apart: no two lanes meet in a bank.
+template <typename E> __host__ __device__ constexpr int box_pitch() { return 32 * (int)sizeof(E) + 16; }
+constexpr int kBox = 32 * box_pitch<float>();
+
 template <int D> struct Cfg {
   static constexpr int NS = D == 256 ? 1 : 2;          // row tiles of a block
   // Warp groups: two softmax a row tile (each half of the keys: one warp a scheduler would wait for its own
@@ -64,7 +68,10 @@ template <int D> struct Cfg {
   static constexpr int V = K + NKV * OP;
   static constexpr int MEAN = V + NKV * MAIN;
   static constexpr int USED = MEAN + kInfo * KT * 4;
-  static constexpr int TOTAL = (USED > 118784 ? USED : 118784) + 1024;   // one block an SM: it takes all tensor memory
+  // Boxes of the eight warps that write a row tile out: over its queries, where they fit.
+  static constexpr int BOX = OP >= 8 * kBox ? Q : USED, BOX_STEP = OP >= 8 * kBox ? OP : 8 * kBox;
+  static constexpr int ALL = BOX == Q ? USED : USED + NS * BOX_STEP;
+  static constexpr int TOTAL = (ALL > 118784 ? ALL : 118784) + 1024;   // one block an SM: it takes all tensor memory
 };
 
 // One piece of work.
@@ -649,6 +656,18 @@ template <int N> __device__ __forceinline__ void row_scale(uint32_t t_o, float f
   sm100::tmem_wait_st();
 }
 
+// The rows of a box, each to where the lane of its number says (or nowhere).
+template <typename E> __device__ __forceinline__ void unbox(const uint8_t* box, E* to) {
+  constexpr int P = 2 * (int)sizeof(E);                // 16-byte words of a row
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int it = 0; it < P; ++it) {
+    const int row = (32 * it + lane) / P, w = (32 * it + lane) % P;
+    uint4* dst = (uint4*)__shfl_sync(0xffffffffu, (unsigned long long)to, row);
+    if (dst) dst[w] = *(const uint4*)(box + row * box_pitch<E>() + 16 * w);
+  }
+}
+
 // Joins the pieces of a cut unit in their order, a warp a row, by the block that wrote the last of them.
 template <typename TO, int D>
 __device__ __forceinline__ void join_unit(const Plan& plan, const Unit& u, TO* __restrict__ out, const AttnArgs& a, const Shape& sh,
@@ -826,7 +845,9 @@ k_prefill4(Pool c, RopeArgs r, TO* __restrict__ out, AttnArgs a, Shape sh, Plan 
         sm100::mbar_arrive(&b_p[sl]);
       }
       // ---- outputs
-      if (nt > 0 && !dead) dead = !sm100::mbar_wait(&b_fin, 0, a.flags);
+      // (The end of the last sum: with two score buffers this row tile may be two sums behind its softmax, and a
+      // parity of b_o would not tell them apart.)
+      if (nt > 0 && !dead) dead = ns == 2 ? !sm100::mbar_wait(&b_o[i], (nt - 1) & 1, a.flags) : !sm100::mbar_wait(&b_fin, 0, a.flags);
       dead = __any_sync(0xffffffffu, dead);
       sm100::tc_fence_after();
       const float2 own = make_float2(f2_lo(sum.l) + f2_hi(sum.l), f2_lo(sum.m) + f2_hi(sum.m));
@@ -840,8 +861,11 @@ k_prefill4(Pool c, RopeArgs r, TO* __restrict__ out, AttnArgs a, Shape sh, Plan 
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         const int64_t at = (int64_t)(u.tok + ti) * a.n_q + h0 + hh;
         const int64_t pr = whole ? 0 : (int64_t)(u.slot + u.part) * part_rows(NS) + i * M + wt;
-        float* po = plan.parts + pr * D + half * (D / 2);
-        TO* wo = out + at * D + half * (D / 2);
+        // 32 coordinates of 32 rows at a time go through shared memory, so that they leave in whole lines: where
+        // the row tile's queries lie, which nothing reads any more, or behind everything.
+        uint8_t* box = smem + C::BOX + i * C::BOX_STEP + (warp & 7) * kBox;
+        TO* wo = is_row ? out + at * D + half * (D / 2) : nullptr;
+        float* po = is_row ? plan.parts + pr * D + half * (D / 2) : nullptr;
 #pragma unroll 1
         for (int ch = 0; ch < D / 64; ++ch) {
           uint32_t x[32];
@@ -852,25 +876,28 @@ k_prefill4(Pool c, RopeArgs r, TO* __restrict__ out, AttnArgs a, Shape sh, Plan 
 #pragma unroll
             for (int e = 0; e < 32; ++e) x[e] = 0u;
           }
-          if (is_row) {
 #pragma unroll
-            for (int g = 0; g < 32; g += 8) {
-              float o[8];
+          for (int g = 0; g < 32; g += 8) {
+            float o[8];
 #pragma unroll
-              for (int e = 0; e < 8; ++e)                                   // (the codes' order undone)
-                o[((e & 1) << 2) + (e >> 1)] = fmaf(__uint_as_float(x[g + e]), vf, mv);
-              if (whole) {
-                TO y[8];
+            for (int e = 0; e < 8; ++e)                                   // (the codes' order undone)
+              o[((e & 1) << 2) + (e >> 1)] = fmaf(__uint_as_float(x[g + e]), vf, mv);
+            if (whole) {
+              TO y[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = from_f<TO>(l == 0.0f ? 0.0f : o[e] * inv);
+              for (int e = 0; e < 8; ++e) y[e] = from_f<TO>(l == 0.0f ? 0.0f : o[e] * inv);
 #pragma unroll
-                for (int e = 0; e < (int)sizeof(TO) / 2; ++e) ((uint4*)(wo + 32 * ch + g))[e] = ((const uint4*)y)[e];
-              } else {
+              for (int e = 0; e < (int)sizeof(TO) / 2; ++e)
+                *(uint4*)(box + lane * box_pitch<TO>() + g * sizeof(TO) + 16 * e) = ((const uint4*)y)[e];
+            } else {
 #pragma unroll
-                for (int e = 0; e < 8; e += 4) *(float4*)(po + 32 * ch + g + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-              }
+              for (int e = 0; e < 8; e += 4)
+                *(float4*)(box + lane * box_pitch<float>() + (g + e) * 4) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
             }
           }
+          __syncwarp();
+          if (whole) unbox(box, wo == nullptr ? nullptr : wo + 32 * ch);
+          else unbox(box, po == nullptr ? nullptr : po + 32 * ch);
           __syncwarp();
         }
         if (is_row && half == 0) {
