@@ -24,8 +24,8 @@
 // leave partial sums, and the piece that ends last joins them in their order.
 //
 // Measured (one B200): a causal prompt of 2048 tokens, 32 query heads, 8 KV heads,
-// head_dim 128: 76 us, 450 TFLOP/s; 512 tokens of two sequences behind 12001 and 16385
-// others, 12 heads on 2: 172 us, 530 TFLOP/s. 128 keys against two row tiles take about
+// head_dim 128: 72 us, 478 TFLOP/s; 512 tokens of two sequences behind 12001 and 16385
+// others, 12 heads on 2: 164 us, 554 TFLOP/s. 128 keys against two row tiles take about
 // 5000 cycles where the products alone are 2176 and the exponentials 2048: a row tile's
 // softmax (2500), the end of its sum and its next scores (2000) follow one another, and
 // the other tile's fall beside them. The unpacked keys and values, the products' reads
