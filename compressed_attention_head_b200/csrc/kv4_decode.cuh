@@ -3,22 +3,26 @@
 // Mathematics. With q' = q 2^e (a power of two a head, so that fp16 holds it) and
 // codes c, the score of token t is s_t (q . c_t) + m_t sum(q), and the output is
 // sum_t (p_t s_t) (c_t - 8) + sum_t p_t (m_t + 8 s_t): the tensor cores multiply the
-// codes themselves, and the pairs act on scores and probabilities, one token at a
-// time, never on coordinates. A code of 4 bits masked out of its word in place is the
-// fp16 subnormal c 2^-24 (bits 0-3) or 16 c 2^-24 (bits 4-7) in each half of the
-// word: one AND makes two operands, exactly, and the 16 goes into q' or out of the
-// sum. ldmatrix (for the values, its transposed form) lays the words out so that
-// the two halves of a word are the two neighbours along k that mma.sync wants.
+// codes themselves, and the pairs act on scores and probabilities, one token at a time,
+// never on coordinates. A code of 4 bits masked out of its word in place is the fp16 subnormal
+// c 2^-24 (bits 0-3) or 16 c 2^-24 (bits 4-7) in each half of the word: one AND makes
+// two operands, exactly, and the 16 goes into q' or out of the sum. ldmatrix (for the
+// values, its transposed form) lays the words out so that the two halves of a word are
+// the two neighbours along k that mma.sync wants.
 //
 // Softmax: one pass, base 2. Each warp keeps a reference maximum a head, raised
 // when a score passes it by more than 2^4 (one vote a tile), and a reference step
 // (a power of two over all value steps it has met), so that p s, scaled to at most
-// 2^15, keeps fp16's full precision. The 8 that is taken from the codes is taken
-// times the sum of the rounded p s, which one more product with ones gives: so a
-// rounding (half a step, 2^-11) meets at most 8 of the 15 codes, and the part of a
-// value that all its coordinates share stays in float. Up to four query heads a KV
-// head take every other column of the product, so that each lane has one head to
-// score; up to eight take all.
+// 2^15, keeps fp16's full precision. Up to four query heads a KV head take every other
+// column of the product, so that each lane has one head to score; up to eight take all.
+//
+// Roundings. For an fp16 or float output p s enters the product in two fp16 parts, 22
+// bits (with up to four heads the second takes the columns between, with more it is a
+// second product), and the 8 comes off the codes before it: a long context's sum is far
+// smaller than its terms' common part, and the tensor cores cut what they add. For a
+// bf16 output, eight times coarser, one part is enough, and 8 times the sum of the
+// rounded p s, which one more product with ones gives, comes off the sum: the rounding
+// (half a step, 2^-11) meets at most 8 of the 15 codes.
 //
 // Work. The tiles of all (sequence, KV head) pairs form one line that the resident
 // blocks (two an SM) share evenly, whatever the lengths; inside a block tile i goes
@@ -30,7 +34,8 @@
 // before has cleared the counters for that).
 //
 // Measured (one B200): 64 x 4096 x 8 KV heads at head_dim 256, two query heads each:
-// 129 us, 4.3 TB/s; 16 x 32768 x 2 at 128, six heads each: 45 us, 3.2 TB/s. 16 warps an
+// 128 us, 4.3 TB/s; 16 x 32768 x 2 at 128, six heads each: 49 us, 2.9 TB/s (45 us with one
+// part and the 8 off the sum, but an output half again as far from the exact one). 16 warps an
 // SM (128 registers) use 56 % of the instruction slots and 56 % of the ALU that takes the
 // codes apart, in turns: neither more warps of fewer registers nor two chains of products
 // a tile were faster.
@@ -114,6 +119,13 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
   return *(const uint32_t*)&h;
 }
 __device__ __forceinline__ float2 unpack_h2(uint32_t u) { return __half22float2(*(const __half2*)&u); }
+
+// Two codes less 8: c 2^-24 or (odd nibbles) 16 c 2^-24, exact.
+__device__ __forceinline__ uint32_t less_middle(uint32_t c, bool odd) {
+  const uint32_t mid = odd ? 0x00800080u : 0x00080008u;
+  const __half2 r = __hsub2(*(const __half2*)&c, *(const __half2*)&mid);
+  return *(const uint32_t*)&r;
+}
 
 // Attended positions [lo, hi) of a row's query; hi = 0 where there is nothing to do.
 struct Span { int lo, hi; };
@@ -282,6 +294,9 @@ __device__ __forceinline__ void join_parts(const float* parts, int begin, int hh
   *l_out = l;
 }
 
+template <typename T> __host__ __device__ constexpr bool is_bf16() { return false; }
+template <> __host__ __device__ constexpr bool is_bf16<__nv_bfloat16>() { return true; }
+
 // JOIN: the block that writes a pair's last piece joins them (AttnArgs::done); else a kernel behind this one does.
 template <typename T, typename TO, int D, bool PAIR, bool JOIN>
 __global__ void __launch_bounds__(32 * W, 2)
@@ -289,6 +304,7 @@ k_decode4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, Att
           Desc* descs) {
   using C = Cfg<D>;
   constexpr int HS = PAIR ? 4 : 8;
+  constexpr bool FINE = !is_bf16<TO>();         // weights in two parts
   constexpr int NC = D / 32;                    // 16-byte chunks of a code row
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[W][C::NST];
@@ -613,7 +629,7 @@ k_decode4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, Att
       // ---- probabilities, and the values' product
 #pragma unroll
       for (int n = 0; n < C::NB; ++n) {
-        uint32_t b[2];
+        uint32_t b[2], b2[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           float ps[2] = {0.0f, 0.0f};
@@ -625,9 +641,19 @@ k_decode4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, Att
             msum[i] = fmaf(p, vm[n][e], msum[i]);
             ps[i] = p * step;
           }
-          b[e] = movm(pack_h2(ps[0], ps[1]));
+          if constexpr (FINE && PAIR) {
+            const float hi = __half2float(__float2half_rn(ps[0]));
+            b[e] = movm(pack_h2(hi, ps[0] - hi));
+          } else {
+            const uint32_t hi = pack_h2(ps[0], ps[1]);
+            b[e] = movm(hi);
+            if constexpr (FINE) {
+              const float2 f = unpack_h2(hi);
+              b2[e] = movm(pack_h2(ps[0] - f.x, ps[1] - f.y));
+            }
+          }
         }
-        mma(tot, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, b[0], b[1]);
+        if constexpr (!FINE) mma(tot, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, b[0], b[1]);
 #pragma unroll
         for (int j = 0; j < NC; j += 2) {
           uint32_t w[4];
@@ -636,9 +662,15 @@ k_decode4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, Att
           for (int p = 0; p < 4; ++p) {
             const uint32_t mask = (p & 1) ? 0x00f000f0u : 0x000f000fu;
             const int sh = p < 2 ? 0 : 8;
-            const uint32_t a0 = (w[0] >> sh) & mask, a1 = (w[1] >> sh) & mask, a2 = (w[2] >> sh) & mask,
-                           a3 = (w[3] >> sh) & mask;
+            uint32_t a0 = (w[0] >> sh) & mask, a1 = (w[1] >> sh) & mask, a2 = (w[2] >> sh) & mask, a3 = (w[3] >> sh) & mask;
+            if constexpr (FINE) {
+              a0 = less_middle(a0, p & 1);
+              a1 = less_middle(a1, p & 1);
+              a2 = less_middle(a2, p & 1);
+              a3 = less_middle(a3, p & 1);
+            }
             mma(acc[2 * j + p], a0, a1, a2, a3, b[0], b[1]);
+            if constexpr (FINE && !PAIR) mma(acc[2 * j + p], a0, a1, a2, a3, b2[0], b2[1]);
           }
         }
       }
@@ -707,7 +739,8 @@ k_decode4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, Att
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
               const float* x = acc[4 * jr + p];
-              o[p] = fmaf(x[2 * half + i], (p & 1) ? 0x1p20f : 0x1p24f, -8.0f * tot[i]) * fw[i];
+              const float v = FINE && PAIR ? x[2 * half] + x[2 * half + 1] : x[2 * half + i], up = (p & 1) ? 0x1p20f : 0x1p24f;
+              o[p] = (FINE ? v * up : fmaf(v, up, -8.0f * tot[i])) * fw[i];
             }
             *(float4*)(merge + (warp * HS + hh) * MC + 64 * jr - r0 + 32 * half + 4 * g) = o4;
           }
