@@ -384,7 +384,7 @@ class PagedKV4(_Described):
     """Caller-owned pool of pages and the page table of a batch (see sq_kv4_cache in sq.h)."""
 
     pages: torch.Tensor          # uint8 [n_pages, n_kv, page_tokens / 16, 16 d + 128]
-    table: torch.Tensor          # int32 [batch, pages_per_row]; the rows may be strided
+    table: torch.Tensor          # int32 [batch, pages_per_row]; the rows may be strided, not share memory
     n_kv: int
     d: int
     page_tokens: int
@@ -399,6 +399,8 @@ class PagedKV4(_Described):
         if self.table.dtype != torch.int32 or self.table.dim() != 2 or (self.table.shape[1] > 1
                                                                         and self.table.stride(1) != 1):
             raise ValueError("table: an int32 tensor [batch, pages_per_row] with rows of stride 1 is wanted")
+        if self.table.shape[0] > 1 and self.table.stride(0) < self.table.shape[1]:
+            raise ValueError("table: rows that share memory (an expanded table?) are not taken, make it contiguous")
 
     @property
     def batch(self) -> int:
@@ -409,9 +411,10 @@ class PagedKV4(_Described):
 
     def struct(self) -> sq_kv4_cache:
         self.check()
+        batch, per_row = self.table.shape
         return sq_kv4_cache(self.pages.data_ptr(), self.table.data_ptr(), self.pages.shape[0],
-                            max(self.table.stride(0), self.table.shape[1]), self.table.shape[0], self.table.shape[1],
-                            self.n_kv, self.d, self.page_tokens)
+                            self.table.stride(0) if batch > 1 else per_row, batch, per_row, self.n_kv, self.d,
+                            self.page_tokens)
 
 
 @dataclass

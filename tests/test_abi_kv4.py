@@ -143,3 +143,23 @@ def test_binding_refuses_wrong_tensors():
         sq.sq_kv4_attn_decode(c, start, k, 0.0, k, 64, torch.zeros(1 << 10, dtype=torch.uint8))
     with pytest.raises(ValueError):
         sq.alloc_kv4(4, 2, 96, 16, table, device="cpu")
+
+
+def test_page_tables_whose_rows_share_memory_are_refused():
+    """A row stride below a row's length would be read past the table; wider rows and a single row are taken."""
+    pages = torch.zeros(8, 2, 1, 16 * 128 + 128, dtype=torch.uint8)
+    row = torch.arange(4, dtype=torch.int32)[None]
+    make = lambda t: sq.PagedKV4(pages, t, 2, 128, 16)  # noqa: E731
+    for bad in (row.expand(3, -1), torch.zeros(16, dtype=torch.int32).as_strided((3, 4), (2, 1)),
+                torch.zeros(16, dtype=torch.int32).as_strided((2, 4), (3, 1))):
+        with pytest.raises(ValueError, match="share memory"):
+            make(bad)
+        c = make(row)
+        c.table = bad                                            # set later, refused by the next call
+        with pytest.raises(ValueError, match="share memory"):
+            c.ref()
+    wide = torch.zeros(3, 10, dtype=torch.int32)
+    for t, stride in ((row, 4), (row.expand(1, -1), 4), (row.expand(3, -1).contiguous(), 4), (wide[:, :4], 10), (wide[:, :1], 10),
+                      (wide[:1, :4], 4), (torch.zeros(16, dtype=torch.int32).as_strided((1, 4), (1, 1)), 4)):
+        s = make(t).struct()
+        assert (s.table_stride, s.batch, s.pages_per_row) == (stride, t.shape[0], t.shape[1])
