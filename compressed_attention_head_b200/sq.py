@@ -366,17 +366,22 @@ def sq_wait_selftest(limit_us, flags, stream=None):
 # spend few on the host: addresses go as plain integers, and the structures of a cache
 # and of a rotation table are made once and again when a field of theirs is set.
 class _Described:
-    """Keeps what describe() made of its fields until one of them is set, or a tensor of them moves."""
+    """Keeps what struct() made of its fields until one of them is set, or a tensor of them moves or changes form."""
 
     def __setattr__(self, name, value):
         self.__dict__[name] = value
         self.__dict__["_made"] = None
 
+    def described(self):
+        """(reference to the structure, the structure, what it was made of)."""
+        made, where = self._made, self.where()
+        if made is None or made[2] != where:
+            struct = self.struct()
+            made = self.__dict__["_made"] = (ctypes.byref(struct), struct, where)
+        return made
+
     def ref(self):
-        made = self._made
-        if made is None or made[1] != self.where():
-            made = self.__dict__["_made"] = (ctypes.byref(self.struct()), self.where())
-        return made[0]
+        return self.described()[0]
 
 
 @dataclass
@@ -407,7 +412,8 @@ class PagedKV4(_Described):
         return self.table.shape[0]
 
     def where(self):
-        return self.pages.data_ptr(), self.table.data_ptr(), self.table.shape
+        p, t = self.pages, self.table
+        return p.data_ptr(), p.numel(), p.is_contiguous(), t.data_ptr(), t.shape, t.stride(), t.dtype
 
     def struct(self) -> sq_kv4_cache:
         self.check()
@@ -432,7 +438,8 @@ class Rope(_Described):
             raise ValueError("rotation table: a contiguous float32 tensor [n_pos, rot_dim] is wanted")
 
     def where(self):
-        return self.table.data_ptr(), self.table.shape
+        t = self.table
+        return t.data_ptr(), t.shape, t.is_contiguous(), t.dtype
 
     def struct(self) -> sq_rope:
         self.check()
@@ -521,10 +528,11 @@ def sq_kv4_append(cache, k, v, start, cu=None, rope=None, flags=None, stream=Non
     kp, k0, k1 = _kv4_heads("k", k, cache.n_kv, cache.d)
     n = k.shape[0]
     vp, v0, v1 = _kv4_heads("v", v, cache.n_kv, cache.d, n, k.dtype)
-    batch = cache.batch
+    ref, made, _ = cache.described()
+    batch = made.batch
     at = _kv4_ints("start", start, batch)
     cu = None if cu is None else _kv4_ints("cu", cu, batch + 1)
-    _check(lib().sq_kv4_append(cache.ref(), kp, vp, DTYPE_CODE[k.dtype], k0, k1, v0, v1, n, cu, at,
+    _check(lib().sq_kv4_append(ref, kp, vp, DTYPE_CODE[k.dtype], k0, k1, v0, v1, n, cu, at,
                                rope.ref() if rope else None, _kv4_at(flags), st), "sq_kv4_append")
 
 
@@ -534,10 +542,11 @@ def sq_kv4_read(cache, start, cu, k_out, v_out, flags=None, stream=None):
     kp, k0, k1 = _kv4_heads("k_out", k_out, cache.n_kv, cache.d)
     n = k_out.shape[0]
     vp, v0, v1 = _kv4_heads("v_out", v_out, cache.n_kv, cache.d, n, k_out.dtype)
-    batch = cache.batch
+    ref, made, _ = cache.described()
+    batch = made.batch
     at = _kv4_ints("start", start, batch)
     cu = None if cu is None else _kv4_ints("cu", cu, batch + 1)
-    _check(lib().sq_kv4_read(cache.ref(), kp, vp, DTYPE_CODE[k_out.dtype], k0, k1, v0, v1, n, cu, at, _kv4_at(flags), st),
+    _check(lib().sq_kv4_read(ref, kp, vp, DTYPE_CODE[k_out.dtype], k0, k1, v0, v1, n, cu, at, _kv4_at(flags), st),
            "sq_kv4_read")
 
 
@@ -549,11 +558,12 @@ def sq_kv4_attn_decode(cache, seq_lens, q, scale, out, max_ctx, ws, rope=None, w
                        stream=None):
     """Attention of q [batch, n_q_heads, d] over the first seq_lens[b] tokens of every sequence (see sq.h)."""
     st = _kv4_call(stream, cache.pages, cache.table, q, out, seq_lens, lse, ws, flags, rope.table if rope else None)
-    batch = cache.batch
+    ref, made, _ = cache.described()
+    batch = made.batch
     qp, q0, q1 = _kv4_heads("q", q, None, cache.d, batch)
     op, lp = _kv4_out(out, lse, q)
     wp, wn = _kv4_bytes(ws)
-    _check(lib().sq_kv4_attn_decode(cache.ref(), _kv4_ints("seq_lens", seq_lens, batch), q.shape[1], max_ctx, qp,
+    _check(lib().sq_kv4_attn_decode(ref, _kv4_ints("seq_lens", seq_lens, batch), q.shape[1], max_ctx, qp,
                                     DTYPE_CODE[q.dtype], q0, q1, rope.ref() if rope else None, scale, window, op,
                                     DTYPE_CODE[out.dtype], lp, wp, wn, _kv4_at(flags), st), "sq_kv4_attn_decode")
 
@@ -562,13 +572,14 @@ def sq_kv4_decode_step(cache, k, v, q, pos, scale, out, max_ctx, ws, rope=None, 
                        stream=None):
     """Append one token a sequence at pos[b], then attend over pos[b] + 1 tokens (see sq.h)."""
     st = _kv4_call(stream, cache.pages, cache.table, k, v, q, out, pos, lse, ws, flags, rope.table if rope else None)
-    batch, n_kv, d, dtype = cache.batch, cache.n_kv, cache.d, q.dtype
+    ref, made, _ = cache.described()
+    batch, n_kv, d, dtype = made.batch, cache.n_kv, cache.d, q.dtype
     qp, q0, q1 = _kv4_heads("q", q, None, d, batch)
     kp, k0, k1 = _kv4_heads("k", k, n_kv, d, batch, dtype)
     vp, v0, v1 = _kv4_heads("v", v, n_kv, d, batch, dtype)
     op, lp = _kv4_out(out, lse, q)
     wp, wn = _kv4_bytes(ws)
-    _check(lib().sq_kv4_decode_step(cache.ref(), kp, vp, qp, DTYPE_CODE[dtype], k0, k1, v0, v1, q0, q1,
+    _check(lib().sq_kv4_decode_step(ref, kp, vp, qp, DTYPE_CODE[dtype], k0, k1, v0, v1, q0, q1,
                                     _kv4_ints("pos", pos, batch), q.shape[1], max_ctx, rope.ref() if rope else None,
                                     scale, window, op, DTYPE_CODE[out.dtype], lp, wp, wn, _kv4_at(flags), st),
            "sq_kv4_decode_step")
@@ -581,11 +592,12 @@ def sq_kv4_attn_prefill_workspace(batch, n_q_heads, n_kv_heads, d, n_tok) -> int
 def sq_kv4_attn_prefill(cache, start, cu, q, scale, out, ws, rope=None, window=0, lse=None, flags=None, stream=None):
     """Causal attention of q [tokens, n_q_heads, d], token cu[b] + i at position start[b] + i (see sq.h)."""
     st = _kv4_call(stream, cache.pages, cache.table, q, out, start, cu, lse, ws, flags, rope.table if rope else None)
-    batch = cache.batch
+    ref, made, _ = cache.described()
+    batch = made.batch
     qp, q0, q1 = _kv4_heads("q", q, None, cache.d)
     op, lp = _kv4_out(out, lse, q)
     wp, wn = _kv4_bytes(ws)
-    _check(lib().sq_kv4_attn_prefill(cache.ref(), _kv4_ints("cu", cu, batch + 1), _kv4_ints("start", start, batch),
+    _check(lib().sq_kv4_attn_prefill(ref, _kv4_ints("cu", cu, batch + 1), _kv4_ints("start", start, batch),
                                      q.shape[1], q.shape[0], qp, DTYPE_CODE[q.dtype], q0, q1, rope.ref() if rope else None,
                                      scale, window, op, DTYPE_CODE[out.dtype], lp, wp, wn, _kv4_at(flags), st),
            "sq_kv4_attn_prefill")

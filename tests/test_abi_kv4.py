@@ -163,3 +163,27 @@ def test_page_tables_whose_rows_share_memory_are_refused():
                       (wide[:1, :4], 4), (torch.zeros(16, dtype=torch.int32).as_strided((1, 4), (1, 1)), 4)):
         s = make(t).struct()
         assert (s.table_stride, s.batch, s.pages_per_row) == (stride, t.shape[0], t.shape[1])
+
+
+def test_descriptions_follow_tensors_that_change_in_place():
+    """Same address, other shape, stride or type: the kept structures are made again, and refused where they do not fit."""
+    table = torch.zeros(64, dtype=torch.int32)[:16].view(4, 4)
+    pages = torch.zeros(8, 2, 1, 16 * 128 + 128, dtype=torch.uint8)
+    c = sq.PagedKV4(pages, table, 2, 128, 16)
+    assert c.described()[1].table_stride == 4 and c.ref() is c.ref()
+    table.as_strided_((4, 4), (16, 1))
+    assert c.described()[1].table_stride == 16
+    table.as_strided_((4, 4), (0, 1))
+    with pytest.raises(ValueError, match="share memory"):
+        c.ref()
+    table.as_strided_((4, 4), (4, 1))
+    pages.resize_(4, 2, 1, 16 * 128 + 128)
+    assert c.described()[1].n_pages == 4
+    pages.as_strided_((2, 2, 1, 16 * 128 + 128), (16 * 128 + 128, 2 * (16 * 128 + 128), 16 * 128 + 128, 1))
+    with pytest.raises(ValueError, match="contiguous"):
+        c.ref()
+    rope = sq.Rope(torch.zeros(16, 16))
+    assert rope.described()[1].rot_dim == 16
+    rope.table.as_strided_((16, 16), (1, 16))
+    with pytest.raises(ValueError, match="contiguous"):
+        rope.ref()
