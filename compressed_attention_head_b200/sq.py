@@ -483,13 +483,14 @@ def _kv4_ints(name, t, n):
 
 
 def _kv4_heads(name, t, heads, d, rows=None, dtype=None):
-    """Address, token stride and head stride of a tensor [rows, heads, d] (heads None: any number)."""
+    """Address, token stride and head stride of a tensor [rows, heads, d] (heads None: any number); the stride of an
+    axis of one element, which may be any number, is 0."""
     if t.dim() == 3:
         n, h, e = t.shape
         s0, s1, s2 = t.stride()
         if ((heads is None or h == heads) and e == d and s2 == 1 and t.dtype in DTYPE_CODE
                 and (rows is None or n == rows) and (dtype is None or t.dtype == dtype)):
-            return t.data_ptr(), s0, s1
+            return t.data_ptr(), s0 if n > 1 else 0, s1 if h > 1 else 0
     raise ValueError(f"{name}: a tensor [{'tokens' if rows is None else rows}, {'heads' if heads is None else heads}, {d}] "
                      f"of stride 1 along the last axis{'' if dtype is None else f' and type {dtype}'} is wanted")
 

@@ -187,3 +187,13 @@ def test_descriptions_follow_tensors_that_change_in_place():
     rope.table.as_strided_((16, 16), (1, 16))
     with pytest.raises(ValueError, match="contiguous"):
         rope.ref()
+
+
+def test_strides_of_axes_of_one_element_are_not_asked_for():
+    """A row or a head taken out of a wider tensor keeps a stride that nothing uses; others are passed on as they are."""
+    wide = torch.zeros(5, 2 * 128 + 4, dtype=torch.float16)
+    assert sq._kv4_heads("q", wide[:1, :256].unflatten(1, (2, 128)), 2, 128)[1:] == (0, 128)
+    assert sq._kv4_heads("q", wide[:3, :256].unflatten(1, (2, 128)), 2, 128)[1:] == (260, 128)
+    odd = torch.zeros(4096, dtype=torch.float16).as_strided((3, 1, 128), (256, 1, 1))
+    assert sq._kv4_heads("k", odd, 1, 128)[1:] == (256, 0)
+    assert sq._kv4_heads("k", odd[:0], 1, 128)[1:] == (0, 0)
