@@ -516,8 +516,12 @@ k_decode4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, Att
           look();
         }
       }
-      if (!dead && !sm100::mbar_wait(&bars[warp][stage], (phase >> stage) & 1u, a.flags)) dead = true;
-      dead = __any_sync(0xffffffffu, dead);
+      if (!dead && __any_sync(0xffffffffu, !sm100::mbar_wait(&bars[warp][stage], (phase >> stage) & 1u, a.flags))) {
+        // given up: no more copies, but those on their way (of the other stages too) are waited for, with a limit again
+        dead = true;
+#pragma unroll 1
+        for (int i = 0; i < C::NST; ++i) sm100::mbar_wait(&bars[warp][i], (phase >> i) & 1u, nullptr);
+      }
       phase ^= 1u << stage;
       const uint32_t sb = ring_u + stage * C::STAGE;
       const uint8_t* sp = ring + stage * C::STAGE;

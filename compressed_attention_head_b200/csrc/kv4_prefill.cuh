@@ -1121,7 +1121,7 @@ k_prefill4(Pool c, RopeArgs r, TO* __restrict__ out, AttnArgs a, Shape sh, Plan 
                            C::OP, &b_q);
       }
       __syncwarp();
-      wait(&b_q, 0);
+      if (!wait(&b_q, 0)) sm100::mbar_wait(&b_q, 0, nullptr);      // given up: the copies are waited for once more
       // Scores may not take the place of probabilities before the product that reads those has ended: products
       // of different accumulators are not ordered among each other, so the end is waited for.
       if (ns == 1) {
