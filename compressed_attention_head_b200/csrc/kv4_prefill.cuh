@@ -8,7 +8,10 @@
 // therefore what the cache holds, to float's roundings. For the values s (c - 8) is
 // unpacked in the same way against the rounded probabilities, and sum p (m + 8 s) is
 // kept in float beside the running sum: only the part that varies within a vector
-// meets a probability of 11 bits.
+// meets a rounded probability. For an fp16 or float output that is two fp16 parts, 21
+// bits, and a second product of the same values; one part left fp16 outputs 1.3 times
+// as far from the exact ones as their own rounding does. For a bf16 output, eight times
+// coarser, it is one part of 11 bits.
 //
 // Split. A block takes one KV head, 128 / group tokens with their query heads as the
 // rows of one accumulator (two of them up to head_dim 128) and 128 keys at a time.
@@ -24,15 +27,16 @@
 // leave partial sums, and the piece that ends last joins them in their order.
 //
 // Measured (one B200): a causal prompt of 2048 tokens, 32 query heads, 8 KV heads,
-// head_dim 128: 72 us, 478 TFLOP/s; 512 tokens of two sequences behind 12001 and 16385
-// others, 12 heads on 2: 164 us, 554 TFLOP/s. 128 keys against two row tiles take about
-// 5000 cycles where the products alone are 2176 and the exponentials 2048: a row tile's
-// softmax (2500), the end of its sum and its next scores (2000) follow one another, and
-// the other tile's fall beside them. The unpacked keys and values, the products' reads
-// of them and the offsets' use 3200 of those cycles of shared memory. Two issuing warps
-// that do not take turns were slower (190 us for the chunks: both softmaxes at once).
-// Not to wait for the end of a sum before the next scores take its operand's place
-// would save about a tenth; nothing orders the two products, so it is waited for.
+// head_dim 128, fp16: 82 us, 422 TFLOP/s (72 with one part); 512 tokens of two
+// sequences behind 12001 and 16385 others, 12 heads on 2, bf16: 165 us, 551 TFLOP/s.
+// With one part 128 keys against two row tiles take about 5000 cycles where the
+// products alone are 2176 and the exponentials 2048: a row tile's softmax (2500), the
+// end of its sum and its next scores (2000) follow one another, and the other tile's
+// fall beside them. The unpacked keys and values, the products' reads of them and the
+// offsets' use 3200 of those cycles of shared memory. Two issuing warps that do not
+// take turns were slower (190 us for the chunks: both softmaxes at once). Not to wait
+// for the end of a sum before the next scores take its operand's place would save about
+// a tenth; nothing orders the two products, so it is waited for.
 #pragma once
 
 #include "kv4_decode.cuh"
@@ -573,9 +577,28 @@ __device__ __forceinline__ float row_max_edge(uint32_t t_s, const uint32_t* ok, 
 }
 
 struct Sums { f2 l, m; };
+// A step's operand of the values' product: the probabilities of 16 keys in 8 columns of tensor memory, and for an fp16
+// or float output what that rounding left of them in 8 more.
+template <bool FINE> __host__ __device__ constexpr int prob_cols() { return FINE ? 16 : 8; }
+// Two probabilities of it. The first part has a float's upper 11 bits (fp16's own below 2^-14), the second the rest.
+template <bool FINE> __device__ __forceinline__ void put_probs(uint32_t* pk, int at, float p0, float p1) {
+  if constexpr (FINE) {
+    const float h0 = __uint_as_float(__float_as_uint(p0) & 0xffffe000u), h1 = __uint_as_float(__float_as_uint(p1) & 0xffffe000u);
+    const f2 rest = f2_add(f2_of(p0, p1), f2_of(-h0, -h1));
+    pk[at] = dec::pack_h2(h0, h1);
+    pk[at + 8] = dec::pack_h2(f2_lo(rest), f2_hi(rest));
+  } else {
+    pk[at] = dec::pack_h2(p0, p1);
+  }
+}
+template <bool FINE> __device__ __forceinline__ void store_probs(uint32_t t_s, const uint32_t* pk) {
+  if constexpr (FINE) st16(t_s, pk);
+  else sm100::tmem_st8(t_s, pk);
+}
 // Scores to probabilities 2^(s fk + nb), which take the place of the first half of
-// them; the sums grow by their sum and their sum with the offsets. The sums and
-// roundings of 16 keys are written beside the exponentials of the next 16.
+// them, or of all; the sums grow by their sum and their sum with the offsets. The sums
+// and roundings of 16 keys are written beside the exponentials of the next 16.
+template <bool FINE>
 __device__ __forceinline__ Sums row_probs(uint32_t t_s, float fk, float nb, const float* mean, Sums sum) {
   const f2 fk2 = f2_of(fk, fk), nb2 = f2_of(nb, nb);
   uint32_t s[2][16];
@@ -584,7 +607,7 @@ __device__ __forceinline__ Sums row_probs(uint32_t t_s, float fk, float nb, cons
 #pragma unroll
   for (int ch = 0; ch <= 4; ++ch) {
     uint32_t* x = s[ch & 1];
-    uint32_t pk[8];
+    uint32_t pk[prob_cols<FINE>()];
     if (ch < 4) {
       ld_wait16(x);
       if (ch < 3) ld16(t_s + 16 * (ch + 1), s[(ch + 1) & 1]);
@@ -598,8 +621,8 @@ __device__ __forceinline__ Sums row_probs(uint32_t t_s, float fk, float nb, cons
         sum.m = f2_fma(pa, mu.x, sum.m);
         sum.l = f2_add(sum.l, pb);
         sum.m = f2_fma(pb, mu.y, sum.m);
-        pk[e / 2] = dec::pack_h2(p[e], p[e + 1]);
-        pk[e / 2 + 1] = dec::pack_h2(p[e + 2], p[e + 3]);
+        put_probs<FINE>(pk, e / 2, p[e], p[e + 1]);
+        put_probs<FINE>(pk, e / 2 + 1, p[e + 2], p[e + 3]);
       }
       if (ch < 4) {
         const f2 ta = f2_fma(f2_of(x[e], x[e + 1]), fk2, nb2), tb = f2_fma(f2_of(x[e + 2], x[e + 3]), fk2, nb2);
@@ -609,15 +632,16 @@ __device__ __forceinline__ Sums row_probs(uint32_t t_s, float fk, float nb, cons
         p[e + 3] = dec::ex2(f2_hi(tb));
       }
     }
-    if (ch > 0) sm100::tmem_st8(t_s + 8 * (ch - 1), pk);
+    if (ch > 0) store_probs<FINE>(t_s + prob_cols<FINE>() * (ch - 1), pk);
   }
   return sum;
 }
+template <bool FINE>
 __device__ __forceinline__ Sums row_probs_edge(uint32_t t_s, float fk, float nb, const float* mean, Sums sum,
                                                const uint32_t* ok, int key0, int lo, int hi) {
 #pragma unroll 1
   for (int ch = 0; ch < 4; ++ch) {
-    uint32_t x[16], pk[8];
+    uint32_t x[16], pk[prob_cols<FINE>()];
     ld16(t_s + 16 * ch, x);
     const uint32_t keep = keys_kept(ok[ch >> 1], key0 + 32 * (ch >> 1), lo, hi) >> (16 * (ch & 1));
     ld_wait16(x);
@@ -630,9 +654,9 @@ __device__ __forceinline__ Sums row_probs_edge(uint32_t t_s, float fk, float nb,
       const f2 p = f2_of(p0, p1);
       sum.l = f2_add(sum.l, p);
       sum.m = f2_fma(p, f2_of(k0 ? m0 : 0.0f, k1 ? m1 : 0.0f), sum.m);
-      pk[e / 2] = dec::pack_h2(p0, p1);
+      put_probs<FINE>(pk, e / 2, p0, p1);
     }
-    sm100::tmem_st8(t_s + 8 * ch, pk);
+    store_probs<FINE>(t_s + prob_cols<FINE>() * ch, pk);
   }
   return sum;
 }
@@ -735,6 +759,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
 k_prefill4(Pool c, RopeArgs r, TO* __restrict__ out, AttnArgs a, Shape sh, Plan plan) {
   using C = Cfg<D>;
   constexpr int NS = C::NS, NKV = C::NKV;
+  constexpr bool FINE = !dec::is_bf16<TO>();     // probabilities in two parts
   constexpr int kUnpack = C::SOFT * 4, kIssuer = kUnpack + 8;        // first unpacking warp, the one that issues
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t b_q, b_fin, b_s[2], b_p[2], b_o[NS], b_kf[NKV], b_ke[NKV], b_vf[NKV], b_ve[NKV], b_i[kInfo];
@@ -839,7 +864,7 @@ k_prefill4(Pool c, RopeArgs r, TO* __restrict__ out, AttnArgs a, Shape sh, Plan 
           vref = nv;
         }
         const float nb = kUp - (mref == -INFINITY ? 0.0f : mref);
-        sum = edge ? row_probs_edge(t_s, fk, nb, mean, sum, ok, key0, lo, hi) : row_probs(t_s, fk, nb, mean, sum);
+        sum = edge ? row_probs_edge<FINE>(t_s, fk, nb, mean, sum, ok, key0, lo, hi) : row_probs<FINE>(t_s, fk, nb, mean, sum);
         sm100::tmem_wait_st();
         sm100::tc_fence_before();
         sm100::mbar_arrive(&b_p[sl]);
@@ -1106,7 +1131,11 @@ k_prefill4(Pool c, RopeArgs r, TO* __restrict__ out, AttnArgs a, Shape sh, Plan 
         const uint64_t vd = desc_of(va, 16384, 1024, 2);
         if (elect_one()) {
 #pragma unroll
-          for (int s = 0; s < KT / 16; ++s) sm100::mma_f16_ts(d, p + 64 * (s >> 2) + 8 * (s & 3), vd + 128 * s, id_o, (s > 0 || k > 0) ? 1u : 0u);
+          for (int s = 0; s < KT / 16; ++s) {
+            const uint32_t ps = p + 64 * (s >> 2) + prob_cols<FINE>() * (s & 3);
+            sm100::mma_f16_ts(d, ps, vd + 128 * s, id_o, (s > 0 || k > 0) ? 1u : 0u);
+            if constexpr (FINE) sm100::mma_f16_ts(d, ps + 8, vd + 128 * s, id_o, 1u);
+          }
           sm100::mma_commit(&b_o[i]);
           if (last) sm100::mma_commit(&b_ve[k % NKV]);
         }

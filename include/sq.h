@@ -607,7 +607,9 @@ size_t sq_kv4_attn_workspace(int batch, int n_q_heads, int n_kv_heads, int d, in
  *               dtype after the rotation.
  *  scale        > 0, or <= 0 for 1 / sqrt(d).
  *  window       0, or the number of last positions attended.
- *  out          device, out_dtype (any) [batch][n_q_heads][d]; 16-byte aligned.
+ *  out          device, out_dtype (any) [batch][n_q_heads][d]; 16-byte aligned. Sums
+ *               are held in float; the softmax's weights keep 21 bits or more for an
+ *               fp16 or float output, 11 for a bf16 one.
  *  lse_out      device float [batch][n_q_heads] (may be NULL): natural logarithm of
  *               the sum of exp(score); -inf where nothing was attended.
  *  ws           16-byte aligned; needs no particular contents, and may be shared by

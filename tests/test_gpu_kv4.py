@@ -754,3 +754,68 @@ def test_offsets_below_zero_name_no_tokens():
         k = torch.randn(2, n_kv, d, device="cuda", dtype=F16)
         sq.sq_kv4_append(cache, k, k, start, torch.tensor([first, 2, 2, 2], dtype=torch.int32, device="cuda"))
         assert torch.equal(cache.pages, before)
+
+
+# ------------------------------------------------------------------ weights of fp16 and float outputs
+def near_uniform(d, n, n_q, seed=0):
+    """Sixteen-token blocks of steps near 1 and offsets -7.5 steps, and queries so small that every weight is close to 1 / n."""
+    pool = random_pool(-(-n // 16), 1, 16, d, seed, device="cpu")
+    q = (torch.randn(n, n_q, d, generator=torch.Generator().manual_seed(seed + 1)) * 2.0 ** -11).to(F16)
+    return pool, q
+
+
+def weighted(pool_np, q, n, one_part=False):
+    """Float64 outputs [n_q, d] of one query over the first n tokens of page after page, and what two-part weights may be off by
+    (below); or the outputs with every weight times its step rounded once to fp16."""
+    d = q.shape[-1]
+    table = np.arange(len(pool_np))[None]
+    (kc, ks, km), (vc, vs, vm) = (rows_of(pool_np, table, 0, 0, n, 16, side) for side in (0, 1))
+    keys, vals = kv4.values(kc, ks, km), kv4.values(vc, vs, vm)
+    s, m = kv4.bf16_value(vs).astype(np.float64), kv4.bf16_value(vm).astype(np.float64)
+    x = q.astype(np.float64) @ keys.T / math.sqrt(d)
+    p = np.exp(x - x.max(-1, keepdims=True))
+    l = p.sum(-1, keepdims=True)
+    mid = vc - 8.0
+    if one_part:
+        w = (p * s * 2048.0).astype(np.float16).astype(np.float64) / 2048.0
+        return (w @ mid + (p * (m + 8 * s)) @ np.ones_like(mid)) / l
+    aq = np.abs(q.astype(np.float64))
+    delta = ((d + 16) * 2.0 ** -24 / math.sqrt(d) * (kv4.bf16_value(ks) * (aq @ kc.T) + np.abs(kv4.bf16_value(km)) * aq.sum(-1, keepdims=True))).max()
+    p /= l
+    spread, size = (p * s) @ np.abs(mid), p @ np.abs(vals)
+    # 2^-21: two parts. Sums of the products: the tokens are one step of 16 along k (two of a tile), in one or two
+    # products, whose 17 terms each may lose a unit of 2^-23 of the largest: 4 x 17 x 2^-23 < 2^-16. Then exponents
+    # (delta and the 2^-20 of a base-2 exponential, in numerator and denominator), fp16's smallest steps, float sums.
+    bound = (2.0 ** -21 + 2.0 ** -16) * spread + 2 * (delta + 2.0 ** -20) * size + n * 2.0 ** -32 * s.max() + (n + 8) * 2.0 ** -24 * size
+    return p @ vals, bound
+
+
+@pytest.mark.parametrize("d,n_q", [(64, 2), (128, 4), (256, 1), (64, 7), (128, 8), (256, 5)])
+def test_fp16_and_float_outputs_take_their_weights_in_two_parts(d, n_q):
+    """Outputs over sixteen near-equal weights, far nearer than weights of 11 bits could bring them: decode and chunks."""
+    n = 16
+    pool, q = near_uniform(d, n, n_q)
+    pn, qn = pool.numpy(), q.float().numpy()
+    want, bound = zip(*[weighted(pn, qn[i], i + 1) for i in range(n)])
+    coarse = np.stack([weighted(pn, qn[i], i + 1, True) for i in range(n)])
+    want, bound = np.stack(want), np.stack(bound)
+    assert (np.abs(coarse - want) > bound)[8:].mean() > 0.5            # one part would be seen
+    unit = np.abs(want.astype(np.float16).astype(np.float64) - want)   # of an exact result rounded once
+    cache = sq.PagedKV4(pool.cuda(), torch.zeros(1, 1, dtype=torch.int32).cuda(), 1, d, 16)
+    one = lambda x: torch.tensor(x, dtype=torch.int32).cuda()  # noqa: E731
+    for out_dtype in (F32, F16):
+        outs = []
+        out = torch.empty(n, n_q, d, device="cuda", dtype=out_dtype)
+        ws = torch.empty(sq.sq_kv4_attn_prefill_workspace(1, n_q, 1, d, n), dtype=torch.uint8, device="cuda")
+        sq.sq_kv4_attn_prefill(cache, one([0]), one([0, n]), q.cuda(), 0.0, out, ws)
+        outs.append(out)
+        out = torch.empty(n, n_q, d, device="cuda", dtype=out_dtype)
+        ws = torch.empty(sq.sq_kv4_attn_workspace(1, n_q, 1, d, n), dtype=torch.uint8, device="cuda")
+        for i in range(n):
+            sq.sq_kv4_attn_decode(cache, one([i + 1]), q[i:i + 1].cuda(), 0.0, out[i:i + 1], n, ws)
+        outs.append(out)
+        for out in outs:
+            err = np.abs(out.double().cpu().numpy() - want)
+            assert np.all(err <= bound + torch.finfo(out_dtype).eps / 2 * np.abs(want) + 2.0 ** -25)
+            if out_dtype == F16:       # root mean squares: the rounding's own, and beside it at most the bound's
+                assert np.sqrt((err ** 2).mean()) <= np.sqrt((unit ** 2).mean()) + np.sqrt((bound ** 2).mean())
