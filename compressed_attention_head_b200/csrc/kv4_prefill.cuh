@@ -175,7 +175,7 @@ __device__ __forceinline__ void make_units(const Pool& c, const RopeArgs& r, con
         n = (int)((uint32_t)(t_hi - t_lo + s.tpu - 1) / (uint32_t)s.tpu);
         const int64_t start = __ldg(a.start + b), last = start + (t_hi - t_lo) - 1;
         uint32_t bits = 0;
-        if (last >= c.cap() || start < -1) bits |= SQ_FLAG_SEQLEN;
+        if (last >= c.cap() || start < 0) bits |= SQ_FLAG_SEQLEN;
         if (r.table && min(last, c.cap() - 1) >= r.n_pos) bits |= SQ_FLAG_ROPE;
         if (bits && a.flags) atomicOr(a.flags, bits);
       }

@@ -646,7 +646,9 @@ size_t sq_kv4_attn_prefill_workspace(int batch, int n_q_heads, int n_kv_heads, i
  * d_start[b] + i of sequence b and attends to the positions up to its own (the
  * chunk appended first), the last `window` of them when window > 0. Other arguments
  * as above, out [n_tok][n_q_heads][d], lse_out [n_tok][n_q_heads]; output rows of
- * tokens from d_cu[batch] on are left as they were.
+ * tokens from d_cu[batch] on are left as they were. d_flags: SQ_FLAG_SEQLEN for a
+ * position below 0 (its outputs are zeros) or past the row's pages (it attends to
+ * what they hold); SQ_FLAG_PAGE and SQ_FLAG_ROPE as above.
  */
 sq_status sq_kv4_attn_prefill(const sq_kv4_cache* cache, const int32_t* d_cu, const int32_t* d_start, int n_q_heads,
                               int64_t n_tok, const void* q, sq_dtype dtype, int64_t q_stride_tok,

@@ -819,3 +819,41 @@ def test_fp16_and_float_outputs_take_their_weights_in_two_parts(d, n_q):
             assert np.all(err <= bound + torch.finfo(out_dtype).eps / 2 * np.abs(want) + 2.0 ** -25)
             if out_dtype == F16:       # root mean squares: the rounding's own, and beside it at most the bound's
                 assert np.sqrt((err ** 2).mean()) <= np.sqrt((unit ** 2).mean()) + np.sqrt((bound ** 2).mean())
+
+
+# ------------------------------------------------------------------ chunks that raise flags
+def guarded(shape, dtype, fill, room=256):
+    """(a tensor of that fill inside a larger buffer, a function that says whether the buffer around it is as it was)."""
+    n = math.prod(shape)
+    room = room // torch.empty(0, dtype=dtype).element_size()
+    buf = torch.full((n + 2 * room,), fill, dtype=dtype, device="cuda")
+    return buf[room:room + n].view(shape), lambda: bool((buf[:room] == fill).all()) and bool((buf[room + n:] == fill).all())
+
+
+def flagged_chunks(cache, table, page, q, start, cu, bit, pos, n_kv, rope=None, skip=None, window=0, like=None):
+    """One call of chunk attention: its flags, the rows of `pos` against the oracle (position -1: zeros), rows that no sequence
+    names (-1, 0) left alone, nothing written around outputs and workspace."""
+    Q_TYPE[0] = q.dtype
+    n_tok, n_q, d = q.shape
+    out, out_ok = guarded((n_tok, n_q, d), F32, 3.0)
+    lse, lse_ok = guarded((n_tok, n_q), F32, 3.0)
+    ws, ws_ok = guarded((sq.sq_kv4_attn_prefill_workspace(len(start), n_q, n_kv, d, n_tok),), torch.uint8, 255)
+    flags = torch.zeros(1, dtype=torch.int32, device="cuda")
+    sq.sq_kv4_attn_prefill(cache, torch.tensor(start, dtype=torch.int32).cuda(), torch.tensor(cu, dtype=torch.int32).cuda(), q,
+                           0.0, out, ws, rope=None if rope is None else sq.Rope(torch.from_numpy(rope).cuda()), window=window,
+                           lse=lse, flags=flags)
+    assert flags.item() == bit
+    assert out_ok() and lse_ok() and ws_ok()
+    if pos is not None:
+        check_attention(out, lse, q, pos, cache.pages, table, page, n_q, n_kv, d, F32, rope, window=window, skip=skip)
+        left = [i for i, (b, _) in enumerate(pos) if b < 0]
+        assert (out[left] == 3).all() and (lse[left] == 3).all()
+
+
+def test_chunks_that_begin_before_position_zero_are_flagged():
+    cache, table = small_cache(batch=2)
+    q = torch.randn(6, 4, 128, generator=torch.Generator().manual_seed(0)).to(F16).cuda()
+    for start, bit in ((-1, sq.SQ_FLAG_SEQLEN), (-2, sq.SQ_FLAG_SEQLEN), (0, 0)):
+        pos = [(0, max(start + i, -1)) for i in range(3)] + [(1, 20 + i) for i in range(2)] + [(-1, 0)]
+        flagged_chunks(cache, table, 16, q, [start, 20], [0, 3, 5], bit, pos, 1)
+    flagged_chunks(cache, table, 16, q, [-7, 20], [0, 0, 5], 0, [(1, 20 + i) for i in range(5)] + [(-1, 0)], 1)   # no token there
