@@ -239,7 +239,8 @@ pre::Shape prefill_shape(int batch, int n_kv, int group, int d, int64_t n_tok) {
   s.tpm = pre::M / s.gt;
   s.tpu = s.tpm * (d == 256 ? 1 : 2);
   s.sms = sms();
-  // Units longer than an even share of the keys are cut, so fewer than `sms` are, into fewer than 2 `sms` pieces.
+  // A unit is cut when it is longer than an even share or more of all tiles of all units, so fewer than `sms` are, into
+  // fewer than 2 `sms` pieces: sum ceil(len / cut) < sum len / cut + sms <= 2 sms.
   s.cap_slots = 2 * s.sms;
   const int64_t units = (int64_t)n_kv * s.nsub * ((n_tok + s.tpu - 1) / s.tpu + batch) + s.cap_slots;
   s.cap_units = units > 0x7fffffff ? 0 : (int)units;

@@ -85,7 +85,7 @@ struct Unit {
   int tok, n;          // first token of the call, tokens
   int off;             // of the first token in its sequence
   int t0, nt;          // key tiles
-  int slot;            // of the first piece's partial sums, -1: the whole of it, -2: nothing to do
+  int slot;            // of the first piece's partial sums, -1: the whole of it
   int part, parts;     // which piece of how many
 };
 struct Head { int units, pad[3]; };
@@ -170,7 +170,8 @@ __device__ __forceinline__ void make_units(const Pool& c, const RopeArgs& r, con
     const int b = b0 + tid;
     int n = 0;
     if (b < c.batch) {
-      const int64_t t_lo = __ldg(a.cu + b), t_hi = min((int64_t)__ldg(a.cu + b + 1), a.n_tok);
+      const int64_t t_lo = __ldg(a.cu + b), t_end = __ldg(a.cu + b + 1), t_hi = min(t_end, a.n_tok);
+      if (t_end < t_lo) raise(a.flags, SQ_FLAG_SEQLEN);   // sequences may name the same tokens, and units have no place
       if (t_lo >= 0 && t_hi > t_lo) {
         n = (int)((uint32_t)(t_hi - t_lo + s.tpu - 1) / (uint32_t)s.tpu);
         const int64_t start = __ldg(a.start + b), last = start + (t_hi - t_lo) - 1;
@@ -307,9 +308,7 @@ __device__ __forceinline__ void make_units(const Pool& c, const RopeArgs& r, con
     int at = atomicAdd(&m.hist[cls(l.len, parts)], parts), slot = -1;
     if (parts > 1) {
       slot = atomicAdd(&m.slots, parts);
-      // (more than there are places for only when the offsets overlap, which is not allowed)
-      if (slot + parts <= s.cap_slots) p.done[slot] = 0;
-      else slot = -2;
+      p.done[slot] = 0;                       // (there are places for all, whatever the offsets: see prefill_shape)
     }
     Unit w = unit_of(c, a, s, l.row, l.j);
     int64_t lo, hi;
@@ -776,7 +775,7 @@ k_prefill4(Pool c, RopeArgs r, TO* __restrict__ out, AttnArgs a, Shape sh, Plan 
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int units = plan.head->units;
   const Unit u = plan.units[blockIdx.x];       // (asked for together with their number: there is a place for each block)
-  if ((int)blockIdx.x >= units || u.slot == -2) return;
+  if ((int)blockIdx.x >= units) return;
   const int ns = u.n > sh.tpm ? NS : 1, nt = u.nt;
   if (warp == kIssuer) sm100::tmem_alloc(&s_tmem, 512);
   if (tid == 0) {

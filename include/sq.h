@@ -571,7 +571,8 @@ size_t sq_kv4_page_bytes(int n_kv_heads, int d, int page_tokens);
  *  n_tok        token rows of k and v.
  *  d_cu         device int32[batch + 1], rising from 0 or more: tokens d_cu[b] ..
  *               d_cu[b + 1] - 1 belong to sequence b; rows from d_cu[batch] on (a padded batch) are
- *               left alone. NULL: token b belongs to sequence b.
+ *               left alone, offsets past n_tok name no rows, and neither does a sequence whose
+ *               first offset is below 0. NULL: token b belongs to sequence b.
  *  d_start      device int32[batch]: position of each sequence's first new token.
  *  rope         NULL: no rotation. The values are never rotated.
  *  d_flags      SQ_FLAG_CAPACITY (a position the row's pages do not reach, or a
@@ -648,7 +649,8 @@ size_t sq_kv4_attn_prefill_workspace(int batch, int n_q_heads, int n_kv_heads, i
  * as above, out [n_tok][n_q_heads][d], lse_out [n_tok][n_q_heads]; output rows of
  * tokens from d_cu[batch] on are left as they were. d_flags: SQ_FLAG_SEQLEN for a
  * position below 0 (its outputs are zeros) or past the row's pages (it attends to
- * what they hold); SQ_FLAG_PAGE and SQ_FLAG_ROPE as above.
+ * what they hold), and for offsets that fall (rows that sequences then share are
+ * undefined, some are not written); SQ_FLAG_PAGE and SQ_FLAG_ROPE as above.
  */
 sq_status sq_kv4_attn_prefill(const sq_kv4_cache* cache, const int32_t* d_cu, const int32_t* d_start, int n_q_heads,
                               int64_t n_tok, const void* q, sq_dtype dtype, int64_t q_stride_tok,

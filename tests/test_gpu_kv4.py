@@ -857,3 +857,18 @@ def test_chunks_that_begin_before_position_zero_are_flagged():
         pos = [(0, max(start + i, -1)) for i in range(3)] + [(1, 20 + i) for i in range(2)] + [(-1, 0)]
         flagged_chunks(cache, table, 16, q, [start, 20], [0, 3, 5], bit, pos, 1)
     flagged_chunks(cache, table, 16, q, [-7, 20], [0, 0, 5], 0, [(1, 20 + i) for i in range(5)] + [(-1, 0)], 1)   # no token there
+
+
+def test_chunk_offsets_that_fall_are_flagged():
+    """Falling offsets raise a flag and write nothing outside the call's rows; offsets past the rows, and sequences that begin
+    below 0, name no rows."""
+    cache, table = small_cache(batch=3)
+    q = torch.randn(8, 4, 128, generator=torch.Generator().manual_seed(0)).to(F16).cuda()
+    rows = lambda *r: [(b, p + i) for b, p, n in r for i in range(n)]  # noqa: E731
+    flagged_chunks(cache, table, 16, q, [0, 5, 9], [0, 4, 2, 8], sq.SQ_FLAG_SEQLEN, None, 1)
+    flagged_chunks(cache, table, 16, q, [0, 5, 9], [0, 3, 3, 1], sq.SQ_FLAG_SEQLEN, rows((0, 0, 3)) + [(-1, 0)] * 5, 1)
+    flagged_chunks(cache, table, 16, q, [0, 5, 9], [0, 3, 400, 401], 0, rows((0, 0, 3), (1, 5, 5)), 1)
+    flagged_chunks(cache, table, 16, q, [7, 5, 9], [-1, 3, 5, 8], 0, [(-1, 0)] * 3 + rows((1, 5, 2), (2, 9, 3)), 1)
+    many, table = small_cache(batch=64, tokens=2048)      # 32 x 32 units, more than the 392 or so that there are places for
+    q = torch.randn(2048, 4, 128, generator=torch.Generator().manual_seed(0)).to(F16).cuda()
+    flagged_chunks(many, table, 16, q, [0] * 64, [0, 2048] * 32 + [0], sq.SQ_FLAG_SEQLEN, None, 1)
