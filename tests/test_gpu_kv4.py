@@ -872,3 +872,38 @@ def test_chunk_offsets_that_fall_are_flagged():
     many, table = small_cache(batch=64, tokens=2048)      # 32 x 32 units, more than the 392 or so that there are places for
     q = torch.randn(2048, 4, 128, generator=torch.Generator().manual_seed(0)).to(F16).cuda()
     flagged_chunks(many, table, 16, q, [0] * 64, [0, 2048] * 32 + [0], sq.SQ_FLAG_SEQLEN, None, 1)
+
+
+@pytest.mark.parametrize("d,group,start,new,page,window", [
+    (128, 4, [100, 0, 16], [40, 30, 1], 16, 0), (64, 1, [5000], [7], 64, 0), (256, 2, [700, 300], [90, 5], 32, 0),
+    (128, 2, [900], [70], 16, 130)])
+def test_chunks_leave_pages_outside_the_pool_out(d, group, start, new, page, window):
+    """Page numbers past the pool and below 0 inside the attended span, in units that are cut (few rows, many keys) and are not."""
+    table, total = make_table([-(-(s + n) // page) for s, n in zip(start, new)], 3)
+    pool = random_pool(total, 1, page, d, 3)
+    skip = {0: (0, (start[0] + 3) // page - 1, (start[0] + 3) // page)} if not window else {0: ((start[0] + 3) // page - 2,)}
+    wrong = table.copy()
+    for b, pages in skip.items():
+        for i, p in enumerate(pages):
+            wrong[b, p] = (total, -1, 2 ** 31 - 1)[i % 3]
+    cache = sq.PagedKV4(pool, torch.from_numpy(wrong).cuda(), 1, d, page)
+    cu = np.concatenate([[0], np.cumsum(new)]).tolist()
+    q = torch.randn(cu[-1], group, d, generator=torch.Generator().manual_seed(1)).to(F16).cuda()
+    pos = [(b, start[b] + i) for b in range(len(new)) for i in range(new[b])]
+    flagged_chunks(cache, table, page, q, start, cu, sq.SQ_FLAG_PAGE, pos, 1, skip=skip, window=window)
+
+
+@pytest.mark.parametrize("d,n_pos,window", [(128, 50, 0), (64, 33, 0), (256, 50, 20), (128, 1, 0), (64, 50, 4)])
+def test_chunks_past_the_rotation_table_give_zeros(d, n_pos, window):
+    cache, table = small_cache(d=d, batch=2, tokens=80)
+    start, cu = [30, 0], [0, 45, 75]
+    q = torch.randn(76, 3, d, generator=torch.Generator().manual_seed(1)).to(F16).cuda()
+    pos = [(b, p if p < n_pos else -1) for b in (0, 1) for p in range(start[b], start[b] + cu[b + 1] - cu[b])] + [(-1, 0)]
+    flagged_chunks(cache, table, 16, q, start, cu, sq.SQ_FLAG_ROPE, pos, 1, rope=kv4.rope_table(n_pos, d), window=window)
+
+
+def test_chunks_past_the_pages_attend_to_what_they_hold():
+    cache, table = small_cache(batch=2)
+    q = torch.randn(10, 4, 128, generator=torch.Generator().manual_seed(1)).to(F16).cuda()
+    pos = [(0, min(60 + i, 63)) for i in range(8)] + [(1, 3), (1, 4)]
+    flagged_chunks(cache, table, 16, q, [60, 3], [0, 8, 10], sq.SQ_FLAG_SEQLEN, pos, 1)
