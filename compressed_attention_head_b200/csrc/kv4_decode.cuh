@@ -452,7 +452,8 @@ k_decode4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, Att
       for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[e]));
 #pragma unroll
       for (int o = 1; o < D / 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      // 2^e with top 2^e in [2^14, 2^15); queries that are zero or not finite are taken as they are
+      // 2^e with top 2^e in [2^14, 2^15); queries that are zero or not finite are taken as they are. Not below 2^-100,
+      // where the score factor, 2^(24 - e), would pass a float's range: queries of 2^116 and above overflow.
       int e2 = 0;
       if (top > 0.0f && top < INFINITY) e2 = max(-100, min(100, 14 - ilogbf(top)));
       const float up = ldexpf(1.0f, e2);

@@ -415,9 +415,9 @@ k_prepare4(Pool c, RopeArgs r, const T* __restrict__ q, AttnArgs a, Shape s, Pla
       for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(x[e >> 3][e & 7]));
 #pragma unroll
       for (int o = 1; o < TPR; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      // 2^e with top 2^e in [2^6, 2^7): the sum over a head stays below 2^15
+      // 2^e with top 2^e in [2^6, 2^7): the sum over a head stays below 2^15 (-121 for the largest floats)
       int e2 = 0;
-      if (top > 0.0f && top < INFINITY) e2 = max(-100, min(100, 6 + 127 - (int)(__float_as_uint(top) >> 23)));
+      if (top > 0.0f && top < INFINITY) e2 = min(100, 6 + 127 - (int)(__float_as_uint(top) >> 23));
       const float up = __int_as_float((127 + e2) << 23);
       float sum = 0.0f;
       uint32_t w[2][4];

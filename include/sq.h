@@ -605,7 +605,8 @@ size_t sq_kv4_attn_workspace(int batch, int n_q_heads, int n_kv_heads, int d, in
  *               position that `rope` turns it by. 0: outputs are zeros.
  *  max_ctx      host bound on the lengths (longer ones are cut, SQ_FLAG_SEQLEN).
  *  q            device, dtype (SQ_F16 or SQ_BF16), strides as above, rounded to
- *               dtype after the rotation.
+ *               dtype after the rotation. Coordinates of magnitude 2^116 and more
+ *               (bf16) give NaN (not in sq_kv4_attn_prefill).
  *  scale        > 0, or <= 0 for 1 / sqrt(d).
  *  window       0, or the number of last positions attended.
  *  out          device, out_dtype (any) [batch][n_q_heads][d]; 16-byte aligned. Sums

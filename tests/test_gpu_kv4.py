@@ -907,3 +907,32 @@ def test_chunks_past_the_pages_attend_to_what_they_hold():
     q = torch.randn(10, 4, 128, generator=torch.Generator().manual_seed(1)).to(F16).cuda()
     pos = [(0, min(60 + i, 63)) for i in range(8)] + [(1, 3), (1, 4)]
     flagged_chunks(cache, table, 16, q, [60, 3], [0, 8, 10], sq.SQ_FLAG_SEQLEN, pos, 1)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_queries_near_the_largest_floats(d):
+    """bf16 queries up to 2^127 (2^116 for single tokens) over keys so small that the scores are moderate."""
+    Q_TYPE[0] = BF16
+    page, n, up = 16, 60, 121
+    table, total = make_table([-(-n // page)], 5)
+    pool = random_pool(total, 1, page, d, 5)
+    pairs = pool[..., 16 * d:].contiguous().view(BF16).view(total, 1, 1, 2, 16, 2).float()
+    pairs[:, :, :, 0] *= 2.0 ** -(up - 1)                 # keys' steps from 2^-124 on
+    cache = lambda pairs: sq.PagedKV4(torch.cat([pool[..., :16 * d], pairs.to(BF16).contiguous().view(torch.uint8).view(total, 1, 1, 128)], -1),  # noqa: E731
+                                      torch.from_numpy(table).cuda(), 1, d, page)
+    q = torch.randn(9, 3, d, generator=torch.Generator().manual_seed(1)).clamp(-3.9, 3.9)
+    q[:, :, 0] = 3.9
+    c, x = cache(pairs), (q * 2.0 ** (up + 4)).to(BF16).cuda()
+    assert torch.isfinite(x).all() and x.float().amax() > 2.0 ** 126
+    out, lse = torch.empty(9, 3, d, device="cuda"), torch.empty(9, 3, device="cuda")
+    ws = torch.empty(sq.sq_kv4_attn_prefill_workspace(1, 3, 1, d, 9), dtype=torch.uint8, device="cuda")
+    sq.sq_kv4_attn_prefill(c, torch.tensor([n - 9], dtype=torch.int32).cuda(), torch.tensor([0, 9], dtype=torch.int32).cuda(),
+                           x, 2.0 ** -8, out, ws, lse=lse)
+    check_attention(out, lse, x, [(0, n - 9 + i) for i in range(9)], c.pages, table, page, 3, 1, d, F32, scale=2.0 ** -8)
+    pairs[:, :, :, 0] *= 2.0 ** 11
+    c, x = cache(pairs), (q[:1] * 2.0 ** (up - 7)).to(BF16).cuda()
+    assert 2.0 ** 115 < x.float().amax() < 2.0 ** 116
+    out, lse = torch.empty(1, 3, d, device="cuda"), torch.empty(1, 3, device="cuda")
+    ws = torch.empty(sq.sq_kv4_attn_workspace(1, 3, 1, d, n), dtype=torch.uint8, device="cuda")
+    sq.sq_kv4_attn_decode(c, torch.tensor([n], dtype=torch.int32).cuda(), x, 2.0 ** -8, out, n, ws, lse=lse)
+    check_attention(out, lse, x, [(0, n - 1)], c.pages, table, page, 3, 1, d, F32, scale=2.0 ** -8)
