@@ -22,7 +22,11 @@
 // smaller than its terms' common part, and the tensor cores cut what they add. For a
 // bf16 output, eight times coarser, one part is enough, and 8 times the sum of the
 // rounded p s, which one more product with ones gives, comes off the sum: the rounding
-// (half a step, 2^-11) meets at most 8 of the 15 codes.
+// (half a step, 2^-11) meets at most 8 of the 15 codes. It comes off every sixteen
+// tiles: the tensor cores cut units of the sum so far, of which a long context leaves
+// little (32768 near-equal weights at head_dim 256: outputs 1.44 times as far from the
+// exact ones as their rounding when it comes off at the end, 1.01 times so, for 2 us
+// of the 125).
 //
 // Work. The tiles of all (sequence, KV head) pairs form one line that the resident
 // blocks (two an SM) share evenly, whatever the lengths; inside a block tile i goes
@@ -66,6 +70,7 @@ namespace dec {
 constexpr int W = 8;                       // warps of a block
 constexpr int kMaxHeads = 8;               // query heads of one pass over a KV head
 constexpr float kSlack = 4.0f;             // log2 of what a probability may exceed 1 by
+constexpr int kTake = 16;                  // tiles of a warp after which 8 times the weights' sum comes off its sums
 constexpr float kTop = 2048.0f;            // 2^11: scale of p s / reference, at most 2^15 with the slack
 
 template <int D> struct Cfg {
@@ -506,178 +511,189 @@ k_decode4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, Att
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
 
-    for (; mine < seg_end; mine += W) {
-      // the next copy goes into the stage that the tile before this one has left
-      {
-        int st = stage + C::NST - 1;
-        st = st >= C::NST ? st - C::NST : st;
-        __syncwarp();
-        if (!dead && pf_has) {
-          issue(st);
-          look();
+    while (mine < seg_end) {
+      const int stop = FINE ? seg_end : min(seg_end, mine + kTake * W);
+      for (; mine < stop; mine += W) {
+        // the next copy goes into the stage that the tile before this one has left
+        {
+          int st = stage + C::NST - 1;
+          st = st >= C::NST ? st - C::NST : st;
+          __syncwarp();
+          if (!dead && pf_has) {
+            issue(st);
+            look();
+          }
         }
-      }
-      if (!dead && __any_sync(0xffffffffu, !sm100::mbar_wait(&bars[warp][stage], (phase >> stage) & 1u, a.flags))) {
-        // given up: no more copies, but those on their way (of the other stages too) are waited for, with a limit again
-        dead = true;
+        if (!dead && __any_sync(0xffffffffu, !sm100::mbar_wait(&bars[warp][stage], (phase >> stage) & 1u, a.flags))) {
+          // given up: no more copies, but those on their way (of the other stages too) are waited for, with a limit again
+          dead = true;
 #pragma unroll 1
-        for (int i = 0; i < C::NST; ++i) sm100::mbar_wait(&bars[warp][i], (phase >> i) & 1u, nullptr);
-      }
-      phase ^= 1u << stage;
-      const uint32_t sb = ring_u + stage * C::STAGE;
-      const uint8_t* sp = ring + stage * C::STAGE;
-      const uint32_t okm = dead ? 0u : oks[warp][stage];
-      stage = stage + 1 == C::NST ? 0 : stage + 1;
-      const int t0 = pos0 + (mine - seg) * C::TT;
-      const bool edge = okm != (1u << C::NB) - 1u || t0 < at.lo || t0 + C::TT > at.hi;
-      if (okm == 0) continue;
-      // ---- scores
-      float u[C::NB][2][NHL], t[C::NB][2][NHL], vs[C::NB][2], vm[C::NB][2];
-      bool over = false;
+          for (int i = 0; i < C::NST; ++i) sm100::mbar_wait(&bars[warp][i], (phase >> i) & 1u, nullptr);
+        }
+        phase ^= 1u << stage;
+        const uint32_t sb = ring_u + stage * C::STAGE;
+        const uint8_t* sp = ring + stage * C::STAGE;
+        const uint32_t okm = dead ? 0u : oks[warp][stage];
+        stage = stage + 1 == C::NST ? 0 : stage + 1;
+        const int t0 = pos0 + (mine - seg) * C::TT;
+        const bool edge = okm != (1u << C::NB) - 1u || t0 < at.lo || t0 + C::TT > at.hi;
+        if (okm == 0) continue;
+        // ---- scores
+        float u[C::NB][2][NHL], t[C::NB][2][NHL], vs[C::NB][2], vm[C::NB][2];
+        bool over = false;
 #pragma unroll
-      for (int n = 0; n < C::NB; ++n) {
-        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int n = 0; n < C::NB; ++n) {
+          float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int j = 0; j < NC; j += 2) {
-          uint32_t w[4];
-          ldsm4(sb + n * blk_bytes(D) + (koff ^ (j << 4)), w);
+          for (int j = 0; j < NC; j += 2) {
+            uint32_t w[4];
+            ldsm4(sb + n * blk_bytes(D) + (koff ^ (j << 4)), w);
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            uint4 b;
-            if constexpr (C::QREG) b = qf[j + k];
-            else b = *(const uint4*)(qsrc + (j + k) * 64);
-            const uint32_t x = w[2 * k], y = w[2 * k + 1], xs = x >> 8, ys = y >> 8;
-            mma(s, x & 0x000f000fu, y & 0x000f000fu, x & 0x00f000f0u, y & 0x00f000f0u, b.x, b.y);
-            mma(s, xs & 0x000f000fu, ys & 0x000f000fu, xs & 0x00f000f0u, ys & 0x00f000f0u, b.z, b.w);
+            for (int k = 0; k < 2; ++k) {
+              uint4 b;
+              if constexpr (C::QREG) b = qf[j + k];
+              else b = *(const uint4*)(qsrc + (j + k) * 64);
+              const uint32_t x = w[2 * k], y = w[2 * k + 1], xs = x >> 8, ys = y >> 8;
+              mma(s, x & 0x000f000fu, y & 0x000f000fu, x & 0x00f000f0u, y & 0x00f000f0u, b.x, b.y);
+              mma(s, xs & 0x000f000fu, ys & 0x000f000fu, xs & 0x00f000f0u, ys & 0x00f000f0u, b.z, b.w);
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t kw = *(const uint32_t*)(sp + n * blk_bytes(D) + k_pairs(D) + (g + 8 * e) * 4);
+            const uint32_t vw = *(const uint32_t*)(sp + n * blk_bytes(D) + v_pairs(D) + (g + 8 * e) * 4);
+            const float ks = __uint_as_float(kw << 16), km = __uint_as_float(kw & 0xffff0000u);
+            vs[n][e] = __uint_as_float(vw << 16);
+            vm[n][e] = fmaf(8.0f, vs[n][e], __uint_as_float(vw & 0xffff0000u));
+#pragma unroll
+            for (int i = 0; i < NHL; ++i) {
+              u[n][e][i] = fmaf(ks, s[2 * e + i], km * fm[i]);
+              t[n][e][i] = fmaf(u[n][e][i], fq[i], nref[i]);
+            }
           }
         }
+        if (edge) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint32_t kw = *(const uint32_t*)(sp + n * blk_bytes(D) + k_pairs(D) + (g + 8 * e) * 4);
-          const uint32_t vw = *(const uint32_t*)(sp + n * blk_bytes(D) + v_pairs(D) + (g + 8 * e) * 4);
-          const float ks = __uint_as_float(kw << 16), km = __uint_as_float(kw & 0xffff0000u);
-          vs[n][e] = __uint_as_float(vw << 16);
-          vm[n][e] = fmaf(8.0f, vs[n][e], __uint_as_float(vw & 0xffff0000u));
+          for (int n = 0; n < C::NB; ++n)
 #pragma unroll
-          for (int i = 0; i < NHL; ++i) {
-            u[n][e][i] = fmaf(ks, s[2 * e + i], km * fm[i]);
-            t[n][e][i] = fmaf(u[n][e][i], fq[i], nref[i]);
-          }
+            for (int e = 0; e < 2; ++e) {
+              const int p = t0 + 16 * n + 8 * e + g;
+              if (p < at.lo || p >= at.hi || !((okm >> n) & 1u)) {
+                vs[n][e] = vm[n][e] = 0.0f;
+#pragma unroll
+                for (int i = 0; i < NHL; ++i) u[n][e][i] = t[n][e][i] = -INFINITY;
+              }
+            }
         }
-      }
-      if (edge) {
+        // ---- the references
 #pragma unroll
         for (int n = 0; n < C::NB; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int p = t0 + 16 * n + 8 * e + g;
-            if (p < at.lo || p >= at.hi || !((okm >> n) & 1u)) {
-              vs[n][e] = vm[n][e] = 0.0f;
+            over |= vs[n][e] > sref;
 #pragma unroll
-              for (int i = 0; i < NHL; ++i) u[n][e][i] = t[n][e][i] = -INFINITY;
-            }
+            for (int i = 0; i < NHL; ++i) over |= t[n][e][i] > kSlack;
           }
-      }
-      // ---- the references
+        if (__any_sync(0xffffffffu, over)) {
+          float st = 0.0f;
 #pragma unroll
-      for (int n = 0; n < C::NB; ++n)
+          for (int n = 0; n < C::NB; ++n) st = fmaxf(st, fmaxf(vs[n][0], vs[n][1]));
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          over |= vs[n][e] > sref;
-#pragma unroll
-          for (int i = 0; i < NHL; ++i) over |= t[n][e][i] > kSlack;
-        }
-      if (__any_sync(0xffffffffu, over)) {
-        float st = 0.0f;
-#pragma unroll
-        for (int n = 0; n < C::NB; ++n) st = fmaxf(st, fmaxf(vs[n][0], vs[n][1]));
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) st = fmaxf(st, __shfl_xor_sync(0xffffffffu, st, o));
-        float down = 1.0f;
-        if (st > sref) {
-          // the power of two at or above the step, kept where its reciprocal stays a float
-          const float ns = fminf(pow2_up(st), 0x1p126f);
-          down = sref / ns;
-          sref = ns;
-          sinv = kTop / ns;
-        }
-#pragma unroll
-        for (int i = 0; i < NHL; ++i) {
-          float mx = -INFINITY;
-#pragma unroll
-          for (int n = 0; n < C::NB; ++n) mx = fmaxf(mx, fmaxf(u[n][0][i], u[n][1][i]));
-#pragma unroll
-          for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-          mx *= fq[i];
-          float f = 1.0f;
-          if (mx > -nref[i]) {
-            f = ex2(-nref[i] - mx);            // 0 the first time
-            nref[i] = -mx;
-            lsum[i] *= f;
-            msum[i] *= f;
+          for (int o = 4; o < 32; o <<= 1) st = fmaxf(st, __shfl_xor_sync(0xffffffffu, st, o));
+          float down = 1.0f;
+          if (st > sref) {
+            // the power of two at or above the step, kept where its reciprocal stays a float
+            const float ns = fminf(pow2_up(st), 0x1p126f);
+            down = sref / ns;
+            sref = ns;
+            sinv = kTop / ns;
           }
-          f *= down;
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (PAIR || (j & 1) == i) tot[j] *= f;
-#pragma unroll
-          for (int m = 0; m < D / 16; ++m)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (PAIR || (j & 1) == i) acc[m][j] *= f;
-#pragma unroll
-          for (int n = 0; n < C::NB; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) t[n][e][i] = u[n][e][i] == -INFINITY ? -INFINITY : fmaf(u[n][e][i], fq[i], nref[i]);
-        }
-      }
-      // ---- probabilities, and the values' product
-#pragma unroll
-      for (int n = 0; n < C::NB; ++n) {
-        uint32_t b[2], b2[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float ps[2] = {0.0f, 0.0f};
-          const float step = vs[n][e] * sinv;
 #pragma unroll
           for (int i = 0; i < NHL; ++i) {
-            const float p = ex2(t[n][e][i]);
-            lsum[i] += p;
-            msum[i] = fmaf(p, vm[n][e], msum[i]);
-            ps[i] = p * step;
+            float mx = -INFINITY;
+#pragma unroll
+            for (int n = 0; n < C::NB; ++n) mx = fmaxf(mx, fmaxf(u[n][0][i], u[n][1][i]));
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            mx *= fq[i];
+            float f = 1.0f;
+            if (mx > -nref[i]) {
+              f = ex2(-nref[i] - mx);            // 0 the first time
+              nref[i] = -mx;
+              lsum[i] *= f;
+              msum[i] *= f;
+            }
+            f *= down;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (PAIR || (j & 1) == i) tot[j] *= f;
+#pragma unroll
+            for (int m = 0; m < D / 16; ++m)
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (PAIR || (j & 1) == i) acc[m][j] *= f;
+#pragma unroll
+            for (int n = 0; n < C::NB; ++n)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) t[n][e][i] = u[n][e][i] == -INFINITY ? -INFINITY : fmaf(u[n][e][i], fq[i], nref[i]);
           }
-          if constexpr (FINE && PAIR) {
-            const float hi = __half2float(__float2half_rn(ps[0]));
-            b[e] = movm(pack_h2(hi, ps[0] - hi));
-          } else {
-            const uint32_t hi = pack_h2(ps[0], ps[1]);
-            b[e] = movm(hi);
-            if constexpr (FINE) {
-              const float2 f = unpack_h2(hi);
-              b2[e] = movm(pack_h2(ps[0] - f.x, ps[1] - f.y));
+        }
+        // ---- probabilities, and the values' product
+#pragma unroll
+        for (int n = 0; n < C::NB; ++n) {
+          uint32_t b[2], b2[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float ps[2] = {0.0f, 0.0f};
+            const float step = vs[n][e] * sinv;
+#pragma unroll
+            for (int i = 0; i < NHL; ++i) {
+              const float p = ex2(t[n][e][i]);
+              lsum[i] += p;
+              msum[i] = fmaf(p, vm[n][e], msum[i]);
+              ps[i] = p * step;
+            }
+            if constexpr (FINE && PAIR) {
+              const float hi = __half2float(__float2half_rn(ps[0]));
+              b[e] = movm(pack_h2(hi, ps[0] - hi));
+            } else {
+              const uint32_t hi = pack_h2(ps[0], ps[1]);
+              b[e] = movm(hi);
+              if constexpr (FINE) {
+                const float2 f = unpack_h2(hi);
+                b2[e] = movm(pack_h2(ps[0] - f.x, ps[1] - f.y));
+              }
+            }
+          }
+          if constexpr (!FINE) mma(tot, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, b[0], b[1]);
+#pragma unroll
+          for (int j = 0; j < NC; j += 2) {
+            uint32_t w[4];
+            ldsm4t(sb + n * blk_bytes(D) + (voff ^ (j << 4)), w);
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+              const uint32_t mask = (p & 1) ? 0x00f000f0u : 0x000f000fu;
+              const int sh = p < 2 ? 0 : 8;
+              uint32_t a0 = (w[0] >> sh) & mask, a1 = (w[1] >> sh) & mask, a2 = (w[2] >> sh) & mask, a3 = (w[3] >> sh) & mask;
+              if constexpr (FINE) {
+                a0 = less_middle(a0, p & 1);
+                a1 = less_middle(a1, p & 1);
+                a2 = less_middle(a2, p & 1);
+                a3 = less_middle(a3, p & 1);
+              }
+              mma(acc[2 * j + p], a0, a1, a2, a3, b[0], b[1]);
+              if constexpr (FINE && !PAIR) mma(acc[2 * j + p], a0, a1, a2, a3, b2[0], b2[1]);
             }
           }
         }
-        if constexpr (!FINE) mma(tot, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, b[0], b[1]);
+      }
+      if constexpr (!FINE) {
 #pragma unroll
-        for (int j = 0; j < NC; j += 2) {
-          uint32_t w[4];
-          ldsm4t(sb + n * blk_bytes(D) + (voff ^ (j << 4)), w);
+        for (int m = 0; m < D / 16; ++m)
 #pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            const uint32_t mask = (p & 1) ? 0x00f000f0u : 0x000f000fu;
-            const int sh = p < 2 ? 0 : 8;
-            uint32_t a0 = (w[0] >> sh) & mask, a1 = (w[1] >> sh) & mask, a2 = (w[2] >> sh) & mask, a3 = (w[3] >> sh) & mask;
-            if constexpr (FINE) {
-              a0 = less_middle(a0, p & 1);
-              a1 = less_middle(a1, p & 1);
-              a2 = less_middle(a2, p & 1);
-              a3 = less_middle(a3, p & 1);
-            }
-            mma(acc[2 * j + p], a0, a1, a2, a3, b[0], b[1]);
-            if constexpr (FINE && !PAIR) mma(acc[2 * j + p], a0, a1, a2, a3, b2[0], b2[1]);
-          }
-        }
+          for (int x = 0; x < 4; ++x) acc[m][x] = fmaf(tot[x], (m & 1) ? -0x1p-17f : -0x1p-21f, acc[m][x]);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) tot[x] = 0.0f;
       }
     }
 
@@ -745,7 +761,7 @@ k_decode4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, Att
             for (int p = 0; p < 4; ++p) {
               const float* x = acc[4 * jr + p];
               const float v = FINE && PAIR ? x[2 * half] + x[2 * half + 1] : x[2 * half + i], up = (p & 1) ? 0x1p20f : 0x1p24f;
-              o[p] = (FINE ? v * up : fmaf(v, up, -8.0f * tot[i])) * fw[i];
+              o[p] = v * up * fw[i];
             }
             *(float4*)(merge + (warp * HS + hh) * MC + 64 * jr - r0 + 32 * half + 4 * g) = o4;
           }

@@ -936,3 +936,49 @@ def test_queries_near_the_largest_floats(d):
     ws = torch.empty(sq.sq_kv4_attn_workspace(1, 3, 1, d, n), dtype=torch.uint8, device="cuda")
     sq.sq_kv4_attn_decode(c, torch.tensor([n], dtype=torch.int32).cuda(), x, 2.0 ** -8, out, n, ws, lse=lse)
     check_attention(out, lse, x, [(0, n - 1)], c.pages, table, page, 3, 1, d, F32, scale=2.0 ** -8)
+
+
+# ------------------------------------------------------------------ long contexts
+@pytest.mark.parametrize("d,group,batch,n", [(64, 1, 296, 20000), (128, 4, 296, 16384), (128, 6, 32, 32768), (256, 2, 296, 32768),
+                                             (128, 8, 296, 16000)])
+def test_long_contexts_of_every_output_type(d, group, batch, n):
+    """Near-equal weights over up to 32768 tokens, against float64: outputs are then far smaller than what sums to them, so
+    that what the tensor cores cut of long sums would show. 296 sequences: one block a sequence, the longest sums."""
+    page = 64
+    g = torch.Generator(device="cuda").manual_seed(1)
+    n_pages = -(-n // page)
+    row = torch.arange(n_pages, dtype=torch.int32, device="cuda")
+    one = sq.alloc_kv4(n_pages, 1, d, page, row[None].clone())
+    k = torch.randn(n_pages * page, 1, d, generator=g, device="cuda").to(F16)
+    v = (torch.randn(n_pages * page, 1, d, generator=g, device="cuda") * 0.3).to(F16)
+    start, cu = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.tensor([0, n_pages * page], dtype=torch.int32, device="cuda")
+    sq.sq_kv4_append(one, k, v, start, cu)
+    ko, vo = (torch.empty(n_pages * page, 1, d, device="cuda") for _ in range(2))
+    sq.sq_kv4_read(one, start, cu, ko, vo)                # one rounding of 2^-24 of what is held
+    keys, vals = ko[:n, 0].double(), vo[:n, 0].double()
+    step = ((vals.amax(-1) - vals.amin(-1)) / 14).amax().item()          # of the values, at most (all use 14 codes or more)
+    cache = sq.PagedKV4(one.pages, row.expand(batch, -1).contiguous(), 1, d, page)
+    q = (torch.randn(batch, group, d, generator=g, device="cuda") * 0.1).to(F16)
+    scale, want, size = 1 / math.sqrt(d), [], []
+    for b in range(batch):
+        p = torch.softmax(q[b].double() @ keys.T * scale, -1)
+        want.append(p @ vals)
+        size.append(p @ vals.abs())
+    want, size = torch.stack(want), torch.stack(size)
+    aq = q.double().abs().sum(-1).amax().item()
+    eps = (d + 16) * 2.0 ** -24 * scale * aq * keys.abs().amax().item() * 2 + 2.0 ** -20
+    lens = torch.full((batch,), n, dtype=torch.int32, device="cuda")
+    ws = torch.empty(sq.sq_kv4_attn_workspace(batch, group, 1, d, n), dtype=torch.uint8, device="cuda")
+    for dtype in (BF16, F16, F32):
+        out = torch.empty(batch, group, d, dtype=dtype, device="cuda")
+        sq.sq_kv4_attn_decode(cache, lens, q, 0.0, out, n, ws)
+        err, unit = (out.double() - want).abs(), (want.to(dtype).double() - want)
+        # A product adds sixteen tokens and cuts a unit of 2^-23 of the sum at hand, of its warp. bf16: codes of 7.5 in the
+        # mean over at most sixteen tiles, and 8 times the weights beside them; else codes less 8, at most 4 in the mean,
+        # over all the warp's tokens.
+        cut = 2.0 ** -23 * (16 * (1 if d == 256 else 2) * 7.5 if dtype == BF16 else n / 128 * 4 * 2) * step
+        near = (2.0 ** -11 if dtype == BF16 else 2.0 ** -21) * 4 * step       # weights of one part, and of two
+        assert (err <= torch.finfo(dtype).eps / 2 * want.abs() + near + cut + 2 * eps * size).all()
+        if dtype == BF16:             # beside the output's own rounding, which the cuts do not follow
+            rms = lambda x: x.pow(2).mean().sqrt().item()  # noqa: E731
+            assert rms(err) <= math.hypot(rms(unit), cut) * 1.02
