@@ -373,11 +373,12 @@ class _Described:
         self.__dict__["_made"] = None
 
     def described(self):
-        """(reference to the structure, the structure, what it was made of)."""
+        """(reference to the structure, the structure, its tensors' device, what it was made of); an address names its
+        device too."""
         made, where = self._made, self.where()
-        if made is None or made[2] != where:
+        if made is None or made[3] != where:
             struct = self.struct()
-            made = self.__dict__["_made"] = (ctypes.byref(struct), struct, where)
+            made = self.__dict__["_made"] = (ctypes.byref(struct), struct, self.device(), where)
         return made
 
     def ref(self):
@@ -411,6 +412,9 @@ class PagedKV4(_Described):
     def batch(self) -> int:
         return self.table.shape[0]
 
+    def device(self):
+        return _kv4_device(self.pages.get_device(), self.pages, self.table)
+
     def where(self):
         p, t = self.pages, self.table
         return p.data_ptr(), p.numel(), p.is_contiguous(), t.data_ptr(), t.shape, t.stride(), t.dtype
@@ -436,6 +440,9 @@ class Rope(_Described):
     def check(self):
         if self.table.dtype != torch.float32 or self.table.dim() != 2 or not self.table.is_contiguous():
             raise ValueError("rotation table: a contiguous float32 tensor [n_pos, rot_dim] is wanted")
+
+    def device(self):
+        return self.table.get_device()
 
     def where(self):
         t = self.table
@@ -465,19 +472,31 @@ def alloc_kv4(n_pages, n_kv, d, page_tokens, table, device="cuda") -> PagedKV4:
                     table, n_kv, d, page_tokens)
 
 
-def _kv4_call(stream, *tensors):
-    """The stream of a call as an integer. Its tensors live on the current device: a kernel cannot read the others."""
-    dev = tensors[0].get_device()
+def _kv4_device(dev, *tensors):
+    """dev, the index of the device that every tensor (or None) is on."""
     for t in tensors:
         if t is not None and t.get_device() != dev:
-            raise ValueError(f"every tensor must be on the current device, got some on {t.device} and {tensors[0].device}")
-    if dev < 0 or dev != torch.cuda.current_device():
-        raise ValueError(f"every tensor must be on the current device, got some on {tensors[0].device}")
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+            raise ValueError(f"every tensor must be on the current device, got some on {t.device} and on device {dev}")
+    return dev
+
+
+def _kv4_call(cache, rope, stream, *tensors):
+    """(the cache's reference and structure, the rotation's reference, the call's stream as an integer). Its tensors live on
+    the current device: a kernel cannot read the others."""
+    ref, made, dev, _ = cache.described()
+    turn = None
+    if rope:
+        turn, _, on, _ = rope.described()
+        if on != dev:
+            raise ValueError(f"every tensor must be on the current device, got some on {rope.table.device} and on device {dev}")
+    _kv4_device(dev, *tensors)
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise ValueError(f"every tensor must be on the current device, got some on {cache.pages.device}")
+    return ref, made, turn, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _kv4_ints(name, t, n):
-    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+    if t.numel() != n or t.dim() != 1 or t.dtype != torch.int32 or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous int32 tensor of {n} elements is wanted")
     return t.data_ptr()
 
@@ -525,25 +544,23 @@ def _kv4_bytes(ws):
 
 def sq_kv4_append(cache, k, v, start, cu=None, rope=None, flags=None, stream=None):
     """Append k, v [tokens, n_kv, d] (any strides but the last axis's) at positions start[b] + i (see sq.h)."""
-    st = _kv4_call(stream, cache.pages, cache.table, k, v, start, cu, flags, rope.table if rope else None)
+    ref, made, turn, st = _kv4_call(cache, rope, stream, k, v, start, cu, flags)
     kp, k0, k1 = _kv4_heads("k", k, cache.n_kv, cache.d)
     n = k.shape[0]
     vp, v0, v1 = _kv4_heads("v", v, cache.n_kv, cache.d, n, k.dtype)
-    ref, made, _ = cache.described()
     batch = made.batch
     at = _kv4_ints("start", start, batch)
     cu = None if cu is None else _kv4_ints("cu", cu, batch + 1)
-    _check(lib().sq_kv4_append(ref, kp, vp, DTYPE_CODE[k.dtype], k0, k1, v0, v1, n, cu, at,
-                               rope.ref() if rope else None, _kv4_at(flags), st), "sq_kv4_append")
+    _check(lib().sq_kv4_append(ref, kp, vp, DTYPE_CODE[k.dtype], k0, k1, v0, v1, n, cu, at, turn, _kv4_at(flags), st),
+           "sq_kv4_append")
 
 
 def sq_kv4_read(cache, start, cu, k_out, v_out, flags=None, stream=None):
     """The tokens at positions start[b] + i, as the cache holds them, into k_out, v_out [tokens, n_kv, d]."""
-    st = _kv4_call(stream, cache.pages, cache.table, k_out, v_out, start, cu, flags)
+    ref, made, _, st = _kv4_call(cache, None, stream, k_out, v_out, start, cu, flags)
     kp, k0, k1 = _kv4_heads("k_out", k_out, cache.n_kv, cache.d)
     n = k_out.shape[0]
     vp, v0, v1 = _kv4_heads("v_out", v_out, cache.n_kv, cache.d, n, k_out.dtype)
-    ref, made, _ = cache.described()
     batch = made.batch
     at = _kv4_ints("start", start, batch)
     cu = None if cu is None else _kv4_ints("cu", cu, batch + 1)
@@ -558,22 +575,20 @@ def sq_kv4_attn_workspace(batch, n_q_heads, n_kv_heads, d, max_ctx) -> int:
 def sq_kv4_attn_decode(cache, seq_lens, q, scale, out, max_ctx, ws, rope=None, window=0, lse=None, flags=None,
                        stream=None):
     """Attention of q [batch, n_q_heads, d] over the first seq_lens[b] tokens of every sequence (see sq.h)."""
-    st = _kv4_call(stream, cache.pages, cache.table, q, out, seq_lens, lse, ws, flags, rope.table if rope else None)
-    ref, made, _ = cache.described()
+    ref, made, turn, st = _kv4_call(cache, rope, stream, q, out, seq_lens, lse, ws, flags)
     batch = made.batch
     qp, q0, q1 = _kv4_heads("q", q, None, cache.d, batch)
     op, lp = _kv4_out(out, lse, q)
     wp, wn = _kv4_bytes(ws)
     _check(lib().sq_kv4_attn_decode(ref, _kv4_ints("seq_lens", seq_lens, batch), q.shape[1], max_ctx, qp,
-                                    DTYPE_CODE[q.dtype], q0, q1, rope.ref() if rope else None, scale, window, op,
+                                    DTYPE_CODE[q.dtype], q0, q1, turn, scale, window, op,
                                     DTYPE_CODE[out.dtype], lp, wp, wn, _kv4_at(flags), st), "sq_kv4_attn_decode")
 
 
 def sq_kv4_decode_step(cache, k, v, q, pos, scale, out, max_ctx, ws, rope=None, window=0, lse=None, flags=None,
                        stream=None):
     """Append one token a sequence at pos[b], then attend over pos[b] + 1 tokens (see sq.h)."""
-    st = _kv4_call(stream, cache.pages, cache.table, k, v, q, out, pos, lse, ws, flags, rope.table if rope else None)
-    ref, made, _ = cache.described()
+    ref, made, turn, st = _kv4_call(cache, rope, stream, k, v, q, out, pos, lse, ws, flags)
     batch, n_kv, d, dtype = made.batch, cache.n_kv, cache.d, q.dtype
     qp, q0, q1 = _kv4_heads("q", q, None, d, batch)
     kp, k0, k1 = _kv4_heads("k", k, n_kv, d, batch, dtype)
@@ -581,7 +596,7 @@ def sq_kv4_decode_step(cache, k, v, q, pos, scale, out, max_ctx, ws, rope=None, 
     op, lp = _kv4_out(out, lse, q)
     wp, wn = _kv4_bytes(ws)
     _check(lib().sq_kv4_decode_step(ref, kp, vp, qp, DTYPE_CODE[dtype], k0, k1, v0, v1, q0, q1,
-                                    _kv4_ints("pos", pos, batch), q.shape[1], max_ctx, rope.ref() if rope else None,
+                                    _kv4_ints("pos", pos, batch), q.shape[1], max_ctx, turn,
                                     scale, window, op, DTYPE_CODE[out.dtype], lp, wp, wn, _kv4_at(flags), st),
            "sq_kv4_decode_step")
 
@@ -592,13 +607,12 @@ def sq_kv4_attn_prefill_workspace(batch, n_q_heads, n_kv_heads, d, n_tok) -> int
 
 def sq_kv4_attn_prefill(cache, start, cu, q, scale, out, ws, rope=None, window=0, lse=None, flags=None, stream=None):
     """Causal attention of q [tokens, n_q_heads, d], token cu[b] + i at position start[b] + i (see sq.h)."""
-    st = _kv4_call(stream, cache.pages, cache.table, q, out, start, cu, lse, ws, flags, rope.table if rope else None)
-    ref, made, _ = cache.described()
+    ref, made, turn, st = _kv4_call(cache, rope, stream, q, out, start, cu, lse, ws, flags)
     batch = made.batch
     qp, q0, q1 = _kv4_heads("q", q, None, cache.d)
     op, lp = _kv4_out(out, lse, q)
     wp, wn = _kv4_bytes(ws)
     _check(lib().sq_kv4_attn_prefill(ref, _kv4_ints("cu", cu, batch + 1), _kv4_ints("start", start, batch),
-                                     q.shape[1], q.shape[0], qp, DTYPE_CODE[q.dtype], q0, q1, rope.ref() if rope else None,
+                                     q.shape[1], q.shape[0], qp, DTYPE_CODE[q.dtype], q0, q1, turn,
                                      scale, window, op, DTYPE_CODE[out.dtype], lp, wp, wn, _kv4_at(flags), st),
            "sq_kv4_attn_prefill")
