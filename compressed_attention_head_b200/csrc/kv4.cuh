@@ -5,8 +5,9 @@
 // (max(x) - m) / 15 rounded up to bf16, so every coordinate lies in [m, m + 15 s]
 // and the nearest code is off by at most s / 2; c = (x - m) / s rounded to
 // nearest, ties to even. bf16 rather than fp16 pairs: their range is float's, so
-// no finite input overflows, and what their 8 bits round away is taken up by the
-// codes, which are formed against the rounded pair.
+// that only a vector whose own range is no finite float has no pair (it reads as
+// NaN), and what their 8 bits round away is taken up by the codes, which are formed
+// against the rounded pair.
 //
 // Sixteen tokens of one KV head are one block of 16 d + 128 contiguous bytes (a
 // multiple of 128): key code rows, value code rows, key pairs, value pairs. One

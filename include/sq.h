@@ -525,8 +525,10 @@ sq_status sq_attn_decode_noalloc(const void* calib_k, const void* calib_v, const
  * A vector x (one head of one token) is held as codes c and a pair (s, m), and
  * reads as m + s c: m = min(x) rounded down to bf16, s = (max(x) - m) / 15 (in
  * float) rounded up to bf16 (at least the smallest normal float, 0 when max(x) =
- * m), c = (x - m) / s rounded to nearest, ties to even. A vector with a value that
- * is not finite reads as NaN throughout. Each block of 16 tokens of one head is
+ * m), c = (x - m) / s rounded to nearest, ties to even (x - m in float). A vector
+ * with a value that is not finite, or whose range max(x) - m is not a finite float
+ * (values near the largest of both signs, or a float minimum that rounds down to
+ * -inf), reads as NaN throughout. Each block of 16 tokens of one head is
  * 16 d + 128 bytes: 16 rows of key codes (d / 2 bytes each), 16 of value codes, 16
  * key pairs, 16 value pairs. Byte j of a code row holds coordinate 2j in its low
  * and 2j + 1 in its high half; the 16-byte chunk at place p of token t's row is

@@ -2,8 +2,8 @@
 
 A vector x is held as m + s c: m = min(x) rounded down to bf16, s = (max(x) - m) / 15 rounded up to
 bf16 (float32 difference and quotient, at least the smallest normal float32, 0 when max(x) = m),
-c = (x - m) / s rounded to nearest, ties to even. A vector with a value that is not finite is held as
-NaN (m) with s = 0 and codes 0.
+c = (x - m) / s rounded to nearest, ties to even. A vector with a value that is not finite, or whose
+range max(x) - m is no finite float32, is held as NaN (m) with s = 0 and codes 0.
 
 A block of 16 tokens of one head: 16 rows of key codes (d / 2 bytes), 16 of value codes, 16 key pairs,
 16 value pairs; coordinate 2j in the low half of byte j; the 16-byte chunk at place p of row t is chunk

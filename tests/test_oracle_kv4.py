@@ -105,3 +105,18 @@ def test_attention_against_dense_softmax():
     assert np.allclose(o, e @ v / e.sum()) and math.isclose(lse, math.log(e.sum())) and np.all(b >= np.abs(o))
     o, lse, _ = kv4.attend(q, k[:0], v[:0], 0.125)
     assert not o.any() and lse == -math.inf
+
+
+def test_ranges_that_are_no_finite_float_read_as_nan():
+    """Finite vectors up to the largest float, and those whose range or rounded minimum passes it."""
+    top = float(np.finfo(np.float32).max)
+    bf = 255 * 2.0 ** 120                                            # the largest bf16
+    for lo, hi, held in ((0.0, top, True), (-bf, 0.0, True), (-bf / 2, bf / 2, True), (-top, 0.0, False), (-bf, bf, False),
+                         (-bf, 2.0 ** 127, False), (top, top, True), (-bf, -bf, True)):
+        x = np.full(64, lo, np.float32)
+        x[1::2] = hi
+        c, sb, mb = kv4.quantize(x)
+        y = kv4.values(c, sb, mb)
+        assert np.isnan(y).all() == (not held) and (held or (sb == 0 and mb == 0x7FC0 and not c.any())), (lo, hi)
+        if held:
+            assert np.all(np.abs(y - x) <= 0.5 * float(kv4.bf16_value(sb)) * (1 + 2.0 ** -20) + 2.0 ** -7 * abs(lo) * (lo == hi))
