@@ -154,7 +154,8 @@ template <typename K> cudaError_t allow_smem(K* kernel, int bytes, std::atomic<u
   return e;
 }
 
-// Launch whose prologue may overlap the kernel before it on the stream (it waits for that kernel itself).
+// Launch that may begin before the kernel before it on the stream has ended, and waits for that itself: once that one's
+// blocks have all allowed it or ended. The append allows nothing, so behind it only the launch itself is hidden.
 template <typename... KA, typename... A>
 cudaError_t launch_overlapped(void (*kernel)(KA...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, A... args) {
   cudaLaunchAttribute at[1];

@@ -203,7 +203,7 @@ __device__ __forceinline__ void make_pair(float mn, float mx, float* s, float* m
   uint32_t sb = 0;
   if (r > 0.0f) {
     // r / 15 as a division rounds it: Markstein's correction of the product with the rounded 1 / 15, which is exact
-    // for this divisor (all 2^23 significands at thirteen exponents compared on the host; below FLT_MIN it is not used)
+    // for this divisor (every significand is compared in tests/test_oracle_kv4.py; below FLT_MIN it is not used)
     const float y = 1.0f / 15.0f, q = __fmul_rn(r, y);
     sb = bf16_up(fmaxf(__fmaf_rn(__fmaf_rn(-15.0f, q, r), y, q), FLT_MIN));
   }

@@ -328,7 +328,7 @@ __device__ __forceinline__ void make_units(const Pool& c, const RopeArgs& r, con
 }
 
 // Block 0 lists the units; the others turn, scale and lay out the queries, D / 16
-// threads a row (eight coordinates of each half, as the append takes them) and four
+// threads a row (eight coordinates of each half, as the append takes them) and two
 // heads of a token at once, under the same angles: fp16, rows of a power of two
 // each, 64 coordinates a 16 KB slab of swizzled lines, eight coordinates in the
 // codes' order. Once a call, so that the pieces of a cut unit do not repeat it and a

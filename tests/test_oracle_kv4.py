@@ -120,3 +120,33 @@ def test_ranges_that_are_no_finite_float_read_as_nan():
         assert np.isnan(y).all() == (not held) and (held or (sb == 0 and mb == 0x7FC0 and not c.any())), (lo, hi)
         if held:
             assert np.all(np.abs(y - x) <= 0.5 * float(kv4.bf16_value(sb)) * (1 + 2.0 ** -20) + 2.0 ** -7 * abs(lo) * (lo == hi))
+
+
+def test_corrected_product_is_the_rounded_quotient_by_fifteen():
+    """r y, y the rounded 1 / 15, and one correction q + (r - 15 q) y, each rounded to 24 bits, give r / 15 rounded: for every
+    significand, in whole numbers (exponents only shift them while r / 15 is normal)."""
+    r = np.arange(1 << 23, 1 << 24, dtype=np.int64)
+    y = 8947849                                                      # of 2^-27: 1 / 15 rounded to 24 bits
+    assert abs(y * 15 - (1 << 27)) * 2 < 15 and 1 << 23 <= y < 1 << 24
+    assert np.float32(1) / np.float32(15) == np.float32(y * 2.0 ** -27)
+
+    def nearest(x, by):                                              # x / 2^by, ties to even
+        q, rest = x >> by, x & ((np.int64(1) << by) - 1)
+        half = np.int64(1) << (by - 1)
+        return q + ((rest > half) | ((rest == half) & (q & 1 == 1)))
+
+    p = r * y                                                        # of 2^-27
+    by = np.where(p < 1 << 47, 23, 24)
+    q = nearest(p, by) << by                                         # of 2^-27, 24 bits
+    assert np.all(q >> by <= 1 << 24)                                # a float
+    rest = (r << 27) - 15 * q                                        # of 2^-27: a float, its low bits are 0
+    bits = rest >> 23
+    assert np.all(bits << 23 == rest) and np.abs(bits).max() < 1 << 24
+    s = (q << 4) + bits * y                                          # of 2^-31: (q 2^-27) + (bits 2^-4)(y 2^-27)
+    by = np.where(s < 1 << 51, 27, 28)
+    got = nearest(s, by) << by                                       # of 2^-31
+    # r / 15 to 24 bits: no tie can occur, as 15 is odd and r has 24 bits
+    unit = np.where(r < 15 << 20, 4, 3)                              # r 2^unit / 15 in [2^23, 2^24)
+    z = r << unit
+    want = (z // 15 + (z % 15 > 7)) << (31 - unit)                   # of 2^-31
+    assert np.array_equal(got, want)
