@@ -372,6 +372,9 @@ class _Described:
         self.__dict__[name] = value
         self.__dict__["_made"] = None
 
+    def __getstate__(self):                       # what is kept names addresses: a copy makes its own
+        return {**self.__dict__, "_made": None}
+
     def described(self):
         """(reference to the structure, the structure, its tensors' device, what it was made of); an address names its
         device too."""

@@ -1,6 +1,8 @@
 """Refusals of the paged 4-bit cache's entry points: they need no GPU."""
 
+import copy
 import ctypes
+import pickle
 
 import pytest
 import torch
@@ -197,3 +199,17 @@ def test_strides_of_axes_of_one_element_are_not_asked_for():
     odd = torch.zeros(4096, dtype=torch.float16).as_strided((3, 1, 128), (256, 1, 1))
     assert sq._kv4_heads("k", odd, 1, 128)[1:] == (256, 0)
     assert sq._kv4_heads("k", odd[:0], 1, 128)[1:] == (0, 0)
+
+
+def test_copies_of_a_cache_describe_their_own_tensors():
+    """After a call has kept its structures too: shallow and deep copies, and pickles."""
+    c = sq.PagedKV4(torch.zeros(8, 2, 1, 16 * 128 + 128, dtype=torch.uint8), torch.zeros(2, 4, dtype=torch.int32), 2, 128, 16)
+    r = sq.Rope(torch.ones(16, 16), True)
+    c.ref(), r.ref()
+    for made in (copy.deepcopy((c, r)), pickle.loads(pickle.dumps((c, r)))):
+        d, s = made
+        assert d.described()[1].pages == d.pages.data_ptr() != c.pages.data_ptr() and d.n_kv == 2
+        assert s.described()[1].table == s.table.data_ptr() != r.table.data_ptr() and s.interleaved
+    d = copy.copy(c)
+    d.table = d.table[:1]
+    assert d.described()[1].batch == 1 and c.described()[1].batch == 2
