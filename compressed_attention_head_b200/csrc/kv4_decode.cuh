@@ -331,7 +331,8 @@ k_decode4(Pool c, RopeArgs r, const T* __restrict__ q, TO* __restrict__ out, Att
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int per_row = c.n_kv * nsub;
   const Plan plan = make_plan<C::TT>(c, r, a, per_row, red);
-  asm volatile("griddepcontrol.wait;" ::: "memory");      // a decode step's append must be in the pool
+  asm volatile("griddepcontrol.wait;" ::: "memory");      // a decode step's append must be in the pool,
+  asm volatile("fence.proxy.async.global;" ::: "memory"); // and its plain stores before the bulk copies that read them
   // rows with nothing to attend
   for (int b = blockIdx.x; b < c.batch; b += gridDim.x) {
     const Span s = span_of(c, r, a, b, tid == 0 ? a.flags : nullptr);
