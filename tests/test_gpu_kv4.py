@@ -982,3 +982,31 @@ def test_long_contexts_of_every_output_type(d, group, batch, n):
         if dtype == BF16:             # beside the output's own rounding, which the cuts do not follow
             rms = lambda x: x.pow(2).mean().sqrt().item()  # noqa: E731
             assert rms(err) <= math.hypot(rms(unit), cut) * 1.02
+
+
+@pytest.mark.parametrize("d,group,dtype", [(64, 4, F16), (128, 3, F16), (128, 6, F16), (256, 3, F16), (256, 8, F16), (128, 3, BF16)])
+def test_log_sum_exps_of_short_spans_are_floats(d, group, dtype):
+    """Decode over one to four tokens, where log-sum-exps are of the size of one score: within 2^-20 of them in the root mean
+    square, as float sums of d products are with room (theirs: 2^-24 to 2^-23)."""
+    page, batch, n = 16, 96, 48
+    g = torch.Generator(device="cuda").manual_seed(d)
+    table = torch.arange(batch * 3, dtype=torch.int32, device="cuda").view(batch, 3)
+    cache = sq.alloc_kv4(batch * 3, 1, d, page, table)
+    large = torch.ones(d, device="cuda")
+    large[:: 32] = 6.0
+    k = (torch.randn(batch * n, 1, d, generator=g, device="cuda") * large).to(dtype)
+    start, cu = torch.zeros(batch, dtype=torch.int32, device="cuda"), torch.arange(0, batch * n + 1, n, dtype=torch.int32, device="cuda")
+    sq.sq_kv4_append(cache, k, k, start, cu)
+    keys, vals = (torch.empty(batch * n, 1, d, device="cuda") for _ in range(2))
+    sq.sq_kv4_read(cache, start, cu, keys, vals)
+    keys = keys.view(batch, n, d).double()
+    q = (torch.randn(batch, group, d, generator=g, device="cuda") * math.sqrt(32 / 67)).to(dtype)
+    ws = torch.empty(sq.sq_kv4_attn_workspace(batch, group, 1, d, n), dtype=torch.uint8, device="cuda")
+    for window in (1, 2, 4):
+        out, lse = torch.empty(batch, group, d, device="cuda"), torch.empty(batch, group, device="cuda")
+        lens = torch.arange(batch, dtype=torch.int32, device="cuda") % (n - 4) + 4
+        sq.sq_kv4_attn_decode(cache, lens, q, 0.0, out, n, ws, window=window, lse=lse)
+        want = torch.stack([torch.logsumexp(q[b].double() @ keys[b, int(lens[b]) - window:int(lens[b])].T / math.sqrt(d), -1)
+                            for b in range(batch)])
+        rms = lambda x: x.pow(2).mean().sqrt().item()  # noqa: E731
+        assert rms(lse.double() - want) <= 2.0 ** -20 * rms(want), window
