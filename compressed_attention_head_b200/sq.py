@@ -517,6 +517,17 @@ def _kv4_heads(name, t, heads, d, rows=None, dtype=None):
                      f"of stride 1 along the last axis{'' if dtype is None else f' and type {dtype}'} is wanted")
 
 
+def _kv4_apart(name, n, h, d, s0, s1):
+    """Refuses an output [n, h, d] whose rows share memory: each stride steps over all that the smaller ones reach."""
+    if (h == 1 or s1 >= d) and (n < 2 or s0 >= (h - 1) * s1 + d):
+        return
+    reach = d
+    for stride, count in sorted(x for x in ((s0, n), (s1, h)) if x[1] > 1):
+        if stride < reach:
+            raise ValueError(f"{name}: an output whose rows share no memory is wanted")
+        reach += (count - 1) * stride
+
+
 def _kv4_out(out, lse, q):
     """Addresses of the outputs."""
     shape = q.shape
@@ -564,6 +575,8 @@ def sq_kv4_read(cache, start, cu, k_out, v_out, flags=None, stream=None):
     kp, k0, k1 = _kv4_heads("k_out", k_out, cache.n_kv, cache.d)
     n = k_out.shape[0]
     vp, v0, v1 = _kv4_heads("v_out", v_out, cache.n_kv, cache.d, n, k_out.dtype)
+    _kv4_apart("k_out", n, cache.n_kv, cache.d, k0, k1)
+    _kv4_apart("v_out", n, cache.n_kv, cache.d, v0, v1)
     batch = made.batch
     at = _kv4_ints("start", start, batch)
     cu = None if cu is None else _kv4_ints("cu", cu, batch + 1)

@@ -213,3 +213,25 @@ def test_copies_of_a_cache_describe_their_own_tensors():
     d = copy.copy(c)
     d.table = d.table[:1]
     assert d.described()[1].batch == 1 and c.described()[1].batch == 2
+
+
+def test_outputs_whose_rows_share_memory_are_refused():
+    """Read back into an expanded or overlapping view would leave rows to whichever block wrote last."""
+    x = torch.zeros(1 << 16, dtype=torch.float16)
+    apart = lambda t: sq._kv4_apart("k_out", t.shape[0], t.shape[1], t.shape[2], *sq._kv4_heads("k_out", t, None, t.shape[2])[1:])  # noqa: E731
+    good = [x[:6 * 2 * 64].view(6, 2, 64), x[:6 * 2 * 64].view(2, 6, 64).transpose(0, 1), x[:64 * 200].view(10, 20, 64)[:, 3:5],
+            x.as_strided((6, 2, 64), (3 * 64, 64, 1)), x.as_strided((1, 2, 64), (1, 64, 1)), x.as_strided((6, 1, 64), (64, 0, 1)),
+            x.as_strided((1, 1, 64), (0, 0, 1)), x.as_strided((0, 2, 64), (0, 64, 1)), x.as_strided((2, 6, 64), (64, 128, 1))]
+    bad = [x[:128].view(1, 2, 64).expand(6, -1, -1), x[:384].view(6, 1, 64).expand(-1, 2, -1), x[:64].view(1, 1, 64).expand(6, 2, -1),
+           x.as_strided((6, 2, 64), (64, 64, 1)), x.as_strided((6, 2, 64), (128, 32, 1)), x.as_strided((6, 2, 64), (96, 64, 1)),
+           x.as_strided((6, 2, 64), (64, 128, 1)), x.as_strided((1, 2, 64), (0, 56, 1)), x.as_strided((3, 1, 64), (56, 0, 1))]
+    for t in good:
+        apart(t)
+    for t in bad:
+        with pytest.raises(ValueError, match="share no memory"):
+            apart(t)
+    rows = lambda t: [set(range(i * t.stride(0) + h * t.stride(1), i * t.stride(0) + h * t.stride(1) + t.shape[2]))  # noqa: E731
+                      for i in range(t.shape[0]) for h in range(t.shape[1])]
+    for t in good + bad:
+        r = rows(t)
+        assert (len(set().union(*r)) == sum(map(len, r))) == any(t is g for g in good)
