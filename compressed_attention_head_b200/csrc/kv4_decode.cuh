@@ -42,11 +42,13 @@
 // before has cleared the counters for that).
 //
 // Measured (one B200): 64 x 4096 x 8 KV heads at head_dim 256, two query heads each:
-// 128 us, 4.3 TB/s; 16 x 32768 x 2 at 128, six heads each: 49 us, 2.9 TB/s (45 us with one
-// part and the 8 off the sum, but an output half again as far from the exact one). 16 warps an
-// SM (128 registers) use 56 % of the instruction slots and 56 % of the ALU that takes the
-// codes apart, in turns: neither more warps of fewer registers nor two chains of products
-// a tile were faster.
+// 125 to 131 us on different GPUs, 4.2 to 4.4 TB/s; 16 x 32768 x 2 at 128, six heads
+// each: 50 us, 2.8 TB/s (4 us less with one part and the 8 off the sum, but an output
+// half again as far from the exact one; what is left is 4 % over it, as the second part
+// is added to the sum of the first and cut with it). 16 warps an SM (128 registers) use
+// 56 % of the instruction slots and 56 % of the ALU that takes the codes apart, in
+// turns: neither more warps of fewer registers nor two chains of products a tile were
+// faster.
 #pragma once
 
 #include "kv4_append.cuh"
